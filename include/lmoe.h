@@ -134,6 +134,70 @@ LMOE_API lmoe_status lmoe_config_from_base(int32_t d, int32_t m, int32_t N, int3
  * OOM / CUDA on allocation or launch failure (nothing is leaked). */
 LMOE_API lmoe_status lmoe_create(const lmoe_config *cfg, const lmoe_weights *w, void *stream, lmoe_handle **out);
 
+/* Microscaled 4-bit values (OCP MXFP4).  A tensor of rows x cols values, cols a
+ * multiple of 32, is
+ *  codes   [rows, cols / 2]   two 4-bit codes per byte, the even column in the
+ *                             low half: a sign bit over a magnitude out of
+ *                             0, 1/2, 1, 3/2, 2, 3, 4, 6
+ *  scales  [rows, cols / 32]  one byte e per block of 32 values along a row:
+ *                             the scale 2^(e - 127); 255 makes the block NaN
+ * both dense and row-major. */
+
+/* Quantise x [rows, cols] (device, dtype, row stride ld elements) into codes
+ * and scales (device).  A block's scale is 2^(floor(log2 m) - 2) with m its
+ * largest magnitude (2^-127 at least), so that m lands in [4, 8); values round
+ * to the nearest magnitude, ties to the even code, those past 6 to 6, signs
+ * kept.  A block that holds an infinity or a NaN gets scale 255 and zero codes.
+ * x and its rows must be 16-byte aligned, codes 4-byte aligned.  rows or cols 0
+ * is a no-op.
+ * INVALID_ARG: NULL pointer, negative size, unknown dtype, ld < cols.
+ * UNSUPPORTED: cols not a multiple of 32, alignment, more than 2^46 values. */
+LMOE_API lmoe_status lmoe_mx4_quantize(const void *x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
+                                       void *codes, void *scales, void *stream);
+
+/* The values of a 4-bit tensor into y [rows, cols] (dtype, row stride ld
+ * elements): exact in either type (magnitudes past the type's largest become
+ * infinite).  Alignment and errors as lmoe_mx4_quantize. */
+LMOE_API lmoe_status lmoe_mx4_dequantize(const void *codes, const void *scales, int64_t rows, int64_t cols,
+                                         int32_t dtype, void *y, int64_t ld, void *stream);
+
+/* Routed experts in 4 bits (device pointers, read only during the create call):
+ * G, U codes of [E, f, l], D codes of [E, l, f], with their scales; quantised
+ * along the last dimension. */
+typedef struct {
+    const void *G, *G_scales, *U, *U_scales, *D, *D_scales;
+} lmoe_mx4_experts;
+
+/* lmoe_create with the routed experts in 4 bits: w->G, w->U and w->D are not
+ * read (they may be NULL), and the handle holds only the 4-bit experts.  All
+ * other weights, and the tokens, are bf16 on the tensor-core path.
+ * Errors as lmoe_create; also UNSUPPORTED for another dtype or gemm = 1, or
+ * codes that are not 16-byte aligned. */
+LMOE_API lmoe_status lmoe_create_mx4(const lmoe_config *cfg, const lmoe_weights *w, const lmoe_mx4_experts *experts,
+                                     void *stream, lmoe_handle **out);
+
+/* Most tokens of one lmoe_forward_few call. */
+#define LMOE_FEW_MAX_T 8
+
+/* Device workspace bytes that lmoe_forward_few needs for T tokens (0 for T = 0).
+ * UNSUPPORTED for T > LMOE_FEW_MAX_T. */
+LMOE_API lmoe_status lmoe_few_workspace_size(const lmoe_handle *h, int64_t T, size_t *bytes);
+
+/* The layer forward for 1 to LMOE_FEW_MAX_T tokens as one kernel (after one
+ * memset of its counters): arguments, outputs and conditions as lmoe_forward,
+ * for every kind of handle.  Against lmoe_forward it reads each weight once in
+ * a single stream without gaps between the stages, takes the selection from
+ * scores in 64 bits, and keeps z, the experts' hidden values and RMSNorm(u) in
+ * more than the token type's precision, so its results differ from
+ * lmoe_forward's by roundings.  Results do not depend on timing: two calls on
+ * the same inputs are bit-identical.  Workspace regions and stage events are
+ * not available; lmoe_check_device on this workspace reports its waits.
+ * UNSUPPORTED: T > LMOE_FEW_MAX_T, x not 16-byte aligned, or no sm_100 device.
+ * INVALID_ARG also when the handle's device is not current. */
+LMOE_API lmoe_status lmoe_forward_few(lmoe_handle *h, const void *x, int64_t T, void *output,
+                                      int32_t *selected_experts, void *mixture_weights,
+                                      void *latent_routed_aggregate, void *workspace, size_t ws_bytes, void *stream);
+
 /* Device workspace bytes that lmoe_forward needs for T tokens (0 for T = 0). */
 LMOE_API lmoe_status lmoe_workspace_size(const lmoe_handle *h, int64_t T, size_t *bytes);
 
@@ -250,12 +314,15 @@ LMOE_API lmoe_status lmoe_set_stage_events(lmoe_handle *h, void *const *events, 
  *      failure in the forward's status word, drains and returns, and
  *      lmoe_check_device then reports LMOE_ERR_DEVICE_TIMEOUT.  Nothing faults
  *      or hangs; the context stays usable.  (arg ignored.)
+ *  LMOE_INJECT_STALL_NEXT_FEW  a wait of the next lmoe_forward_few call runs out
+ *      in the same way (arg ignored).
  *  LMOE_INJECT_FAIL_ALLOC  the arg-th device allocation (1-based) of the next
  *      lmoe_create fails as if cudaMalloc had: lmoe_create returns LMOE_ERR_OOM
  *      and frees what it had allocated.
  * INVALID_ARG for an unknown `what` or arg < 1 with LMOE_INJECT_FAIL_ALLOC. */
 #define LMOE_INJECT_STALL_NEXT_GEMM 1
 #define LMOE_INJECT_FAIL_ALLOC 2
+#define LMOE_INJECT_STALL_NEXT_FEW 3
 LMOE_API lmoe_status lmoe_debug_inject(int32_t what, int32_t arg);
 
 /* Number of kernels one lmoe_forward of T tokens launches (its two memsets,

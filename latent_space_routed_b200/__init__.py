@@ -13,7 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Dict, Optional
+from typing import Dict, NamedTuple, Optional
 
 import torch
 
@@ -33,7 +33,8 @@ REGION = {"scores": 0, "p32": 1, "counts": 2, "offsets": 3, "slot_of": 4, "perm_
           "Y": 8, "HS": 9, "status": 10, "cutoff": 11, "Zp": 12}
 
 EXPORTS = ("lmoe_config_from_base", "lmoe_create", "lmoe_workspace_size", "lmoe_forward", "lmoe_host_workspace_size",
-           "lmoe_forward_host", "lmoe_forward_noalloc", "lmoe_debug_inject", "lmoe_set_bias", "lmoe_qb_histogram", "lmoe_qb_bias_update", "lmoe_set_stage_events", "lmoe_launch_count", "lmoe_workspace_region", "lmoe_check_device", "lmoe_check_device_host",
+           "lmoe_forward_host", "lmoe_forward_noalloc", "lmoe_create_mx4", "lmoe_few_workspace_size", "lmoe_forward_few",
+           "lmoe_mx4_quantize", "lmoe_mx4_dequantize", "lmoe_debug_inject", "lmoe_set_bias", "lmoe_qb_histogram", "lmoe_qb_bias_update", "lmoe_set_stage_events", "lmoe_launch_count", "lmoe_workspace_region", "lmoe_check_device", "lmoe_check_device_host",
            "lmoe_last_error", "lmoe_destroy")
 
 
@@ -51,6 +52,10 @@ class lmoe_config(ctypes.Structure):
                 ("standard", ctypes.c_int32)]
 
 
+class lmoe_mx4_experts(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("G", "G_scales", "U", "U_scales", "D", "D_scales")]
+
+
 class lmoe_weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("W_r", "b", "W_down", "W_up", "G", "U", "D", "Gs", "Us", "Ds")]
 
@@ -63,6 +68,12 @@ def _load() -> ctypes.CDLL:
     sig = {
         "lmoe_config_from_base": (I32, [I32, I32, I32, I32, I32, I32, ctypes.c_char_p, ctypes.POINTER(lmoe_config)]),
         "lmoe_create": (I32, [ctypes.POINTER(lmoe_config), ctypes.POINTER(lmoe_weights), P, ctypes.POINTER(P)]),
+        "lmoe_create_mx4": (I32, [ctypes.POINTER(lmoe_config), ctypes.POINTER(lmoe_weights),
+                                  ctypes.POINTER(lmoe_mx4_experts), P, ctypes.POINTER(P)]),
+        "lmoe_few_workspace_size": (I32, [P, I64, ctypes.POINTER(SZ)]),
+        "lmoe_forward_few": (I32, [P, P, I64, P, P, P, P, P, SZ, P]),
+        "lmoe_mx4_quantize": (I32, [P, I32, I64, I64, I64, P, P, P]),
+        "lmoe_mx4_dequantize": (I32, [P, P, I64, I64, I32, P, I64, P]),
         "lmoe_workspace_size": (I32, [P, I64, ctypes.POINTER(SZ)]),
         "lmoe_forward": (I32, [P, P, I64, P, P, P, P, P, SZ, P]),
         "lmoe_host_workspace_size": (I32, [P, I64, ctypes.POINTER(SZ)]),
@@ -132,6 +143,35 @@ def lmoe_create(cfg: lmoe_config, weights: Dict[str, torch.Tensor], stream=None)
     return h.value
 
 
+def lmoe_create_mx4(cfg: lmoe_config, weights: Dict[str, torch.Tensor], experts: Dict[str, "Mx4"], stream=None) -> int:
+    w = lmoe_weights(*[_ptr(weights.get(n)) if n not in ("G", "U", "D") else None
+                       for n in ("W_r", "b", "W_down", "W_up", "G", "U", "D", "Gs", "Us", "Ds")])
+    x4 = lmoe_mx4_experts(*[_ptr(t) for n in ("G", "U", "D") for t in (experts[n].codes, experts[n].scales)])
+    h = ctypes.c_void_p()
+    _check(_lib.lmoe_create_mx4(ctypes.byref(cfg), ctypes.byref(w), ctypes.byref(x4), _stream(stream), ctypes.byref(h)))
+    return h.value
+
+
+def lmoe_few_workspace_size(h: int, T: int) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.lmoe_few_workspace_size(h, T, ctypes.byref(n)))
+    return n.value
+
+
+def lmoe_forward_few(h, x, T, output, selected_experts, mixture_weights, latent_routed_aggregate, workspace, ws_bytes,
+                     stream=None):
+    _check(_lib.lmoe_forward_few(h, _ptr(x), T, _ptr(output), _ptr(selected_experts), _ptr(mixture_weights),
+                                 _ptr(latent_routed_aggregate), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def lmoe_mx4_quantize(x, dtype, rows, cols, ld, codes, scales, stream=None):
+    _check(_lib.lmoe_mx4_quantize(_ptr(x), dtype, rows, cols, ld, _ptr(codes), _ptr(scales), _stream(stream)))
+
+
+def lmoe_mx4_dequantize(codes, scales, rows, cols, dtype, y, ld, stream=None):
+    _check(_lib.lmoe_mx4_dequantize(_ptr(codes), _ptr(scales), rows, cols, dtype, _ptr(y), ld, _stream(stream)))
+
+
 def lmoe_destroy(h: int):
     _lib.lmoe_destroy(h)
 
@@ -162,7 +202,8 @@ def lmoe_forward_host(h, x_host, T, output_host, selected_experts_host, mixture_
 
 
 LMOE_NOALLOC_WORKSPACE_BYTES = 64 << 20
-LMOE_INJECT_STALL_NEXT_GEMM, LMOE_INJECT_FAIL_ALLOC = 1, 2
+LMOE_INJECT_STALL_NEXT_GEMM, LMOE_INJECT_FAIL_ALLOC, LMOE_INJECT_STALL_NEXT_FEW = 1, 2, 3
+LMOE_FEW_MAX_T = 8
 
 
 def lmoe_debug_inject(what, arg=0):
@@ -225,12 +266,85 @@ def lmoe_check_device_host(h, T, workspace, stream=None):
 _TORCH_DT = {LMOE_F32: torch.float32, LMOE_BF16: torch.bfloat16}
 
 
+_LM_DT = {torch.float32: LMOE_F32, torch.bfloat16: LMOE_BF16}
+
+
+class Mx4(NamedTuple):
+    """A microscaled 4-bit tensor (see include/lmoe.h): codes [..., cols / 2] and scales [..., cols / 32], uint8."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    @property
+    def shape(self):
+        return (*self.codes.shape[:-1], 2 * self.codes.shape[-1])
+
+    def check(self, what: str) -> "Mx4":
+        c, s = self.codes, self.scales
+        if c.dtype != torch.uint8 or s.dtype != torch.uint8:
+            raise TypeError(f"{what}: codes and scales must be uint8, got {c.dtype} and {s.dtype}")
+        if c.dim() < 1 or c.shape[-1] % 16 or tuple(s.shape) != (*c.shape[:-1], c.shape[-1] // 16):
+            raise ValueError(f"{what}: codes [..., cols / 2] and scales [..., cols / 32] do not match: "
+                             f"{tuple(c.shape)}, {tuple(s.shape)}")
+        if not c.is_cuda or c.device != s.device:
+            raise ValueError(f"{what}: codes and scales must be on one CUDA device")
+        if not c.is_contiguous() or not s.is_contiguous():
+            raise ValueError(f"{what}: codes and scales must be contiguous")
+        return self
+
+
+def _on(device, stream):
+    """The stream handle to use for tensors of `device`."""
+    return torch.cuda.current_stream(device) if stream is None else stream
+
+
+def mx4_quantize(x: torch.Tensor, stream=None) -> Mx4:
+    """x [..., cols] (fp32 or bf16 on a CUDA device, cols a multiple of 32) in 4 bits."""
+    if x.dtype not in _LM_DT:
+        raise TypeError(f"fp32 or bf16 expected, got {x.dtype}")
+    if not x.is_cuda:
+        raise ValueError("x must be on a CUDA device")
+    if x.dim() < 1:
+        raise ValueError("x needs a last dimension")
+    cols, lead = x.shape[-1], x.shape[:-1]
+    if cols % 32:
+        raise ValueError(f"the last dimension {cols} is not a multiple of 32")
+    per16 = 16 // x.element_size()
+    # a matrix whose rows are whole and 16-byte aligned is read as it lies; anything else is laid out first
+    x2 = x if x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= cols and x.stride(0) % per16 == 0 \
+        else x.reshape(-1, cols).contiguous() if cols else x.reshape(x.numel() or 0, 0)
+    if x2.data_ptr() % 16:
+        x2 = x2.clone(memory_format=torch.contiguous_format)
+    with torch.cuda.device(x.device):
+        q = Mx4(torch.empty((*lead, cols // 2), dtype=torch.uint8, device=x.device),
+                torch.empty((*lead, cols // 32), dtype=torch.uint8, device=x.device))
+        if x.numel():
+            lmoe_mx4_quantize(x2, _LM_DT[x.dtype], x2.shape[0], cols, x2.stride(0) if x2.shape[0] > 1 else cols,
+                              q.codes, q.scales, _on(x.device, stream))
+    return q
+
+
+def mx4_dequantize(q: Mx4, dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """The values of a 4-bit tensor, exact in either type."""
+    if dtype not in _LM_DT:
+        raise TypeError(f"fp32 or bf16 expected, got {dtype}")
+    q.check("q")
+    cols = 2 * q.codes.shape[-1]
+    with torch.cuda.device(q.codes.device):
+        y = torch.empty(q.shape, dtype=dtype, device=q.codes.device)
+        if y.numel():
+            lmoe_mx4_dequantize(q.codes, q.scales, y.numel() // cols, cols, _LM_DT[dtype], y, cols,
+                                _on(y.device, stream))
+    return y
+
+
 class LatentMoE:
     """A LatentMoE layer on the current CUDA device.
 
     ``weights`` holds W_r [E, d] fp32, b [E] fp32, W_down [l, d], W_up [d, l],
     G, U [E, f, l], D [E, l, f], Gs, Us [2, f_s, d], Ds [2, d, f_s] (CUDA
     tensors; copied and repacked at construction, so they may be freed after).
+    G, U and D may all be ``Mx4`` tensors of the same shapes: the routed experts
+    are then held and computed in 4 bits.
     ``layer(x)`` with x [..., d] returns the dict of the "Stable LatentMoE"
     contract: output [..., d], selected_experts [..., k] int32,
     mixture_weights [..., k], latent_routed_aggregate [..., l].
@@ -244,11 +358,24 @@ class LatentMoE:
         for n in ("W_r", "b", "W_down", "W_up", "G", "U", "D", "Gs", "Us", "Ds"):
             if cfg.standard and n in ("W_down", "W_up"):
                 continue                 # the standard-MoE form has no projections
+            if isinstance(weights[n], Mx4):
+                continue
             want = torch.float32 if n in ("W_r", "b") else self.dtype
             w[n] = weights[n].to(device=dev, dtype=want).contiguous()
-        self.handle = lmoe_create(cfg, w, stream)
+        self.mx4 = any(isinstance(weights[n], Mx4) for n in ("G", "U", "D"))
+        if self.mx4:
+            shapes = {"G": (cfg.E, cfg.f, cfg.l), "U": (cfg.E, cfg.f, cfg.l), "D": (cfg.E, cfg.l, cfg.f)}
+            for n, shape in shapes.items():
+                if not isinstance(weights[n], Mx4):
+                    raise TypeError("G, U and D must all be Mx4 tensors, or none of them")
+                if weights[n].check(n).shape != shape:
+                    raise ValueError(f"{n}: shape {weights[n].shape} != {shape}")
+            self.handle = lmoe_create_mx4(cfg, w, {n: weights[n] for n in shapes}, stream)
+        else:
+            self.handle = lmoe_create(cfg, w, stream)
         self.device = dev
         self._ws = None
+        self._few_ws = {}
 
     def close(self):
         if getattr(self, "handle", None):
@@ -283,17 +410,44 @@ class LatentMoE:
                      out["latent_routed_aggregate"], ws, ws.numel(), stream)
         return out
 
-    def __call__(self, x: torch.Tensor, stream=None) -> Dict[str, torch.Tensor]:
+    def few_workspace(self, T: int) -> torch.Tensor:
+        """The layer's own workspace of forward_few_into for T tokens."""
+        ws = self._few_ws.get(T)
+        if ws is None:
+            ws = self._few_ws[T] = torch.empty(max(lmoe_few_workspace_size(self.handle, T), 256), dtype=torch.uint8,
+                                               device=self.device)
+        return ws
+
+    def forward_few_into(self, x: torch.Tensor, out: Dict[str, torch.Tensor], workspace: Optional[torch.Tensor] = None,
+                         stream=None):
+        """The layer for x [T, d] of 1 to 8 tokens in one kernel, into the four output tensors.
+
+        Calls that may overlap on the GPU, and graphs that may replay beside other
+        calls, need a ``workspace`` of their own (``lmoe_few_workspace_size`` bytes)."""
+        T = x.shape[0]
+        ws = self.few_workspace(T) if workspace is None else workspace
+        lmoe_forward_few(self.handle, x, T, out["output"], out["selected_experts"], out["mixture_weights"],
+                         out["latent_routed_aggregate"], ws, ws.numel(), stream)
+        return out
+
+    def forward_few(self, x: torch.Tensor, stream=None) -> Dict[str, torch.Tensor]:
+        """``layer(x)`` for at most 8 tokens, in one kernel."""
+        return self._call(x, self.forward_few_into, stream)
+
+    def _call(self, x: torch.Tensor, forward_into, stream) -> Dict[str, torch.Tensor]:
         c = self.cfg
         if x.shape[-1] != c.d:
             raise ValueError(f"last dim {x.shape[-1]} != d={c.d}")
         lead = x.shape[:-1]
         x2 = x.reshape(-1, c.d).to(device=self.device, dtype=self.dtype).contiguous()
-        out = self.forward_into(x2, self.empty_outputs(x2.shape[0]), stream)
+        out = forward_into(x2, self.empty_outputs(x2.shape[0]), stream=stream)
         return {"output": out["output"].reshape(*lead, c.d),
                 "selected_experts": out["selected_experts"].reshape(*lead, c.k),
                 "mixture_weights": out["mixture_weights"].reshape(*lead, c.k),
                 "latent_routed_aggregate": out["latent_routed_aggregate"].reshape(*lead, c.l)}
+
+    def __call__(self, x: torch.Tensor, stream=None) -> Dict[str, torch.Tensor]:
+        return self._call(x, self.forward_into, stream)
 
     def forward_host(self, x_host: torch.Tensor, out_host: Dict[str, torch.Tensor], stream=None):
         """Host buffers in and out (pinned for async copies); copies are inside the library call."""

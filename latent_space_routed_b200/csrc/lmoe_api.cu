@@ -36,12 +36,15 @@
 
 #include "lmoe_internal.cuh"
 #include "gemm_tc.cuh"
+#include "few.cuh"
+#include "mx4.cuh"
 
 using namespace lmoe;
 
 namespace {
 
 thread_local std::string g_err;
+std::atomic<int> g_stall_few{0};       // test hook: a wait of the next few-token layer runs out
 std::atomic<int> g_fail_alloc_at{0};   // test hook: this allocation of the next lmoe_create fails
 
 lmoe_status fail(lmoe_status s, const char *fmt, ...)
@@ -104,6 +107,12 @@ struct lmoe_handle {
     void *Wdown;      // [l, d]
     void *Wgu;        // [E, 2f, l] interleaved
     void *D;          // [E, l, f]
+    // 4-bit routed experts (lmoe_create_mx4): Wgu and D hold codes, half a byte per value
+    bool mx4 = false;
+    uint8_t *Wgu_scales = nullptr;   // [E, 2f, mx4_scale_pitch(l)]
+    uint8_t *D_scales = nullptr;     // [E, l, mx4_scale_pitch(f)]
+    FewMaps few;                     // few-token layer: tensor maps of the weights above
+    bool few_ok = false;
     void *Wgu_s;      // [4 f_s, d] interleaved (both shared experts as one of width 2 f_s)
     void *Wcat;       // [d, 2 f_s + l]
     void *const *stage_events;  // caller's cudaEvent_t[LMOE_NUM_STAGES + 1] or NULL
@@ -270,7 +279,7 @@ lmoe_status check_config(const lmoe_config *c, bool *tc)
 void free_handle(lmoe_handle *h)
 {
     if (!h) return;
-    void *ptrs[] = {h->Wr, h->Wr3, h->b, h->Wdown, h->Wgu, h->D, h->Wgu_s, h->Wcat};
+    void *ptrs[] = {h->Wr, h->Wr3, h->b, h->Wdown, h->Wgu, h->D, h->Wgu_s, h->Wcat, h->Wgu_scales, h->D_scales};
     for (void *p : ptrs)
         if (p) cudaFree(p);
     if (h->side) cudaStreamDestroy(h->side);
@@ -314,7 +323,9 @@ lmoe_status lmoe_config_from_base(int32_t d, int32_t m, int32_t N, int32_t K, in
     return LMOE_OK;
 }
 
-lmoe_status lmoe_create(const lmoe_config *cfg, const lmoe_weights *w, void *stream, lmoe_handle **out)
+// lmoe_create, or lmoe_create_mx4 when x4 is not NULL.
+static lmoe_status create_handle(const lmoe_config *cfg, const lmoe_weights *w, const lmoe_mx4_experts *x4,
+                                 void *stream, lmoe_handle **out)
 {
     g_err.clear();
     if (!out) return fail(LMOE_ERR_INVALID_ARG, "out is NULL");
@@ -322,13 +333,19 @@ lmoe_status lmoe_create(const lmoe_config *cfg, const lmoe_weights *w, void *str
     bool tc = false;
     lmoe_status st = check_config(cfg, &tc);
     if (st != LMOE_OK) return st;
-    if (!w || !w->W_r || !w->b || !w->G || !w->U || !w->D || !w->Gs || !w->Us || !w->Ds ||
+    if (!w || !w->W_r || !w->b || !w->Gs || !w->Us || !w->Ds || (!x4 && (!w->G || !w->U || !w->D)) ||
         (!cfg->standard && (!w->W_down || !w->W_up)))
         return fail(LMOE_ERR_INVALID_ARG, "a weight pointer is NULL");
-    if (tc) {
-        st = tc_check_device();
-        if (st != LMOE_OK) return st;
+    if (x4) {
+        if (!x4->G || !x4->G_scales || !x4->U || !x4->U_scales || !x4->D || !x4->D_scales)
+            return fail(LMOE_ERR_INVALID_ARG, "a 4-bit expert pointer is NULL");
+        if (!tc) return fail(LMOE_ERR_UNSUPPORTED, "4-bit experts need bf16 tokens and the tensor-core path");
+        if (((uintptr_t)x4->G | (uintptr_t)x4->U | (uintptr_t)x4->D) & 15u)
+            return fail(LMOE_ERR_UNSUPPORTED, "4-bit codes must be 16-byte aligned");
     }
+    st = tc_check_device();   // the tensor-map encoder and an sm_100 device
+    if (tc && st != LMOE_OK) return st;
+    const bool few_ok = st == LMOE_OK;
     cudaStream_t s = (cudaStream_t)stream;
     lmoe_handle *h = new lmoe_handle();
     h->cfg = *cfg;
@@ -336,6 +353,7 @@ lmoe_status lmoe_create(const lmoe_config *cfg, const lmoe_weights *w, void *str
     h->tc = tc;
     h->ib = tc ? TC_BN / 4 : SIMT_BN / 2;   // tensor cores: 64-row blocks (see the GLU epilogue)
     h->tb = cfg->dtype == LMOE_BF16 ? 2 : 4;
+    h->mx4 = x4 != nullptr;
     const lmoe_config &c = *cfg;
     const size_t tb = h->tb;
     const int64_t fs = c.f_shared;
@@ -363,15 +381,32 @@ lmoe_status lmoe_create(const lmoe_config *cfg, const lmoe_weights *w, void *str
     ALLOC(h->Wr, sizeof(float) * c.E * c.d);
     ALLOC(h->b, sizeof(float) * c.E);
     if (!c.standard) ALLOC(h->Wdown, tb * c.l * c.d);
-    ALLOC(h->Wgu, tb * (size_t)c.E * 2 * c.f * c.l);
-    ALLOC(h->D, tb * (size_t)c.E * c.l * c.f);
+    const int64_t pitch_l = mx4_scale_pitch(c.l), pitch_f = mx4_scale_pitch(c.f);
+    if (x4) {   // 128 bytes behind the codes: a row's last 128-byte k-block may reach past the last row
+        ALLOC(h->Wgu, (size_t)c.E * 2 * c.f * (c.l / 2) + 128);
+        ALLOC(h->D, (size_t)c.E * c.l * (c.f / 2) + 128);
+        ALLOC(h->Wgu_scales, (size_t)c.E * 2 * c.f * pitch_l);
+        ALLOC(h->D_scales, (size_t)c.E * c.l * pitch_f);
+    } else {
+        ALLOC(h->Wgu, tb * (size_t)c.E * 2 * c.f * c.l);
+        ALLOC(h->D, tb * (size_t)c.E * c.l * c.f);
+    }
     ALLOC(h->Wgu_s, tb * 4 * fs * c.d);
     ALLOC(h->Wcat, tb * c.d * hs_cols(c));
     STEP(cudaMemcpyAsync(h->Wr, w->W_r, sizeof(float) * c.E * c.d, cudaMemcpyDeviceToDevice, s));
     STEP(cudaMemcpyAsync(h->b, w->b, sizeof(float) * c.E, cudaMemcpyDeviceToDevice, s));
     if (!c.standard) STEP(cudaMemcpyAsync(h->Wdown, w->W_down, tb * c.l * c.d, cudaMemcpyDeviceToDevice, s));
-    STEP(cudaMemcpyAsync(h->D, w->D, tb * (size_t)c.E * c.l * c.f, cudaMemcpyDeviceToDevice, s));
-    STEP(launch_pack_glu(w->G, w->U, h->Wgu, c.E, c.f, c.l, h->ib, (int)tb, s));
+    if (x4) {
+        STEP(cudaMemcpyAsync(h->D, x4->D, (size_t)c.E * c.l * (c.f / 2), cudaMemcpyDeviceToDevice, s));
+        STEP(launch_pack_glu(x4->G, x4->U, h->Wgu, c.E, c.f, c.l / 32, h->ib, 16, s));
+        STEP(launch_mx4_pack_scales((const uint8_t *)x4->G_scales, (const uint8_t *)x4->U_scales, h->Wgu_scales, c.E,
+                                    c.f, c.l / 32, pitch_l, h->ib, s));
+        STEP(launch_mx4_pack_scales((const uint8_t *)x4->D_scales, nullptr, h->D_scales, c.E, c.l, c.f / 32, pitch_f,
+                                    h->ib, s));
+    } else {
+        STEP(cudaMemcpyAsync(h->D, w->D, tb * (size_t)c.E * c.l * c.f, cudaMemcpyDeviceToDevice, s));
+        STEP(launch_pack_glu(w->G, w->U, h->Wgu, c.E, c.f, c.l, h->ib, (int)tb, s));
+    }
     // [2, f_s, d] stacks are the rows of one expert of width 2 f_s
     STEP(launch_pack_glu(w->Gs, w->Us, h->Wgu_s, 1, 2 * c.f_shared, c.d, h->ib, (int)tb, s));
     // standard: [D_s1 | D_s2] only (u is added in the final GEMM's epilogue)
@@ -387,6 +422,10 @@ lmoe_status lmoe_create(const lmoe_config *cfg, const lmoe_weights *w, void *str
     STEP(cudaStreamCreateWithFlags(&h->copy_in, cudaStreamNonBlocking));
     STEP(cudaStreamCreateWithFlags(&h->copy_out, cudaStreamNonBlocking));
     for (cudaEvent_t &e : h->ev_host) STEP(cudaEventCreateWithFlags(&e, cudaEventDisableTiming));
+    if (few_ok) {
+        const FewWeights fw = {h->Wr, h->Wdown, h->Wgu_s, h->Wcat, h->Wgu, h->D, h->Wgu_scales, h->D_scales, h->mx4};
+        h->few_ok = few_make_maps(c, fw, &h->few);
+    }
     STEP(cudaStreamSynchronize(s));
 #undef ALLOC
 #undef STEP
@@ -394,7 +433,102 @@ lmoe_status lmoe_create(const lmoe_config *cfg, const lmoe_weights *w, void *str
     return LMOE_OK;
 }
 
+lmoe_status lmoe_create(const lmoe_config *cfg, const lmoe_weights *w, void *stream, lmoe_handle **out)
+{
+    return create_handle(cfg, w, nullptr, stream, out);
+}
+
+lmoe_status lmoe_create_mx4(const lmoe_config *cfg, const lmoe_weights *w, const lmoe_mx4_experts *experts,
+                            void *stream, lmoe_handle **out)
+{
+    static const lmoe_mx4_experts none = {};
+    return create_handle(cfg, w, experts ? experts : &none, stream, out);
+}
+
 void lmoe_destroy(lmoe_handle *h) { free_handle(h); }
+
+// The handle's device must be current: its kernels are launched there, and the
+// streams and buffers of another device would be used from the wrong one.
+static lmoe_status check_current_device(const lmoe_handle *h)
+{
+    int dev = -1;
+    LMOE_CUDA(cudaGetDevice(&dev));
+    if (dev != h->device)
+        return fail(LMOE_ERR_INVALID_ARG, "the handle's device %d is not current (device %d is)", h->device, dev);
+    return LMOE_OK;
+}
+
+lmoe_status lmoe_few_workspace_size(const lmoe_handle *h, int64_t T, size_t *bytes)
+{
+    g_err.clear();
+    if (!h || !bytes) return fail(LMOE_ERR_INVALID_ARG, "NULL argument");
+    if (T < 0) return fail(LMOE_ERR_INVALID_ARG, "T < 0");
+    if (T > LMOE_FEW_MAX_T) return fail(LMOE_ERR_UNSUPPORTED, "T=%lld > %d", (long long)T, LMOE_FEW_MAX_T);
+    *bytes = few_workspace_bytes(h->cfg, T);
+    return LMOE_OK;
+}
+
+lmoe_status lmoe_forward_few(lmoe_handle *h, const void *x, int64_t T, void *output, int32_t *selected_experts,
+                             void *mixture_weights, void *latent_routed_aggregate, void *workspace, size_t ws_bytes,
+                             void *stream)
+{
+    g_err.clear();
+    if (!h) return fail(LMOE_ERR_INVALID_ARG, "handle is NULL");
+    if (T < 0) return fail(LMOE_ERR_INVALID_ARG, "T < 0");
+    if (T == 0) return LMOE_OK;
+    if (T > LMOE_FEW_MAX_T) return fail(LMOE_ERR_UNSUPPORTED, "T=%lld > %d", (long long)T, LMOE_FEW_MAX_T);
+    if (!x || !output || !selected_experts || !mixture_weights || !latent_routed_aggregate || !workspace)
+        return fail(LMOE_ERR_INVALID_ARG, "NULL tensor pointer");
+    if (ws_bytes < few_workspace_bytes(h->cfg, T))
+        return fail(LMOE_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, few_workspace_bytes(h->cfg, T));
+    if ((uintptr_t)workspace % 256) return fail(LMOE_ERR_WORKSPACE, "workspace not 256-byte aligned");
+    if ((uintptr_t)x & 15u) return fail(LMOE_ERR_UNSUPPORTED, "x must be 16-byte aligned");
+    if (!h->few_ok) return fail(LMOE_ERR_UNSUPPORTED, "the few-token layer needs an sm_100 device");
+    const lmoe_status st = check_current_device(h);
+    if (st != LMOE_OK) return st;
+    LMOE_CUDA(few_launch(h->cfg, h->few, h->mx4, h->b, x, (int)T, output, selected_experts, mixture_weights,
+                         latent_routed_aggregate, workspace, g_stall_few.exchange(0) != 0, (cudaStream_t)stream));
+    return LMOE_OK;
+}
+
+// Checks shared by the two directions of the 4-bit conversion.
+static lmoe_status check_mx4(const void *a, const void *b, const void *c, int32_t dtype, int64_t rows, int64_t cols,
+                             int64_t ld, const void *values, const void *codes)
+{
+    if (rows < 0 || cols < 0) return fail(LMOE_ERR_INVALID_ARG, "negative size");
+    if (dtype != LMOE_F32 && dtype != LMOE_BF16) return fail(LMOE_ERR_INVALID_ARG, "unknown dtype");
+    if (cols % 32) return fail(LMOE_ERR_UNSUPPORTED, "cols=%lld is not a multiple of 32", (long long)cols);
+    if (rows == 0 || cols == 0) return LMOE_OK;
+    if (!a || !b || !c) return fail(LMOE_ERR_INVALID_ARG, "NULL pointer");
+    if (ld < cols) return fail(LMOE_ERR_INVALID_ARG, "row stride %lld < cols=%lld", (long long)ld, (long long)cols);
+    if (rows > ((int64_t)1 << 46) / cols) return fail(LMOE_ERR_UNSUPPORTED, "more than 2^46 values");
+    const int64_t per16 = dtype == LMOE_BF16 ? 8 : 4;
+    if (((uintptr_t)values & 15u) || (rows > 1 && ld % per16) || ((uintptr_t)codes & 3u))
+        return fail(LMOE_ERR_UNSUPPORTED, "values and their rows must be 16-byte aligned, codes 4-byte aligned");
+    return LMOE_OK;
+}
+
+lmoe_status lmoe_mx4_quantize(const void *x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, void *codes,
+                              void *scales, void *stream)
+{
+    g_err.clear();
+    const lmoe_status st = check_mx4(x, codes, scales, dtype, rows, cols, ld, x, codes);
+    if (st != LMOE_OK || rows == 0 || cols == 0) return st;
+    LMOE_CUDA(launch_mx4_quantize(x, dtype == LMOE_BF16, rows, cols, rows > 1 ? ld : cols, (uint8_t *)codes,
+                                  (uint8_t *)scales, (cudaStream_t)stream));
+    return LMOE_OK;
+}
+
+lmoe_status lmoe_mx4_dequantize(const void *codes, const void *scales, int64_t rows, int64_t cols, int32_t dtype,
+                                void *y, int64_t ld, void *stream)
+{
+    g_err.clear();
+    const lmoe_status st = check_mx4(codes, scales, y, dtype, rows, cols, ld, y, codes);
+    if (st != LMOE_OK || rows == 0 || cols == 0) return st;
+    LMOE_CUDA(launch_mx4_dequantize((const uint8_t *)codes, (const uint8_t *)scales, rows, cols, y,
+                                    dtype == LMOE_BF16, rows > 1 ? ld : cols, (cudaStream_t)stream));
+    return LMOE_OK;
+}
 
 lmoe_status lmoe_workspace_size(const lmoe_handle *h, int64_t T, size_t *bytes)
 {
@@ -437,6 +571,10 @@ lmoe_status lmoe_debug_inject(int32_t what, int32_t arg)
     g_err.clear();
     if (what == LMOE_INJECT_STALL_NEXT_GEMM) {
         tc_debug_stall_next();
+        return LMOE_OK;
+    }
+    if (what == LMOE_INJECT_STALL_NEXT_FEW) {
+        g_stall_few.store(1);
         return LMOE_OK;
     }
     if (what == LMOE_INJECT_FAIL_ALLOC) {
@@ -530,6 +668,7 @@ static lmoe_status forward_body(lmoe_handle *h, const void *x, int64_t T, void *
     if (!h) return fail(LMOE_ERR_INVALID_ARG, "handle is NULL");
     if (T < 0) return fail(LMOE_ERR_INVALID_ARG, "T < 0");
     if (T == 0) return LMOE_OK;
+    if (h->mx4) return fail(LMOE_ERR_UNSUPPORTED, "4-bit experts: not built yet");
     if (!x || !output || !selected_experts || !mixture_weights || !latent_routed_aggregate || !workspace)
         return fail(LMOE_ERR_INVALID_ARG, "NULL tensor pointer");
     if (T * h->cfg.k > 0x7fffffffLL) return fail(LMOE_ERR_UNSUPPORTED, "T * k exceeds 2^31 - 1");

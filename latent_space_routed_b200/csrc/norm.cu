@@ -290,7 +290,9 @@ cudaError_t launch_combine_norm(const void *Yp, const int32_t *slot_of, int64_t 
 cudaError_t launch_pack_glu(const void *G, const void *U, void *P, int nE, int F, int K, int ib, int elem_bytes,
                             cudaStream_t s)
 {
-    if (elem_bytes == 2)
+    if (elem_bytes == 16)      // K counts 16-byte units (rows of 4-bit codes)
+        pack_glu_kernel<uint4><<<2048, 256, 0, s>>>((const uint4 *)G, (const uint4 *)U, (uint4 *)P, nE, F, K, ib);
+    else if (elem_bytes == 2)
         pack_glu_kernel<bf16><<<2048, 256, 0, s>>>((const bf16 *)G, (const bf16 *)U, (bf16 *)P, nE, F, K, ib);
     else
         pack_glu_kernel<float><<<2048, 256, 0, s>>>((const float *)G, (const float *)U, (float *)P, nE, F, K, ib);
