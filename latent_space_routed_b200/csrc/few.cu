@@ -25,7 +25,7 @@
 // producer warps keep the next items' tiles in flight while its other warps
 // still wait for the activations: HBM does not idle between the stages.
 //
-// Roles (14 warps, one block per SM):
+// Roles (15 warps, one block per SM):
 //   warps 0-7   consumers: products from shared memory, sums over the warps, epilogues
 //   warp 8, 9   producers: TMA copies of 16-row (router: 4-row) tiles into a ring of 16 KB stages;
 //               a stage is two boxes of 8 KB, one per producer (one thread's copies go out one
@@ -34,6 +34,8 @@
 //               successive K ranges of one row group
 //   warps 10-13 loaders: bring an item's activations from global memory into one of two
 //               shared-memory slots, in the form that the product wants, one set ahead
+//   warp 14     signaller: publishes finished items to the other blocks (the fence before the
+//               counter costs 1000 to 2000 cycles, which the consumers would otherwise spend per item)
 //
 // Arithmetic: bf16 weights are the A operand of m16n8k16 (16 weight rows), the tokens its
 // eight columns, fp32 sums.  tcgen05 would need 128 rows per tile and gains nothing here: the
@@ -58,7 +60,7 @@ namespace {
 using namespace ptx;
 
 constexpr int CONSUMERS = 8, LOADERS = 4;
-constexpr int THREADS = 32 * (CONSUMERS + 2 + LOADERS);
+constexpr int THREADS = 32 * (CONSUMERS + 2 + LOADERS + 1);
 constexpr int CT = 32 * CONSUMERS, LT = 32 * LOADERS;
 constexpr int STAGE_BYTES = 16384, BOX_BYTES = 8192;
 constexpr int SCALE_BOX = 512;                   // 16 rows of 32 scales (1024 values), per box
@@ -81,9 +83,9 @@ struct Item {
     int out0;            // first output row
 };
 
-// A touched expert: its id, the number of its slots and the slots in token order.
+// A touched expert: its id, the tokens that selected it (a bit each) and its slots in token order.
 struct Touched {
-    int16_t expert, n, slot[FEW_MAX_T];
+    int16_t expert, mask, slot[FEW_MAX_T];
 };
 
 struct FewParams {
@@ -97,7 +99,7 @@ struct FewParams {
     double *r64;             // [T, E] biased scores' raw scores
     float *p32;              // [T, k]
     Touched *tab;
-    float *z, *hs, *H, *part, *ysl, *u;
+    float *z, *hs, *H, *part, *ysl, *u, *ssq;   // ssq: [T, l / 32] sums of squares of u
     int stages, slot_bytes, scales;
     int stall_test;
 };
@@ -190,26 +192,45 @@ __device__ __forceinline__ float f16_scale(float amax, float *inverse)
     return __uint_as_float((uint32_t)(268 - e) << 23);
 }
 
-__device__ __forceinline__ float4 scaled(float4 v, float s) { return make_float4(v.x * s, v.y * s, v.z * s, v.w * s); }
-
-// One row of `n` fp32 values (a multiple of 32) into the slot, by the loader threads.
-template <int FORM>
-__device__ __forceinline__ void load_row(uint32_t row, uint32_t plane, const float *src, int n, float s, int tid)
+// The loaders' rows: `rows` rows of n4 groups of four values, dealt to the loader
+// threads one after another so that every thread keeps four loads in flight
+// across rows.  src(row) is the row's first value, mul(row) its factor.
+template <int FORM, typename Src, typename Mul>
+__device__ __forceinline__ void load_rows(uint32_t dst, int stride, uint32_t plane, int rows, int n4, int tid, Src src,
+                                          Mul mul)
 {
-    const float4 *v = reinterpret_cast<const float4 *>(src);
-    const int n4 = n / 4;
-    int c = tid;
-    for (; c + 3 * LT < n4; c += 4 * LT) {
-        float4 t[4];
+    int row = 0, c = tid;
+    auto settle = [&]() {
+        while (c >= n4 && row < rows) {
+            c -= n4;
+            ++row;
+        }
+    };
+    settle();
+    while (row < rows) {
+        float4 v[4];
+        float m[4];
+        int r[4], cc[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) t[i] = __ldcg(v + c + i * LT);
+        for (int i = 0; i < 4; ++i) {
+            r[i] = row;
+            cc[i] = c;
+            if (row < rows) {
+                v[i] = __ldcg(reinterpret_cast<const float4 *>(src(row)) + c);
+                m[i] = mul(row);
+                c += LT;
+                settle();
+            }
+        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) put4<FORM>(row, plane, 4 * (c + i * LT), scaled(t[i], s));
+        for (int i = 0; i < 4; ++i)
+            if (r[i] < rows)
+                put4<FORM>(dst + (uint32_t)(r[i] * stride), plane, 4 * cc[i],
+                           make_float4(v[i].x * m[i], v[i].y * m[i], v[i].z * m[i], v[i].w * m[i]));
     }
-    for (; c < n4; c += LT) put4<FORM>(row, plane, 4 * c, scaled(__ldcg(v + c), s));
 }
 
-// One row of tokens x (bf16) as fp32 scaled terms, for 4-bit experts at the model width.
+// One row of tokens x (bf16) as scaled terms, for 4-bit experts at the model width.
 __device__ __forceinline__ void load_row_bf16_scaled(uint32_t row, uint32_t plane, const bf16 *src, int n, float s,
                                                      int tid)
 {
@@ -246,11 +267,12 @@ __device__ __forceinline__ unsigned long long key64(double v)
 struct RoleBarrier {
     uint32_t bar, parity;
     const volatile int *abort;
+    bool ok;                 // false once a wait gave up
     __device__ __forceinline__ bool sync()
     {
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-        const bool ok = mbar_wait(bar, parity, abort);
+        ok = mbar_wait(bar, parity, abort);
         parity ^= 1u;
         return ok;
     }
@@ -265,7 +287,7 @@ struct Shared {
     float *inv;              // [2 slots][8]: inverse of the activations' scale
     float *lred;             // loaders' sums [4]
     // [0] abort, [1] items published, [2] stages issued by A, [4] stages consumed,
-    // [8, 16) scan, [16, 20) items passed by each loader, [20] by B
+    // [8, 16) scan, items passed: [16, 20) by each loader, [20] by B, [21] by the signaller; [22] items stored (x 8)
     int *flags;
 };
 
@@ -327,7 +349,7 @@ __device__ __forceinline__ bool decode(const FewParams &p, const Counts &n, cons
         it->kind = ROUTED_DOWN; it->ti = i / per; it->out0 = 32 * (i % per);
         it->row0 = tab[it->ti].expert * p.l + it->out0; it->row1 = it->row0 + 16;
         it->nkb = WT == W_MX4 ? (p.f + 255) / 256 : p.f / KE;
-        it->ncol = tab[it->ti].n;
+        it->ncol = __popc((unsigned)tab[it->ti].mask);
         return true;
     }
     i -= n.routed_down;
@@ -367,11 +389,56 @@ struct Consumer {
 };
 
 // Sum of the warps' partial products: thread (row, column) of 16 x 8, warps [w0, w0 + n).
-__device__ __forceinline__ float red_sum(const float *red, int w0, int n, int cell)
+// `packed`: the lo terms' sums are four columns further.
+__device__ __forceinline__ float red_sum(const float *red, int w0, int n, int cell, bool packed)
 {
     float v = 0.f;
     for (int w = w0; w < w0 + n; ++w) v += red[w * 128 + cell];
+    if (packed && (cell & 4) == 0)
+        for (int w = w0; w < w0 + n; ++w) v += red[w * 128 + cell + 4];
     return v;
+}
+
+// Four blocks of 32 values (half 0 or 1 of a 128-byte k-block) of 16 rows of 4-bit
+// weights against eight columns: acc += scale of the row's block * partial sum.
+template <bool PACKED>
+__device__ __forceinline__ void mx4_blocks(float (&acc)[4], uint32_t tile, uint32_t arow, uint32_t plane, uint2 sa,
+                                           uint2 sb, int gid, int c4, int half, int nb)
+{
+    uint32_t a[4], b[4];
+    uint4 h[4], lo[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (4 * half + j < nb) {
+            const uint32_t off = (uint32_t)((((4 * half + j) ^ gid) << 4) + 4 * c4);
+            a[j] = lds32(tile + off);
+            b[j] = lds32(tile + 1024 + off);
+            h[j] = lds128(arow + 64u * (4 * half + j));
+            if (!PACKED) lo[j] = lds128(arow + plane + 64u * (4 * half + j));
+        }
+    const uint32_t ea = half ? sa.y : sa.x, eb = half ? sb.y : sb.x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (4 * half + j < nb) {
+            uint32_t wa[4], wb[4];
+            e2m1x8_to_f16(wa, a[j]);
+            e2m1x8_to_f16(wb, b[j]);
+            float t[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_f16(t, wa[0], wb[0], wa[1], wb[1], h[j].x, h[j].y);
+            mma_f16(t, wa[2], wb[2], wa[3], wb[3], h[j].z, h[j].w);
+            if (!PACKED) {
+                mma_f16(t, wa[0], wb[0], wa[1], wb[1], lo[j].x, lo[j].y);
+                mma_f16(t, wa[2], wb[2], wa[3], wb[3], lo[j].z, lo[j].w);
+            }
+            // 2^(e - 127); e = 0 counts as zero (below fp32's normal range), 255 is NaN
+            const uint32_t xa = (ea >> (8 * j)) & 255u, xb = (eb >> (8 * j)) & 255u;
+            const float fa = __uint_as_float(xa == 255u ? 0x7fffffffu : xa << 23);
+            const float fb = __uint_as_float(xb == 255u ? 0x7fffffffu : xb << 23);
+            acc[0] = fmaf(t[0], fa, acc[0]);
+            acc[1] = fmaf(t[1], fa, acc[1]);
+            acc[2] = fmaf(t[2], fb, acc[2]);
+            acc[3] = fmaf(t[3], fb, acc[3]);
+        }
 }
 
 template <int WT>
@@ -390,13 +457,14 @@ __device__ __forceinline__ void store_token(void *x, int64_t i, float v)
 // order with their slots.  One warp per token: k rounds of a warp maximum over
 // 64-bit score keys, lowest index first among equals.
 template <int WT>
-__device__ __noinline__ bool route_item(const FewParams &p, const Shared &sh, RoleBarrier &bar, int warp, int lane)
+__device__ __noinline__ RoleBarrier route_item(const FewParams &p, float *red, int *scan, RoleBarrier bar, int warp,
+                                               int lane)
 {
     constexpr unsigned FULL = 0xffffffffu;
-    uint8_t *slot_of = reinterpret_cast<uint8_t *>(sh.red);       // [8 tokens][MAX_E]: slot + 1
+    uint8_t *slot_of = reinterpret_cast<uint8_t *>(red);       // [8 tokens][MAX_E]: slot + 1
     const int tid = warp * 32 + lane;
     for (int i = tid; i < FEW_MAX_T * MAX_E / 4; i += CT) reinterpret_cast<uint32_t *>(slot_of)[i] = 0u;
-    if (!bar.sync()) return false;
+    if (!bar.sync()) return bar;
     if (warp < p.T) {
         const int t = warp;
         const double *r = p.r64 + (int64_t)t * p.E;
@@ -461,7 +529,7 @@ __device__ __noinline__ bool route_item(const FewParams &p, const Shared &sh, Ro
             if (lane == 0) p.ctl[C_AMAX_X + t] = __float_as_uint(m);
         }
     }
-    if (!bar.sync()) return false;
+    if (!bar.sync()) return bar;
     // touched experts: thread i takes experts [4 i, 4 i + 4)
     int mask[4], mine = 0;
 #pragma unroll
@@ -476,16 +544,15 @@ __device__ __noinline__ bool route_item(const FewParams &p, const Shared &sh, Ro
         const int v = __shfl_up_sync(FULL, incl, o);
         if (lane >= o) incl += v;
     }
-    int *scan = sh.flags + 8;
     if (lane == 31) scan[warp] = incl;
-    if (!bar.sync()) return false;
+    if (!bar.sync()) return bar;
     int at = incl - mine;
     for (int w = 0; w < warp; ++w) at += scan[w];
     for (int q = 0; q < 4; ++q)
         if (mask[q]) {
             Touched e;
             e.expert = (int16_t)(4 * tid + q);
-            e.n = (int16_t)__popc(mask[q]);
+            e.mask = (int16_t)mask[q];
             int c = 0;
             for (int t = 0; t < FEW_MAX_T; ++t) e.slot[t] = -1;
             for (int t = 0; t < p.T; ++t)
@@ -494,9 +561,9 @@ __device__ __noinline__ bool route_item(const FewParams &p, const Shared &sh, Ro
         }
     int total = 0;
     for (int w = 0; w < CONSUMERS; ++w) total += scan[w];
-    if (!bar.sync()) return false;
+    if (!bar.sync()) return bar;
     if (tid == 0) red_release(p.ctl + C_ROUTED, (unsigned)total);   // never 0: T, k >= 1
-    return true;
+    return bar;
 }
 
 template <int WT>
@@ -521,10 +588,12 @@ __device__ __forceinline__ void combine_item(const FewParams &p, const Item &it,
             store_token<WT>(p.y, (int64_t)t * p.d + c, __ldcg(q) + __ldcg(q + (int64_t)p.T * p.d) + u);
         } else {
             p.u[(int64_t)t * p.l + c] = u;
+            float ss = u * u;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (lane == 0) p.ssq[t * (p.l / 32) + it.out0 / 32] = ss;
         }
     }
-    __syncwarp();
-    if (lane == 0) red_release(p.ctl + C_U, 1u);
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -627,7 +696,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 if (more) next = atomicAdd(p.ctl + C_TICKET, 1u);   // used in the next round
                 // the entry's previous item must be behind every reader (rarely a wait)
                 const long long t0 = clock64();
-                for (int r = 0; r < LOADERS + 1 && ok; ++r)
+                for (int r = 0; r < LOADERS + 2 && ok; ++r)
                     while (q - passed[r] >= QUEUE && ok)
                         if (*abort || clock64() - t0 > WAIT_LIMIT_CYCLES) ok = false;
                 if (!ok) give_up(0x1);
@@ -727,11 +796,11 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 }
             }
         }
-    } else if (warp > CONSUMERS + 1) {
+    } else if (warp > CONSUMERS + 1 && warp < CONSUMERS + 2 + LOADERS) {
         // ------------------------------------------------------------ loaders
         const int tid = threadIdx.x - 32 * (CONSUMERS + 2), lw = warp - CONSUMERS - 2;
-        RoleBarrier bar = {sh.load, 0u, abort};
-        int set = 0, cur_key = -1, cur_seg = -1;
+        RoleBarrier bar = {sh.load, 0u, abort, true};
+        int set = 0, cur_key = -1, cur_seg = -1, ready = -1;   // ready: last kind whose inputs are complete
         bool ok = true;
         for (int q = 0; ok; ++q) {
             int good = 1;
@@ -756,25 +825,24 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
             const bool mx4 = WT == W_MX4 && (it.kind == ROUTED_GU || it.kind == ROUTED_DOWN);
             for (int seg = 0; seg < a.nseg && ok; ++seg) {
                 if (a.key == cur_key && seg == cur_seg) continue;
-                const bool same_rows = a.key == cur_key;
                 cur_key = a.key;
                 cur_seg = seg;
                 const int slot = set & 1;
                 if (lane == 0) {
                     good = mbar_wait(sh.act_empty + 8u * slot, (uint32_t)((set >> 1) & 1) ^ 1u, abort);
-                    // the producers of these values, once per set of rows
-                    if (good && !same_rows) {
-                        if (it.kind == ROUTED_GU && !p.standard) good = wait_count(p.ctl, C_Z, 4u * n.down, abort);
+                    if (good && it.kind != ready) {          // the items that write these values
+                        if (it.kind == ROUTED_GU && !p.standard) good = wait_count(p.ctl, C_Z, n.down, abort);
                         // (the failure-detection test waits for one count too many)
                         if (it.kind == SHARED_DOWN)
-                            good = wait_count(p.ctl, C_HS, 4u * n.shared_gu + (p.stall_test ? 1u : 0u), abort);
+                            good = wait_count(p.ctl, C_HS, n.shared_gu + (p.stall_test ? 1u : 0u), abort);
                         if (it.kind == ROUTED_DOWN)
-                            good = wait_count(p.ctl, C_H, 4u * ld_acquire(p.ctl + C_ROUTED) * (p.f / 16), abort);
+                            good = wait_count(p.ctl, C_H, ld_acquire(p.ctl + C_ROUTED) * (p.f / 16), abort);
                         if (it.kind == UP)
-                            good = wait_count(p.ctl, C_U, 8u * n.combine, abort) &&
-                                   wait_count(p.ctl, C_PART, 8u * n.shared_down, abort);
+                            good = wait_count(p.ctl, C_U, n.combine, abort) &&
+                                   wait_count(p.ctl, C_PART, n.shared_down, abort);
                     }
                 }
+                ready = it.kind;
                 ok = __shfl_sync(0xffffffffu, good, 0) != 0;
                 if (!ok) {
                     if (lane == 0) give_up(0x4);
@@ -784,134 +852,137 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 const uint32_t plane = (uint32_t)(it.ncol * a.stride);
                 const int k0 = seg * a.kseg, kn = a.K - k0 < a.kseg ? a.K - k0 : a.kseg;
                 float *inv = sh.inv + 8 * slot;
+                const bool x_rows = it.kind <= SHARED_GU || (it.kind == ROUTED_GU && p.standard);
+                if (x_rows && !mx4) {
+                    // x as it is: one bulk copy per row
+                    if (tid == 0) {
+                        const uint32_t bytes = (uint32_t)(kn * a.eb);
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        mbar_expect_tx(sh.act_full + 8u * slot, bytes * (uint32_t)it.ncol);
+                        for (int t = 0; t < it.ncol; ++t)
+                            bulk_load(dst + (uint32_t)(t * a.stride),
+                                      (const char *)p.x + ((int64_t)t * p.d + k0) * a.eb, bytes, sh.act_full + 8u * slot);
+                    } else if (lane == 0) {
+                        mbar_arrive(sh.act_full + 8u * slot);
+                    }
+                    ++set;
+                    continue;
+                }
                 if (it.kind == UP) {
-                    // RMSNorm: the sum of squares over the whole row, in a fixed order
-                    for (int t = 0; t < it.ncol; ++t) {
-                        const float4 *v = reinterpret_cast<const float4 *>(p.u + (int64_t)t * p.l);
+                    // RMSNorm: each token's sum of squares from the combine items' parts, in a fixed order
+                    const int nb = p.l / 32;
+                    for (int t = lw; t < it.ncol; t += LOADERS) {
                         float ss = 0.f;
-#pragma unroll 4
-                        for (int c = tid; c < p.l / 4; c += LT) {
-                            const float4 w = __ldcg(v + c);
-                            ss += w.x * w.x + w.y * w.y + w.z * w.z + w.w * w.w;
-                        }
+                        for (int c = lane; c < nb; c += 32) ss += __ldcg(p.ssq + t * nb + c);
 #pragma unroll
                         for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-                        if (lane == 0) sh.lred[lw] = ss;
-                        if (!(ok = bar.sync())) break;
-                        const float rms = 1.0f / sqrtf((sh.lred[0] + sh.lred[1] + sh.lred[2] + sh.lred[3]) / (float)p.l +
-                                                       p.eps);
-                        if (!(ok = bar.sync())) break;
-                        const uint32_t row = dst + (uint32_t)(t * a.stride);
-                        const float *src = p.u + (int64_t)t * p.l + k0;
-                        if (WT == W_F32) load_row<F_F32>(row, plane, src, kn, rms, tid);
-                        else load_row<F_BF16X2>(row, plane, src, kn, rms, tid);
+                        if (lane == 0) sh.lred[t] = 1.0f / sqrtf(ss / (float)p.l + p.eps);
+                    }
+                    if (!(ok = bar.sync())) {
+                        if (lane == 0) give_up(0x4);
+                        break;
+                    }
+                    load_rows<WT == W_F32 ? F_F32 : F_BF16X2>(
+                        dst, a.stride, plane, it.ncol, kn / 4, tid,
+                        [&](int t) { return p.u + (int64_t)t * p.l + k0; }, [&](int t) { return sh.lred[t]; });
+                } else if (mx4) {
+                    const unsigned *amax = p.ctl + (it.kind == ROUTED_DOWN ? C_AMAX_H : x_rows ? C_AMAX_X : C_AMAX_Z);
+                    const Touched &e = sh.tab[it.ti];
+                    auto at = [&](int t) { return it.kind == ROUTED_DOWN ? (int)e.slot[t] : t; };
+                    auto mul = [&](int t) {
+                        float back;
+                        return f16_scale(__uint_as_float(__ldcg(amax + at(t))), &back);
+                    };
+                    if (tid < it.ncol) f16_scale(__uint_as_float(__ldcg(amax + at(tid))), &inv[tid]);
+                    if (x_rows) {
+                        for (int t = 0; t < it.ncol; ++t)
+                            load_row_bf16_scaled(dst + (uint32_t)(t * a.stride), plane,
+                                                 (const bf16 *)p.x + (int64_t)t * p.d + k0, kn, mul(t), tid);
+                    } else {
+                        const float *src = (it.kind == ROUTED_DOWN ? p.H : p.z) + k0;
+                        load_rows<F_F16X2>(dst, a.stride, plane, it.ncol, kn / 4, tid,
+                                           [&](int t) { return src + (int64_t)at(t) * a.K; }, mul);
                     }
                 } else {
-                    for (int t = 0; t < it.ncol; ++t) {
-                        const uint32_t row = dst + (uint32_t)(t * a.stride);
-                        const float *src = nullptr;
-                        const unsigned *amax = nullptr;
-                        if (it.kind == ROUTED_GU && !p.standard) {
-                            src = p.z + (int64_t)t * p.l;
-                            amax = p.ctl + C_AMAX_Z + t;
-                        } else if (it.kind == SHARED_DOWN) {
-                            src = p.hs + (int64_t)t * 2 * p.fs + it.ti * p.fs;
-                        } else if (it.kind == ROUTED_DOWN) {
-                            const int sl = sh.tab[it.ti].slot[t];
-                            src = p.H + (int64_t)sl * p.f;
-                            amax = p.ctl + C_AMAX_H + sl;
-                        } else if (mx4) {
-                            amax = p.ctl + C_AMAX_X + t;
-                        }
-                        if (!src && !mx4) {          // x as it is
-                            if (WT == W_F32) {
-                                const uint4 *v = reinterpret_cast<const uint4 *>((const float *)p.x + (int64_t)t * p.d + k0);
-                                for (int c = tid; c < kn / 4; c += LT) {
-                                    const uint4 w = v[c];
-                                    sts128(row + 16u * c, w.x, w.y, w.z, w.w);
-                                }
-                            } else {
-                                const uint4 *v = reinterpret_cast<const uint4 *>((const bf16 *)p.x + (int64_t)t * p.d + k0);
-                                for (int c = tid; c < kn / 8; c += LT) {
-                                    const uint4 w = v[c];
-                                    sts128(row + 16u * c, w.x, w.y, w.z, w.w);
-                                }
-                            }
-                        } else if (mx4) {
-                            float back;
-                            const float sc = f16_scale(__uint_as_float(__ldcg(amax)), &back);
-                            if (tid == 0) inv[t] = back;
-                            if (src) load_row<F_F16X2>(row, plane, src + k0, kn, sc, tid);
-                            else load_row_bf16_scaled(row, plane, (const bf16 *)p.x + (int64_t)t * p.d + k0, kn, sc, tid);
-                        } else if (WT == W_F32) {
-                            load_row<F_F32>(row, plane, src + k0, kn, 1.f, tid);
-                        } else {
-                            load_row<F_BF16X2>(row, plane, src + k0, kn, 1.f, tid);
-                        }
-                    }
-                }
-                if (!ok) {
-                    if (lane == 0) give_up(0x4);
-                    break;
+                    const Touched &e = sh.tab[it.ti];
+                    const int kind = it.kind;
+                    const float *src = (kind == ROUTED_DOWN ? p.H : kind == SHARED_DOWN ? p.hs + it.ti * p.fs : p.z) + k0;
+                    const int64_t ld = kind == ROUTED_DOWN ? p.f : kind == SHARED_DOWN ? 2 * p.fs : p.l;
+                    load_rows<WT == W_F32 ? F_F32 : F_BF16X2>(
+                        dst, a.stride, plane, it.ncol, kn / 4, tid,
+                        [&](int t) { return src + (int64_t)(kind == ROUTED_DOWN ? (int)e.slot[t] : t) * ld; },
+                        [](int) { return 1.f; });
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(sh.act_full + 8u * slot);
                 ++set;
             }
         }
-    } else {
+    } else if (warp < CONSUMERS) {
         // ------------------------------------------------------------ consumers
-        RoleBarrier bar = {sh.cons, 0u, abort};
+        RoleBarrier bar = {sh.cons, 0u, abort, true};
         int s = 0, set = -1, cur_key = -1, cur_seg = -1, par = 0, consumed = 0;
         uint32_t ph = 0;
         const int box = warp >> 2, sub = warp & 3;
         const int gid = lane >> 2, c4 = lane & 3;
         bool ok = true;
+        auto release = [&]() {           // this warp is done with the current stage
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sh.empty + 8u * s);
+            if (threadIdx.x == 0) sh.flags[4] = ++consumed;
+            if (++s == S) {
+                s = 0;
+                ph ^= 1u;
+            }
+        };
+        auto done = [&]() {              // this warp's part of the item is stored
+            __syncwarp();
+            if (lane == 0) red_shared_release(smem_u32(sh.flags + 22), 1u);
+        };
         for (;;) {
             if (!mbar_wait(sh.full + 8u * s, ph, abort)) {
-                if (lane == 0) give_up(0x8);
+                ok = false;
                 break;
             }
-            const int2 m0 = sh.meta[s];
-            const Item it = sh.queue[m0.x % QUEUE];
-            auto release = [&]() {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(sh.empty + 8u * s);
-                if (threadIdx.x == 0) sh.flags[4] = ++consumed;
-                if (++s == S) {
-                    s = 0;
-                    ph ^= 1u;
-                }
-            };
-            if (it.kind == END) {
+            const Item it = sh.queue[sh.meta[s].x % QUEUE];
+            const int kind = it.kind;
+            if (kind == END) {
                 release();
                 break;
             }
-            if (weightless(it.kind)) {
+            if (weightless(kind)) {
                 int good = 1;
                 if (lane == 0) {
-                    if (it.kind == ROUTE) {
+                    if (kind == ROUTE) {
                         good = wait_count(p.ctl, C_ROUTER, (unsigned)n.router, abort);
                     } else {
-                        good = wait_count(p.ctl, C_YS, 8u * ld_acquire(p.ctl + C_ROUTED) * (p.l / 32), abort);
-                        if (good && p.standard) good = wait_count(p.ctl, C_PART, 8u * n.shared_down, abort);
+                        good = wait_count(p.ctl, C_YS, ld_acquire(p.ctl + C_ROUTED) * (p.l / 32), abort);
+                        if (good && p.standard) good = wait_count(p.ctl, C_PART, n.shared_down, abort);
                     }
                 }
-                ok = __shfl_sync(0xffffffffu, good, 0) != 0;
-                if (ok && it.kind == ROUTE) ok = bar.sync() && route_item<WT>(p, sh, bar, warp, lane);
-                else if (ok) combine_item<WT>(p, it, warp, lane);
+                ok = __shfl_sync(0xffffffffu, good, 0) != 0 && bar.sync();
                 if (!ok) break;
+                if (kind == ROUTE) {
+                    bar = route_item<WT>(p, sh.red, sh.flags + 8, bar, warp, lane);
+                    if (!(ok = bar.ok)) break;
+                } else {
+                    combine_item<WT>(p, it, warp, lane);
+                    done();
+                }
                 release();
                 continue;
             }
 
             const ActPlan a = act_plan<WT>(p, it);
-            const bool two = two_groups(it.kind);
-            const int kb = box_kb(it.kind), nc = chunks(it);
-            const int col = gid < it.ncol ? gid : it.ncol - 1;   // columns past the tokens repeat the last one
-            // activations of the segment that holds value k; false when a wait gave up
-            uint32_t act = 0;
-            auto segment = [&](int k) -> bool {
+            const bool two = two_groups(kind);
+            const int nc = chunks(it), nkb = it.nkb;
+            const uint32_t plane = (uint32_t)(it.ncol * a.stride);
+            // Four columns or fewer of two terms: hi in columns 0-3, lo in 4-7 of one product
+            const bool packed = a.planes == 2 && it.ncol <= 4;
+            uint32_t act = 0;                 // the current segment's rows
+            // Stage c of the item and the activations for its values from k on; false when a wait gave up.
+            auto stage_ready = [&](int c, int k) -> bool {
+                if (c > 0 && !mbar_wait(sh.full + 8u * s, ph, abort)) return false;
                 const int seg = a.nseg == 1 ? 0 : k / a.kseg;
                 if (a.key != cur_key || seg != cur_seg) {
                     if (set >= 0) {
@@ -922,27 +993,24 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                     cur_key = a.key;
                     cur_seg = seg;
                     if (!mbar_wait(sh.act_full + 8u * (set & 1), (uint32_t)(set >> 1) & 1u, abort)) return false;
+                    act = sh.act + (uint32_t)((set & 1) * p.slot_bytes);
                 }
-                act = sh.act + (uint32_t)((set & 1) * p.slot_bytes);
                 return true;
             };
-            auto next_stage = [&](int c) -> bool {
-                if (c > 0 && !mbar_wait(sh.full + 8u * s, ph, abort)) return false;
-                return true;
-            };
+            act = sh.act + (uint32_t)((set & 1) * p.slot_bytes);
             float *red = sh.red + par * 1024;
 
-            if (it.kind == ROUTER) {
+            if (kind == ROUTER) {
                 // ---- 4 rows, 64-bit products: lane (row, 4-value piece)
                 double acc[FEW_MAX_T] = {};
                 const int row = lane >> 3, piece = lane & 7;
                 for (int c = 0; c < nc; ++c) {
-                    if (!(ok = next_stage(c) && segment(c * 1024))) break;
+                    if (!(ok = stage_ready(c, c * 1024))) break;
                     const uint32_t tile = sh.ring + (uint32_t)s * STAGE_BYTES + (uint32_t)box * BOX_BYTES;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int ko = sub * 4 + i, kblk = (2 * c + box) * 16 + ko;
-                        if (kblk >= it.nkb) break;
+                        if (kblk >= nkb) break;
                         const int R = ko * 4 + row;
                         const uint4 w = lds128(tile + (uint32_t)(R * 128 + ((piece ^ (R & 7)) << 4)));
                         const double w0 = __uint_as_float(w.x), w1 = __uint_as_float(w.y), w2 = __uint_as_float(w.z),
@@ -986,23 +1054,22 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                         for (int w = 0; w < CONSUMERS; ++w) v += rd[w * 32 + lane];
                         p.r64[(int64_t)t * p.E + e] = 1.0 / (1.0 + exp(-v));
                     }
-                    __syncwarp();
-                    if (lane == 0) red_release(p.ctl + C_ROUTER, 1u);
                 }
+                done();
                 par ^= 1;
                 continue;
             }
 
-            const bool mx4 = WT == W_MX4 && (it.kind == ROUTED_GU || it.kind == ROUTED_DOWN);
+            const bool mx4 = WT == W_MX4 && (kind == ROUTED_GU || kind == ROUTED_DOWN);
             if (WT == W_F32) {
                 // ---- fp32: lane (4-value piece, rows rq + 4 i)
                 float acc[4][FEW_MAX_T] = {};
                 const int piece = lane & 7, rq = lane >> 3;
                 for (int c = 0; c < nc; ++c) {
-                    if (!(ok = next_stage(c) && segment(c * (two ? 128 : 256)))) break;
+                    if (!(ok = stage_ready(c, c * (two ? 128 : 256)))) break;
                     const uint32_t tile = sh.ring + (uint32_t)s * STAGE_BYTES + (uint32_t)(box * BOX_BYTES + sub * 2048);
                     const int kblk = two ? c * 4 + sub : (2 * c + box) * 4 + sub;
-                    if (kblk < it.nkb) {
+                    if (kblk < nkb) {
                         const int k = kblk * 32 + 4 * piece - cur_seg * a.kseg;
                         float4 w[4];
 #pragma unroll
@@ -1041,105 +1108,121 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                     }
             } else {
                 float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                // the activation row of one of the eight columns (columns past the tokens repeat the last)
+                auto column = [&](int r) -> uint32_t {
+                    const int t = packed ? (r & 3) : r;
+                    return (uint32_t)((t < it.ncol ? t : it.ncol - 1) * a.stride) + (packed && r >= 4 ? plane : 0u);
+                };
                 if (mx4) {
                     // ---- 4-bit rows: a 16-byte piece of a row is one block of 32 values, eight of
                     // them (a word) per lane; the block's partial sum times its row's scale
-                    const int nblk = (it.kind == ROUTED_GU ? p.l : p.f) / 32;
-                    const uint32_t plane = (uint32_t)(it.ncol * a.stride);
+                    const int nblk = (kind == ROUTED_GU ? p.l : p.f) / 32;
+                    const uint32_t mycol = column(gid) + 16u * c4;
                     for (int c = 0; c < nc; ++c) {
-                        if (!(ok = next_stage(c) && segment(c * 1024))) break;
+                        if (!(ok = stage_ready(c, c * 1024))) break;
                         const uint32_t tile =
                             sh.ring + (uint32_t)s * STAGE_BYTES + (uint32_t)(box * BOX_BYTES + sub * 2048) + 128u * gid;
                         const int kblk = c * 4 + sub;
-                        int nb = nblk - kblk * 8;
+                        const int nb = min(nblk - kblk * 8, 8);
                         if (nb > 0) {
-                            if (nb > 8) nb = 8;
                             const uint32_t sc = sh.scales + (uint32_t)(s * 2 * SCALE_BOX + box * SCALE_BOX + 32 * gid + 8 * sub);
                             const uint2 sa = lds64(sc), sb = lds64(sc + 8 * 32);
-                            const uint32_t arow = act + (uint32_t)(col * a.stride + 2 * (kblk * 256 - cur_seg * a.kseg + 8 * c4));
+                            const uint32_t arow = act + mycol + (uint32_t)(2 * (kblk * 256 - cur_seg * a.kseg));
+                            if (packed) {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                if (j < nb) {
-                                    const uint32_t off = (uint32_t)(((j ^ gid) << 4) + 4 * c4);
-                                    uint32_t wa[4], wb[4];
-                                    e2m1x8_to_f16(wa, lds32(tile + off));
-                                    e2m1x8_to_f16(wb, lds32(tile + 1024 + off));
-                                    const uint4 h = lds128(arow + 64u * j), lo = lds128(arow + plane + 64u * j);
-                                    float t[4] = {0.f, 0.f, 0.f, 0.f};
-                                    mma_f16(t, wa[0], wb[0], wa[1], wb[1], h.x, h.y);
-                                    mma_f16(t, wa[0], wb[0], wa[1], wb[1], lo.x, lo.y);
-                                    mma_f16(t, wa[2], wb[2], wa[3], wb[3], h.z, h.w);
-                                    mma_f16(t, wa[2], wb[2], wa[3], wb[3], lo.z, lo.w);
-                                    // 2^(e - 127); e = 0 counts as zero (below fp32's normal range), 255 is NaN
-                                    const uint32_t ea = __byte_perm(j < 4 ? sa.x : sa.y, 0, 0x4440 + (j & 3));
-                                    const uint32_t eb = __byte_perm(j < 4 ? sb.x : sb.y, 0, 0x4440 + (j & 3));
-                                    const float fa = __uint_as_float(ea == 255u ? 0x7fffffffu : ea << 23);
-                                    const float fb = __uint_as_float(eb == 255u ? 0x7fffffffu : eb << 23);
-                                    acc[0] = fmaf(t[0], fa, acc[0]);
-                                    acc[1] = fmaf(t[1], fa, acc[1]);
-                                    acc[2] = fmaf(t[2], fb, acc[2]);
-                                    acc[3] = fmaf(t[3], fb, acc[3]);
-                                }
+                                for (int half = 0; half < 2; ++half)
+                                    mx4_blocks<true>(acc, tile, arow, 0u, sa, sb, gid, c4, half, nb);
+                            } else {
+#pragma unroll
+                                for (int half = 0; half < 2; ++half)
+                                    mx4_blocks<false>(acc, tile, arow, plane, sa, sb, gid, c4, half, nb);
                             }
                         }
                         release();
                     }
                 } else {
-                    // ---- bf16 rows: 64 values of 16 rows per k-block
-                    const uint32_t plane = (uint32_t)(it.ncol * a.stride);
-                    const int lrow = (lane & 7) + ((lane >> 3) & 1) * 8, lpiece = lane >> 4;
-                    const int arow = (lane & 7) < it.ncol ? (lane & 7) : it.ncol - 1;
-                    for (int c = 0; c < nc; ++c) {
-                        if (!(ok = next_stage(c) && segment(c * (two ? 256 : 512)))) break;
-                        const uint32_t tile =
-                            sh.ring + (uint32_t)s * STAGE_BYTES + (uint32_t)(box * BOX_BYTES + sub * 2048 + lrow * 128);
-                        const int kblk = two ? c * 4 + sub : (2 * c + box) * 4 + sub;
-                        if (kblk < it.nkb) {
-                            const uint32_t arow_at =
-                                act + (uint32_t)(arow * a.stride + 2 * (kblk * 64 - cur_seg * a.kseg) + 16 * (lane >> 3));
+                    // ---- bf16 rows: 64 values of 16 rows per k-block, two chains of sums
+                    const int lrow = (lane & 7) + ((lane >> 3) & 1) * 8;
+                    const uint32_t mycol = column(lane & 7) + 16u * (lane >> 3);
+                    const uint32_t wrow = (uint32_t)(box * BOX_BYTES + sub * 2048 + lrow * 128);
+                    uint32_t piece[4];
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                uint32_t w0[4], w1[4], b[4];
-                                ldmatrix_x4(w0, tile + (uint32_t)(((4 * h + lpiece) ^ (lrow & 7)) << 4));
-                                ldmatrix_x4(w1, tile + (uint32_t)(((4 * h + 2 + lpiece) ^ (lrow & 7)) << 4));
-                                ldmatrix_x4(b, arow_at + 64u * h);
-                                mma_bf16(acc, w0, b[0], b[1]);
-                                mma_bf16(acc, w1, b[2], b[3]);
-                                if (a.planes == 2) {
-                                    ldmatrix_x4(b, arow_at + plane + 64u * h);
-                                    mma_bf16(acc, w0, b[0], b[1]);
-                                    mma_bf16(acc, w1, b[2], b[3]);
-                                }
+                    for (int i = 0; i < 4; ++i) piece[i] = wrow + (uint32_t)(((2 * i + (lane >> 4)) ^ (lrow & 7)) << 4);
+                    const bool lo_too = a.planes == 2 && !packed;
+                    float acc2[4] = {0.f, 0.f, 0.f, 0.f};
+                    for (int c = 0; c < nc; ++c) {
+                        if (!(ok = stage_ready(c, c * (two ? 256 : 512)))) break;
+                        const uint32_t tile = sh.ring + (uint32_t)s * STAGE_BYTES;
+                        const int kblk = two ? c * 4 + sub : (2 * c + box) * 4 + sub;
+                        if (kblk < nkb) {
+                            const uint32_t arow = act + mycol + (uint32_t)(2 * (kblk * 64 - cur_seg * a.kseg));
+                            uint32_t w[4][4], b0[4], b1[4];
+                            ldmatrix_x4(b0, arow);
+                            ldmatrix_x4(b1, arow + 64u);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) ldmatrix_x4(w[i], tile + piece[i]);
+                            if (lo_too) {
+                                uint32_t c0[4], c1[4];
+                                ldmatrix_x4(c0, arow + plane);
+                                ldmatrix_x4(c1, arow + plane + 64u);
+                                mma_bf16(acc2, w[0], c0[0], c0[1]);
+                                mma_bf16(acc, w[0], b0[0], b0[1]);
+                                mma_bf16(acc2, w[1], c0[2], c0[3]);
+                                mma_bf16(acc, w[1], b0[2], b0[3]);
+                                mma_bf16(acc2, w[2], c1[0], c1[1]);
+                                mma_bf16(acc, w[2], b1[0], b1[1]);
+                                mma_bf16(acc2, w[3], c1[2], c1[3]);
+                                mma_bf16(acc, w[3], b1[2], b1[3]);
+                            } else {
+                                mma_bf16(acc, w[0], b0[0], b0[1]);
+                                mma_bf16(acc2, w[1], b0[2], b0[3]);
+                                mma_bf16(acc, w[2], b1[0], b1[1]);
+                                mma_bf16(acc2, w[3], b1[2], b1[3]);
                             }
                         }
                         release();
                     }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[i] += acc2[i];
                 }
                 if (!ok) break;
                 float2 *r = reinterpret_cast<float2 *>(red + warp * 128 + gid * 8 + 2 * c4);
                 r[0] = make_float2(acc[0], acc[1]);
                 r[32] = make_float2(acc[2], acc[3]);
             }
-            if (!(ok = bar.sync())) break;
 
-            // ---- sums over the warps, and what becomes of them
+            // ---- sums over the warps, and what becomes of them: thread (row, token) of 16 x 8.
+            // What the epilogue reads from global memory is asked for before the barrier.
             const int cell = threadIdx.x & 127, row = cell >> 3, t = cell & 7, grp = threadIdx.x >> 7;
             const bool real = t < it.ncol;
+            const int r = it.out0 + (two && kind != SHARED_GU && kind != ROUTED_GU ? 16 * grp : 0) + row;
+            float add = 0.f;
+            int slot = -1;
+            if (kind == UP) {
+                if (real && grp == 0) {
+                    const float *q = p.part + (int64_t)t * p.d + r;
+                    add = __ldcg(q) + __ldcg(q + (int64_t)p.T * p.d);
+                }
+            } else if (kind == ROUTED_DOWN) {
+                if (real) {
+                    slot = sh.tab[it.ti].slot[t];
+                    add = __ldcg(p.p32 + slot);
+                }
+            } else if (kind == ROUTED_GU) {
+                const unsigned mask = (unsigned)sh.tab[it.ti].mask;
+                if (mask >> t & 1u) slot = sh.tab[it.ti].slot[__popc(mask & ((1u << t) - 1u))];
+            }
             const float back = mx4 && real ? sh.inv[8 * (set & 1) + t] : 1.f;
-            if (it.kind == SHARED_GU || it.kind == ROUTED_GU) {
+            if (!(ok = bar.sync())) break;
+            auto sum = [&](int w0, int nw) { return red_sum(red, w0, nw, cell, packed) * back; };
+            if (kind == SHARED_GU || kind == ROUTED_GU) {
                 if (grp == 0) {
-                    const float gv = red_sum(red, 0, 4, cell) * back, uv = red_sum(red, 4, 4, cell) * back;
+                    const float gv = sum(0, 4), uv = sum(4, 4);
                     const float h = glu_act(p.act, gv, uv, p.gate_cap, p.up_cap);
-                    if (it.kind == SHARED_GU) {
-                        if (real) p.hs[(int64_t)t * 2 * p.fs + it.out0 + row] = h;
+                    if (kind == SHARED_GU) {
+                        if (real) p.hs[(int64_t)t * 2 * p.fs + r] = h;
                     } else {
-                        int slot = -1;
-#pragma unroll
-                        for (int i = 0; i < FEW_MAX_T; ++i) {
-                            const int v = sh.tab[it.ti].slot[i];
-                            if (v >= 0 && v / p.k == t) slot = v;
-                        }
-                        if (slot >= 0) p.H[(int64_t)slot * p.f + it.out0 + row] = h;
+                        if (slot >= 0) p.H[(int64_t)slot * p.f + r] = h;
                         if (WT == W_MX4) {
                             float m = slot >= 0 ? fabsf(h) : 0.f;
                             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
@@ -1147,14 +1230,11 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                             if (lane < 8 && slot >= 0) atomicMax(p.ctl + C_AMAX_H + slot, __float_as_uint(m));
                         }
                     }
-                    __syncwarp();
-                    if (lane == 0) red_release(p.ctl + (it.kind == SHARED_GU ? C_HS : C_H), 1u);
                 }
-            } else if (it.kind == DOWN || it.kind == UP) {
+            } else if (kind == DOWN || kind == UP) {
                 if (grp == 0) {
-                    const float v = red_sum(red, 0, 8, cell);
-                    const int r = it.out0 + row;
-                    if (it.kind == DOWN) {
+                    const float v = sum(0, 8);
+                    if (kind == DOWN) {
                         if (real) p.z[(int64_t)t * p.l + r] = v;
                         if (WT == W_MX4) {
                             float m = real ? fabsf(v) : 0.f;
@@ -1162,28 +1242,58 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
                             if (lane < 8 && real) atomicMax(p.ctl + C_AMAX_Z + t, __float_as_uint(m));
                         }
-                        __syncwarp();
-                        if (lane == 0) red_release(p.ctl + C_Z, 1u);
                     } else if (real) {
-                        const float *q = p.part + (int64_t)t * p.d + r;
-                        store_token<WT>(p.y, (int64_t)t * p.d + r, v + (__ldcg(q) + __ldcg(q + (int64_t)p.T * p.d)));
+                        store_token<WT>(p.y, (int64_t)t * p.d + r, v + add);
                     }
                 }
             } else {
-                const float v = red_sum(red, 4 * grp, 4, cell) * back;
-                const int r = it.out0 + 16 * grp + row;
-                if (it.kind == SHARED_DOWN) {
+                const float v = sum(4 * grp, 4);
+                if (kind == SHARED_DOWN) {
                     if (real) p.part[((int64_t)it.ti * p.T + t) * p.d + r] = v;
                 } else if (real) {
-                    const int slot = sh.tab[it.ti].slot[t];
-                    p.ysl[(int64_t)slot * p.l + r] = __ldcg(p.p32 + slot) * v;
+                    p.ysl[(int64_t)slot * p.l + r] = add * v;
                 }
-                __syncwarp();
-                if (lane == 0) red_release(p.ctl + (it.kind == SHARED_DOWN ? C_PART : C_YS), 1u);
             }
+            done();
             par ^= 1;
         }
         if (!ok && lane == 0) give_up(0x8);
+    } else {
+        // ------------------------------------------------------------ signaller
+        // An item is stored once all eight warps have counted it: no warp counts the
+        // next item before every warp has passed that item's barrier, hence counted this one.
+        if (lane == 0) {
+            unsigned counted = 0;
+            bool ok = true;
+            for (int q = 0; ok; ++q) {
+                passed[LOADERS + 1] = q;
+                const long long t0 = clock64();
+                while (*published <= q && ok) {
+                    __nanosleep(20);
+                    if (*abort || clock64() - t0 > 2 * WAIT_LIMIT_CYCLES) ok = false;
+                }
+                __threadfence_block();
+                const int kind = ok ? sh.queue[q % QUEUE].kind : (int)END;
+                if (kind == END) break;
+                if (kind == ROUTE) continue;
+                counted += CONSUMERS;
+                const uint32_t word = smem_u32(sh.flags + 22);
+                const long long t1 = clock64();
+                while (lds_acquire(word) < counted && ok)
+                    if (*abort || clock64() - t1 > 2 * WAIT_LIMIT_CYCLES) ok = false;
+                if (!ok) break;
+                const int at = kind == ROUTER        ? C_ROUTER
+                               : kind == DOWN        ? C_Z
+                               : kind == SHARED_GU   ? C_HS
+                               : kind == ROUTED_GU   ? C_H
+                               : kind == SHARED_DOWN ? C_PART
+                               : kind == ROUTED_DOWN ? C_YS
+                               : kind == COMBINE     ? C_U
+                                                     : C_WORDS;
+                if (at < C_WORDS) red_release(p.ctl + at, 1u);      // (nothing waits for UP)
+            }
+            if (!ok) give_up(0x20);
+        }
     }
 
     __syncthreads();
@@ -1204,7 +1314,7 @@ size_t fixed_smem()
 }
 
 struct FewLayout {
-    size_t ctl, r64, p32, tab, z, hs, H, part, ysl, u, total;
+    size_t ctl, r64, p32, tab, z, hs, H, part, ysl, u, ssq, total;
 };
 
 FewLayout few_layout(const lmoe_config &c, int64_t T)
@@ -1227,6 +1337,7 @@ FewLayout few_layout(const lmoe_config &c, int64_t T)
     L.part = take(8 * (size_t)T * c.d);
     L.ysl = take(4 * S * c.l);
     L.u = take(c.standard ? 0 : 4 * (size_t)T * c.l);
+    L.ssq = take(c.standard ? 0 : 4 * (size_t)T * (c.l / 32));
     L.total = o;
     return L;
 }
@@ -1289,6 +1400,7 @@ cudaError_t few_launch(const lmoe_config &c, const FewMaps &m, bool mx4, const f
     p.ctl = (unsigned *)(ws + L.ctl); p.r64 = (double *)(ws + L.r64); p.p32 = (float *)(ws + L.p32);
     p.tab = (Touched *)(ws + L.tab); p.z = (float *)(ws + L.z); p.hs = (float *)(ws + L.hs); p.H = (float *)(ws + L.H);
     p.part = (float *)(ws + L.part); p.ysl = (float *)(ws + L.ysl); p.u = (float *)(ws + L.u);
+    p.ssq = (float *)(ws + L.ssq);
     p.scales = mx4; p.stall_test = stall_test;
     // Activation slots: the longest row set of any item, up to 58 KB (longer ones
     // come in segments); the rest of shared memory is the weight ring.
