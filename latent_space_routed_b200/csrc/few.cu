@@ -27,11 +27,12 @@
 //
 // Roles (15 warps, one block per SM):
 //   warps 0-7   consumers: products from shared memory, sums over the warps, epilogues
-//   warp 8, 9   producers: TMA copies of 16-row (router: 4-row) tiles into a ring of 16 KB stages;
-//               a stage is two boxes of 8 KB, one per producer (one thread's copies go out one
-//               after another, and one thread alone would not reach HBM's rate).  Items with two
-//               row groups (gate and up, or 32 rows) put one in each box; the others put two
-//               successive K ranges of one row group
+//   warp 8      producer: one thread keeps a ring of 16 KB stages full, one TMA copy each (measured:
+//               one thread issuing 16 KB boxes streams 7.3 TB/s, as 8 KB boxes 6.4 TB/s).  A box is
+//               four 128-byte k-blocks of two groups of 16 rows (gate and up, or 32 rows), eight
+//               k-blocks of 16 rows, or 32 of 4 rows (router)
+//   warp 9      scheduler: takes tickets and describes their items in a queue, at most two items
+//               ahead of the producer (its integer work per item would stall the copies)
 //   warps 10-13 loaders: bring an item's activations from global memory into one of two
 //               shared-memory slots, in the form that the product wants, one set ahead
 //   warp 14     signaller: publishes finished items to the other blocks (the fence before the
@@ -62,9 +63,9 @@ using namespace ptx;
 constexpr int CONSUMERS = 8, LOADERS = 4;
 constexpr int THREADS = 32 * (CONSUMERS + 2 + LOADERS + 1);
 constexpr int CT = 32 * CONSUMERS, LT = 32 * LOADERS;
-constexpr int STAGE_BYTES = 16384, BOX_BYTES = 8192;
-constexpr int SCALE_BOX = 512;                   // 16 rows of 32 scales (1024 values), per box
-constexpr int MAX_STAGES = 12, QUEUE = 32;
+constexpr int STAGE_BYTES = 16384, KBLK_BYTES = 2048;   // a k-block of 16 rows
+constexpr int SCALE_BYTES = 1024;                // 2 x 16 rows of 32 scales (1024 values)
+constexpr int MAX_STAGES = 12, QUEUE = 32, AHEAD = 2;
 constexpr int MAX_E = 1024;
 constexpr int SMEM_MAX = 232448;
 
@@ -76,7 +77,7 @@ enum Ctl { C_STATUS = 0, C_TICKET = 32, C_ROUTER = 64, C_Z = 96, C_ROUTED = 128,
 
 struct Item {
     int kind;
-    int row0, row1;      // rows of the two boxes (one row group: equal)
+    int c1, c2;          // coordinates of the box: row (of its block), and block of rows (two groups)
     int kb0, nkb;        // first k-block (128 bytes of a row) in the matrix, and their number
     int ncol;            // columns of the product in use
     int ti;              // touched-expert index, or half of the shared experts
@@ -283,11 +284,11 @@ struct Shared {
     float *red;              // [2][8 warps][16 rows][8 columns]
     Touched *tab;
     Item *queue;
-    int2 *meta;              // per stage: queue index, chunk
+    int *meta;               // per stage: queue index
     float *inv;              // [2 slots][8]: inverse of the activations' scale
     float *lred;             // loaders' sums [4]
-    // [0] abort, [1] items published, [2] stages issued by A, [4] stages consumed,
-    // [8, 16) scan, items passed: [16, 20) by each loader, [20] by B, [21] by the signaller; [22] items stored (x 8)
+    // [0] abort, [1] items published, [2] stages issued, [4] stages consumed,
+    // [8, 16) scan, items passed: [16, 20) by each loader, [20] by the producer, [21] by the signaller; [22] items stored (x 8)
     int *flags;
 };
 
@@ -298,96 +299,79 @@ struct Counts {
 
 template <int WT> constexpr int k_elems() { return WT == W_F32 ? 32 : 64; }   // values per 128-byte k-block
 
+// n / d for 0 <= n < 2^24 by a reciprocal (the quotient is off by one at most).
+struct Divisor {
+    int d;
+    float inv;
+    __device__ __forceinline__ explicit Divisor(int v) : d(v), inv(1.0f / (float)v) {}
+    __device__ __forceinline__ int div(int n) const
+    {
+        int q = (int)((float)n * inv);
+        q -= q * d > n;
+        q += (q + 1) * d <= n;
+        return q;
+    }
+};
+
 template <int WT>
-__device__ __forceinline__ bool decode(const FewParams &p, const Counts &n, const Touched *tab, unsigned tk, Item *it)
-{
-    constexpr int KE = k_elems<WT>();
-    int i = (int)tk;
-    it->ti = 0;
-    it->kb0 = 0;
-    it->ncol = p.T;
-    it->row1 = it->row0 = it->out0 = 0;
-    it->nkb = 0;
-    if (i < n.router) {
-        it->kind = ROUTER; it->row0 = it->row1 = it->out0 = 4 * i; it->nkb = p.d / 32;
-        return true;
+struct Decoder {
+    static constexpr int KE = k_elems<WT>();
+    Divisor gu, sd, rd;      // items of one expert: routed gate/up, shared down, routed down
+    __device__ __forceinline__ explicit Decoder(const FewParams &p) : gu(p.f / 16), sd(p.d / 32), rd(p.l / 32) {}
+
+    // The item of ticket `tk`; kind END past the last.
+    __device__ __forceinline__ Item operator()(const FewParams &p, const Counts &n, const Touched *tab, unsigned tk) const
+    {
+        Item it = {END, 0, 0, 0, 0, p.T, 0, 0};
+        int i = (int)tk;
+        if (i < n.router) {
+            it.kind = ROUTER; it.c1 = it.out0 = 4 * i; it.nkb = p.d / 32;
+        } else if ((i -= n.router) < n.down) {
+            it.kind = DOWN; it.c1 = it.out0 = 16 * i; it.nkb = p.d / KE;
+        } else if ((i -= n.down) < 1) {
+            it.kind = ROUTE;
+        } else if ((i -= 1) < n.shared_gu) {      // gate and up rows interleaved in blocks of 64
+            it.kind = SHARED_GU; it.out0 = 16 * i; it.nkb = p.d / KE;
+            it.c1 = 16 * (i & 3); it.c2 = 2 * (i >> 2);
+        } else if ((i -= n.shared_gu) < n.routed_gu) {
+            it.kind = ROUTED_GU; it.ti = gu.div(i);
+            const int j = i - it.ti * gu.d;
+            it.out0 = 16 * j;
+            it.nkb = WT == W_MX4 ? (p.l + 255) / 256 : p.l / KE;
+            it.c1 = 16 * (j & 3); it.c2 = tab[it.ti].expert * (p.f / 32) + 2 * (j >> 2);
+        } else if ((i -= n.routed_gu) < n.shared_down) {
+            it.kind = SHARED_DOWN; it.ti = i >= sd.d;
+            it.out0 = 32 * (i - it.ti * sd.d); it.c2 = it.out0 / 16;
+            it.nkb = p.fs / KE; it.kb0 = it.ti * it.nkb;
+        } else if ((i -= n.shared_down) < n.routed_down) {
+            it.kind = ROUTED_DOWN; it.ti = rd.div(i);
+            it.out0 = 32 * (i - it.ti * rd.d);
+            it.c2 = (tab[it.ti].expert * p.l + it.out0) / 16;
+            it.nkb = WT == W_MX4 ? (p.f + 255) / 256 : p.f / KE;
+            it.ncol = __popc((unsigned)tab[it.ti].mask);
+        } else if ((i -= n.routed_down) < n.combine) {
+            it.kind = COMBINE; it.out0 = 32 * i;
+        } else if ((i -= n.combine) < n.up) {
+            it.kind = UP; it.c1 = it.out0 = 16 * i; it.nkb = p.l / KE; it.kb0 = 2 * p.fs / KE;
+        }
+        return it;
     }
-    i -= n.router;
-    if (i < n.down) {
-        it->kind = DOWN; it->row0 = it->row1 = it->out0 = 16 * i; it->nkb = p.d / KE;
-        return true;
-    }
-    i -= n.down;
-    if (i < 1) {
-        it->kind = ROUTE;
-        return true;
-    }
-    i -= 1;
-    if (i < n.shared_gu) {      // gate and up rows interleaved in blocks of 64
-        it->kind = SHARED_GU; it->out0 = 16 * i; it->nkb = p.d / KE;
-        it->row0 = 128 * (i / 4) + 16 * (i % 4); it->row1 = it->row0 + 64;
-        return true;
-    }
-    i -= n.shared_gu;
-    if (i < n.routed_gu) {
-        const int per = p.f / 16, j = i % per;
-        it->kind = ROUTED_GU; it->ti = i / per; it->out0 = 16 * j;
-        it->nkb = WT == W_MX4 ? (p.l + 255) / 256 : p.l / KE;
-        it->row0 = tab[it->ti].expert * 2 * p.f + 128 * (j / 4) + 16 * (j % 4); it->row1 = it->row0 + 64;
-        return true;
-    }
-    i -= n.routed_gu;
-    if (i < n.shared_down) {
-        const int per = p.d / 32;
-        it->kind = SHARED_DOWN; it->ti = i / per; it->row0 = it->out0 = 32 * (i % per); it->row1 = it->row0 + 16;
-        it->nkb = p.fs / KE; it->kb0 = it->ti * it->nkb;
-        return true;
-    }
-    i -= n.shared_down;
-    if (i < n.routed_down) {
-        const int per = p.l / 32;
-        it->kind = ROUTED_DOWN; it->ti = i / per; it->out0 = 32 * (i % per);
-        it->row0 = tab[it->ti].expert * p.l + it->out0; it->row1 = it->row0 + 16;
-        it->nkb = WT == W_MX4 ? (p.f + 255) / 256 : p.f / KE;
-        it->ncol = __popc((unsigned)tab[it->ti].mask);
-        return true;
-    }
-    i -= n.routed_down;
-    if (i < n.combine) {
-        it->kind = COMBINE; it->out0 = 32 * i;
-        return true;
-    }
-    i -= n.combine;
-    if (i < n.up) {
-        it->kind = UP; it->row0 = it->row1 = it->out0 = 16 * i; it->nkb = p.l / KE; it->kb0 = 2 * p.fs / KE;
-        return true;
-    }
-    it->kind = END;
-    return false;
-}
+};
 
 __device__ __forceinline__ bool weightless(int kind) { return kind == ROUTE || kind == COMBINE || kind == END; }
 __device__ __forceinline__ bool two_groups(int kind)
 {
     return kind == SHARED_GU || kind == ROUTED_GU || kind == SHARED_DOWN || kind == ROUTED_DOWN;
 }
-// k-blocks per box
-__device__ __forceinline__ int box_kb(int kind) { return kind == ROUTER ? 16 : 4; }
+// k-blocks per stage: 4, 8 or 32
+__device__ __forceinline__ int stage_kb_log2(int kind) { return kind == ROUTER ? 5 : two_groups(kind) ? 2 : 3; }
 __device__ __forceinline__ int chunks(const Item &it)
 {
-    const int per = box_kb(it.kind) * (two_groups(it.kind) ? 1 : 2);
-    return weightless(it.kind) ? 1 : (it.nkb + per - 1) / per;
+    const int sh = stage_kb_log2(it.kind);
+    return weightless(it.kind) ? 1 : (it.nkb + (1 << sh) - 1) >> sh;
 }
 
 // ------------------------------------------------------------------ consumers
-struct Consumer {
-    int warp, lane, s;
-    uint32_t ph;
-    int set;                 // activation sets taken so far - 1
-    int cur_key, cur_seg;
-    int parity;              // reduction buffer
-};
-
 // Sum of the warps' partial products: thread (row, column) of 16 x 8, warps [w0, w0 + n).
 // `packed`: the lo terms' sums are four columns further.
 __device__ __forceinline__ float red_sum(const float *red, int w0, int n, int cell, bool packed)
@@ -439,6 +423,20 @@ __device__ __forceinline__ void mx4_blocks(float (&acc)[4], uint32_t tile, uint3
             acc[2] = fmaf(t[2], fb, acc[2]);
             acc[3] = fmaf(t[3], fb, acc[3]);
         }
+}
+
+// Wait until item q is in the queue.
+__device__ __forceinline__ bool wait_published(volatile int *published, int q, volatile int *abort)
+{
+    if (*published <= q) {
+        const long long t0 = clock64();
+        while (*published <= q) {
+            __nanosleep(20);
+            if (*abort || clock64() - t0 > 2 * WAIT_LIMIT_CYCLES) return false;
+        }
+    }
+    __threadfence_block();
+    return true;
 }
 
 template <int WT>
@@ -608,13 +606,13 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
     Shared sh;
     uint32_t o = 0;
     sh.ring = base; o += (uint32_t)p.stages * STAGE_BYTES;
-    sh.scales = base + o; o += p.scales ? (uint32_t)p.stages * 2 * SCALE_BOX : 0u;
+    sh.scales = base + o; o += p.scales ? (uint32_t)p.stages * SCALE_BYTES : 0u;
     sh.act = base + o; o += 2u * (uint32_t)p.slot_bytes;
     sh.red = reinterpret_cast<float *>(g + o); o += 2 * 8 * 128 * 4;
     sh.tab = reinterpret_cast<Touched *>(g + o); o += sizeof(Touched) * FEW_MAX_SLOTS;
     sh.queue = reinterpret_cast<Item *>(g + o); o += sizeof(Item) * QUEUE;
     uint64_t *bars = reinterpret_cast<uint64_t *>(g + o); o += 8 * (2 * MAX_STAGES + 6);
-    sh.meta = reinterpret_cast<int2 *>(g + o); o += sizeof(int2) * MAX_STAGES;
+    sh.meta = reinterpret_cast<int *>(g + o); o += sizeof(int) * MAX_STAGES;
     sh.inv = reinterpret_cast<float *>(g + o); o += 64;
     sh.lred = reinterpret_cast<float *>(g + o); o += 64;
     sh.flags = reinterpret_cast<int *>(g + o);
@@ -625,7 +623,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
     sh.cons = sh.act_empty + 16u;
     sh.load = sh.cons + 8u;
     volatile int *abort = sh.flags;
-    volatile int *published = sh.flags + 1, *issued_a = sh.flags + 2, *passed = sh.flags + 16;
+    volatile int *published = sh.flags + 1, *passed = sh.flags + 16;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = p.stages;
@@ -665,15 +663,59 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
     };
 
     if (warp == CONSUMERS) {
-        // ------------------------------------------------------------ producer A: tickets, box 0
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            int s = 0, issued = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int q = 0; ok; ++q) {
+                passed[LOADERS] = q;
+                if (!(ok = wait_published(published, q, abort))) break;
+                const Item it = sh.queue[q % QUEUE];
+                const int nc = chunks(it), kb = 1 << stage_kb_log2(it.kind);
+                const bool light = weightless(it.kind), two = two_groups(it.kind);
+                const bool mx4 = WT == W_MX4 && (it.kind == ROUTED_GU || it.kind == ROUTED_DOWN);
+                const uint32_t bytes = STAGE_BYTES + (mx4 ? SCALE_BYTES : 0);
+                const CUtensorMap *map = it.kind == ROUTER        ? &maps.router
+                                         : it.kind == DOWN        ? &maps.down
+                                         : it.kind == SHARED_GU   ? &maps.shared_gu
+                                         : it.kind == ROUTED_GU   ? &maps.routed_gu
+                                         : it.kind == SHARED_DOWN ? &maps.shared_down
+                                         : it.kind == ROUTED_DOWN ? &maps.routed_down
+                                                                  : &maps.up;
+                const CUtensorMap *smap = it.kind == ROUTED_GU ? &maps.routed_gu_scales : &maps.routed_down_scales;
+                for (int c = 0; c < nc; ++c) {
+                    const uint32_t fb = sh.full + 8u * s;
+                    if (!(ok = mbar_wait(sh.empty + 8u * s, ph ^ 1u, abort))) break;
+                    sh.meta[s] = q;
+                    if (light) {
+                        mbar_arrive(fb);
+                    } else {
+                        mbar_expect_tx(fb, bytes);
+                        const uint32_t dst = sh.ring + (uint32_t)s * STAGE_BYTES;
+                        if (two) tma_load_4d(dst, map, fb, it.c1, it.c2, it.kb0 + c * kb);
+                        else tma_load_3d(dst, map, fb, it.c1, it.kb0 + c * kb);
+                        if (mx4) tma_load_3d_at(sh.scales + (uint32_t)s * SCALE_BYTES, smap, fb, 32 * c, it.c1, it.c2);
+                    }
+                    sh.flags[2] = ++issued;
+                    if (++s == S) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (it.kind == END) break;
+            }
+            if (!ok) give_up(0x1);
+        }
+    } else if (warp == CONSUMERS + 1) {
+        // ------------------------------------------------------------ scheduler
+        const Decoder<WT> item(p);
         unsigned next = 0;
         if (lane == 0) next = atomicAdd(p.ctl + C_TICKET, 1u);
         const unsigned fixed = (unsigned)(n.router + n.down + 1 + n.shared_gu);   // tickets that need no selection
-        int q = 0, s = 0, issued = 0;
-        uint32_t ph = 0;
-        bool ok = true;
-        while (ok) {
+        for (int q = 0;; ++q) {
             const unsigned tk = __shfl_sync(0xffffffffu, next, 0);
+            int good = 1;
             if (tk >= fixed && n.touched == 0) {
                 int touched = 0;
                 if (lane == 0) touched = wait_count(p.ctl, C_ROUTED, 1u, abort) ? (int)ld_acquire(p.ctl + C_ROUTED) : 0;
@@ -690,111 +732,26 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 __threadfence_block();
                 __syncwarp();
             }
-            Item it;
-            const bool more = decode<WT>(p, n, sh.tab, tk, &it);
+            const Item it = item(p, n, sh.tab, tk);
             if (lane == 0) {
-                if (more) next = atomicAdd(p.ctl + C_TICKET, 1u);   // used in the next round
-                // the entry's previous item must be behind every reader (rarely a wait)
+                if (it.kind != END) next = atomicAdd(p.ctl + C_TICKET, 1u);   // used in the next round
+                // not far ahead of the producer, and the entry's previous item behind every reader
                 const long long t0 = clock64();
-                for (int r = 0; r < LOADERS + 2 && ok; ++r)
-                    while (q - passed[r] >= QUEUE && ok)
-                        if (*abort || clock64() - t0 > WAIT_LIMIT_CYCLES) ok = false;
-                if (!ok) give_up(0x1);
-                sh.queue[q % QUEUE] = it;
-                __threadfence_block();
-                *published = q + 1;
-                const int nc = chunks(it), kb = box_kb(it.kind);
-                const bool two = two_groups(it.kind), light = weightless(it.kind);
-                const bool mx4 = WT == W_MX4 && (it.kind == ROUTED_GU || it.kind == ROUTED_DOWN);
-                const CUtensorMap *map = it.kind == ROUTER      ? &maps.router
-                                         : it.kind == DOWN      ? &maps.down
-                                         : it.kind == SHARED_GU ? &maps.shared_gu
-                                         : it.kind == ROUTED_GU ? &maps.routed_gu
-                                         : it.kind == ROUTED_DOWN ? &maps.routed_down
-                                                                  : &maps.cat;
-                for (int c = 0; c < nc && ok; ++c) {
-                    if (!mbar_wait(sh.empty + 8u * s, ph ^ 1u, abort)) {
-                        give_up(0x1);
-                        ok = false;
-                        break;
-                    }
-                    sh.meta[s] = make_int2(q, c);
-                    const uint32_t fb = sh.full + 8u * s;
-                    if (light) {
-                        mbar_arrive(fb);
-                    } else {
-                        const int kb0 = two ? c * kb : 2 * c * kb;
-                        const bool second = two || kb0 + kb < it.nkb;
-                        mbar_expect_tx(fb, (uint32_t)((BOX_BYTES + (mx4 ? SCALE_BOX : 0)) * (second ? 2 : 1)));
-                        tma_load_3d(sh.ring + (uint32_t)s * STAGE_BYTES, map, fb, it.row0, it.kb0 + kb0);
-                        if (mx4)
-                            tma_load_2d(sh.scales + (uint32_t)s * 2 * SCALE_BOX,
-                                        it.kind == ROUTED_GU ? &maps.routed_gu_scales : &maps.routed_down_scales, fb,
-                                        32 * c, it.row0);
-                    }
-                    *issued_a = ++issued;
-                    if (++s == S) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
-                }
-            }
-            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-            ++q;
-            if (!more) break;
-        }
-    } else if (warp == CONSUMERS + 1) {
-        // ------------------------------------------------------------ producer B: box 1
-        if (lane == 0) {
-            // Box 1 of a stage follows producer A's box 0: A has waited for the slot, and
-            // A's expected bytes keep the consumers from releasing it without this box.
-            int s = 0, stage = 0;
-            bool ok = true;
-            for (int q = 0; ok; ++q) {
-                passed[LOADERS] = q;
-                const long long t0 = clock64();
-                while (*published <= q && ok) {
-                    __nanosleep(20);
-                    if (*abort || clock64() - t0 > 2 * WAIT_LIMIT_CYCLES) ok = false;
-                }
-                if (!ok) {
-                    give_up(0x2);
-                    break;
-                }
-                __threadfence_block();
-                const Item it = sh.queue[q % QUEUE];
-                if (it.kind == END) break;
-                const int nc = chunks(it), kb = box_kb(it.kind);
-                const bool two = two_groups(it.kind), light = weightless(it.kind);
-                const bool mx4 = WT == W_MX4 && (it.kind == ROUTED_GU || it.kind == ROUTED_DOWN);
-                const CUtensorMap *map = it.kind == ROUTER      ? &maps.router
-                                         : it.kind == DOWN      ? &maps.down
-                                         : it.kind == SHARED_GU ? &maps.shared_gu
-                                         : it.kind == ROUTED_GU ? &maps.routed_gu
-                                         : it.kind == ROUTED_DOWN ? &maps.routed_down
-                                                                  : &maps.cat;
-                for (int c = 0; c < nc && ok; ++c, ++stage) {
-                    const long long t1 = clock64();
-                    while (*issued_a <= stage && ok) {
+                for (int r = 0; r < LOADERS + 2 && good; ++r)
+                    while (q - passed[r] >= (r == LOADERS ? AHEAD : QUEUE) && good) {
                         __nanosleep(20);
-                        if (*abort || clock64() - t1 > WAIT_LIMIT_CYCLES) ok = false;
+                        if (*abort || clock64() - t0 > 2 * WAIT_LIMIT_CYCLES) good = 0;
                     }
-                    if (!ok) {
-                        give_up(0x2);
-                        break;
-                    }
-                    const int kb0 = two ? c * kb : (2 * c + 1) * kb;
-                    if (!light && kb0 < it.nkb) {
-                        const uint32_t fb = sh.full + 8u * s;
-                        tma_load_3d(sh.ring + (uint32_t)s * STAGE_BYTES + BOX_BYTES, map, fb, it.row1, it.kb0 + kb0);
-                        if (mx4)
-                            tma_load_2d(sh.scales + (uint32_t)s * 2 * SCALE_BOX + SCALE_BOX,
-                                        it.kind == ROUTED_GU ? &maps.routed_gu_scales : &maps.routed_down_scales, fb,
-                                        32 * c, it.row1);
-                    }
-                    if (++s == S) s = 0;
+                if (good) {
+                    sh.queue[q % QUEUE] = it;
+                    __threadfence_block();
+                    *published = q + 1;
+                } else {
+                    give_up(0x10);
                 }
             }
+            good = __shfl_sync(0xffffffffu, good, 0);
+            if (!good || it.kind == END) break;
         }
     } else if (warp > CONSUMERS + 1 && warp < CONSUMERS + 2 + LOADERS) {
         // ------------------------------------------------------------ loaders
@@ -805,14 +762,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
         for (int q = 0; ok; ++q) {
             int good = 1;
             if (lane == 0) passed[lw] = q;
-            if (lane == 0) {
-                const long long t0 = clock64();
-                while (*published <= q && good) {
-                    __nanosleep(20);
-                    if (*abort || clock64() - t0 > 2 * WAIT_LIMIT_CYCLES) good = 0;
-                }
-                __threadfence_block();
-            }
+            if (lane == 0) good = wait_published(published, q, abort);
             ok = __shfl_sync(0xffffffffu, good, 0) != 0;
             if (!ok) {
                 if (lane == 0) give_up(0x4);
@@ -944,7 +894,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 ok = false;
                 break;
             }
-            const Item it = sh.queue[sh.meta[s].x % QUEUE];
+            const Item it = sh.queue[sh.meta[s] % QUEUE];
             const int kind = it.kind;
             if (kind == END) {
                 release();
@@ -976,6 +926,9 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
             const ActPlan a = act_plan<WT>(p, it);
             const bool two = two_groups(kind);
             const int nc = chunks(it), nkb = it.nkb;
+            // this warp's k-block of a stage and where its 16 rows lie
+            const int mykb = two ? sub : warp, perkb = two ? 4 : 8;
+            const uint32_t mytile = (uint32_t)((two ? 2 * sub + box : warp) * KBLK_BYTES);
             const uint32_t plane = (uint32_t)(it.ncol * a.stride);
             // Four columns or fewer of two terms: hi in columns 0-3, lo in 4-7 of one product
             const bool packed = a.planes == 2 && it.ncol <= 4;
@@ -1006,12 +959,12 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 const int row = lane >> 3, piece = lane & 7;
                 for (int c = 0; c < nc; ++c) {
                     if (!(ok = stage_ready(c, c * 1024))) break;
-                    const uint32_t tile = sh.ring + (uint32_t)s * STAGE_BYTES + (uint32_t)box * BOX_BYTES;
+                    const uint32_t tile = sh.ring + (uint32_t)s * STAGE_BYTES + (uint32_t)(warp * KBLK_BYTES);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int ko = sub * 4 + i, kblk = (2 * c + box) * 16 + ko;
+                        const int kblk = c * 32 + warp * 4 + i;      // 512 bytes each: 4 rows
                         if (kblk >= nkb) break;
-                        const int R = ko * 4 + row;
+                        const int R = i * 4 + row;
                         const uint4 w = lds128(tile + (uint32_t)(R * 128 + ((piece ^ (R & 7)) << 4)));
                         const double w0 = __uint_as_float(w.x), w1 = __uint_as_float(w.y), w2 = __uint_as_float(w.z),
                                      w3 = __uint_as_float(w.w);
@@ -1067,8 +1020,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 const int piece = lane & 7, rq = lane >> 3;
                 for (int c = 0; c < nc; ++c) {
                     if (!(ok = stage_ready(c, c * (two ? 128 : 256)))) break;
-                    const uint32_t tile = sh.ring + (uint32_t)s * STAGE_BYTES + (uint32_t)(box * BOX_BYTES + sub * 2048);
-                    const int kblk = two ? c * 4 + sub : (2 * c + box) * 4 + sub;
+                    const uint32_t tile = sh.ring + (uint32_t)s * STAGE_BYTES + mytile;
+                    const int kblk = c * perkb + mykb;
                     if (kblk < nkb) {
                         const int k = kblk * 32 + 4 * piece - cur_seg * a.kseg;
                         float4 w[4];
@@ -1120,12 +1073,11 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                     const uint32_t mycol = column(gid) + 16u * c4;
                     for (int c = 0; c < nc; ++c) {
                         if (!(ok = stage_ready(c, c * 1024))) break;
-                        const uint32_t tile =
-                            sh.ring + (uint32_t)s * STAGE_BYTES + (uint32_t)(box * BOX_BYTES + sub * 2048) + 128u * gid;
+                        const uint32_t tile = sh.ring + (uint32_t)s * STAGE_BYTES + mytile + 128u * gid;
                         const int kblk = c * 4 + sub;
                         const int nb = min(nblk - kblk * 8, 8);
                         if (nb > 0) {
-                            const uint32_t sc = sh.scales + (uint32_t)(s * 2 * SCALE_BOX + box * SCALE_BOX + 32 * gid + 8 * sub);
+                            const uint32_t sc = sh.scales + (uint32_t)(s * SCALE_BYTES + box * (SCALE_BYTES / 2) + 32 * gid + 8 * sub);
                             const uint2 sa = lds64(sc), sb = lds64(sc + 8 * 32);
                             const uint32_t arow = act + mycol + (uint32_t)(2 * (kblk * 256 - cur_seg * a.kseg));
                             if (packed) {
@@ -1144,7 +1096,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                     // ---- bf16 rows: 64 values of 16 rows per k-block, two chains of sums
                     const int lrow = (lane & 7) + ((lane >> 3) & 1) * 8;
                     const uint32_t mycol = column(lane & 7) + 16u * (lane >> 3);
-                    const uint32_t wrow = (uint32_t)(box * BOX_BYTES + sub * 2048 + lrow * 128);
+                    const uint32_t wrow = mytile + (uint32_t)(lrow * 128);
                     uint32_t piece[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) piece[i] = wrow + (uint32_t)(((2 * i + (lane >> 4)) ^ (lrow & 7)) << 4);
@@ -1153,7 +1105,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                     for (int c = 0; c < nc; ++c) {
                         if (!(ok = stage_ready(c, c * (two ? 256 : 512)))) break;
                         const uint32_t tile = sh.ring + (uint32_t)s * STAGE_BYTES;
-                        const int kblk = two ? c * 4 + sub : (2 * c + box) * 4 + sub;
+                        const int kblk = c * perkb + mykb;
                         if (kblk < nkb) {
                             const uint32_t arow = act + mycol + (uint32_t)(2 * (kblk * 64 - cur_seg * a.kseg));
                             uint32_t w[4][4], b0[4], b1[4];
@@ -1267,20 +1219,17 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
             bool ok = true;
             for (int q = 0; ok; ++q) {
                 passed[LOADERS + 1] = q;
-                const long long t0 = clock64();
-                while (*published <= q && ok) {
-                    __nanosleep(20);
-                    if (*abort || clock64() - t0 > 2 * WAIT_LIMIT_CYCLES) ok = false;
-                }
-                __threadfence_block();
-                const int kind = ok ? sh.queue[q % QUEUE].kind : (int)END;
+                if (!(ok = wait_published(published, q, abort))) break;
+                const int kind = sh.queue[q % QUEUE].kind;
                 if (kind == END) break;
                 if (kind == ROUTE) continue;
                 counted += CONSUMERS;
                 const uint32_t word = smem_u32(sh.flags + 22);
                 const long long t1 = clock64();
-                while (lds_acquire(word) < counted && ok)
+                while (lds_acquire(word) < counted && ok) {
+                    __nanosleep(20);
                     if (*abort || clock64() - t1 > 2 * WAIT_LIMIT_CYCLES) ok = false;
+                }
                 if (!ok) break;
                 const int at = kind == ROUTER        ? C_ROUTER
                                : kind == DOWN        ? C_Z
@@ -1310,7 +1259,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
 size_t fixed_smem()
 {
     return 1024 + 2 * 8 * 128 * 4 + sizeof(Touched) * FEW_MAX_SLOTS + sizeof(Item) * QUEUE + 8 * (2 * MAX_STAGES + 6) +
-           sizeof(int2) * MAX_STAGES + 64 + 64 + 128;
+           sizeof(int) * MAX_STAGES + 64 + 64 + 128;
 }
 
 struct FewLayout {
@@ -1360,31 +1309,37 @@ bool few_make_maps(const lmoe_config &c, const FewWeights &w, FewMaps *m)
     const CUtensorMapDataType ty = f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const uint32_t ke = f32 ? 32 : 64;
     const uint64_t eb = f32 ? 4 : 2;
-    // rows of K values in 128-byte k-blocks: a box is 16 rows of four of them
-    auto rows = [&](CUtensorMap *t, const void *base, uint64_t K, uint64_t nrows) {
-        return tc_encode_map(t, ty, base, ke, nrows, K / ke, K * eb, 128, ke, 16, 4, true);
+    // Rows of K values as 128-byte k-blocks.  One group: a box is eight k-blocks of
+    // 16 rows.  Two groups: rows in blocks of `block` (64: gate and up alternate;
+    // 16: consecutive rows), a box is four k-blocks of 16 rows of two blocks.
+    auto one = [&](CUtensorMap *t, const void *base, uint64_t K, uint64_t nrows) {
+        return tc_encode_map(t, ty, base, 3, {ke, nrows, K / ke}, {K * eb, 128}, {ke, 16, 8}, true);
     };
-    auto codes = [&](CUtensorMap *t, const void *base, uint64_t K, uint64_t nrows) {
-        return tc_encode_map(t, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, 128, nrows, (K / 2 + 127) / 128, K / 2, 128, 128, 16, 4,
-                             true);
+    auto two = [&](CUtensorMap *t, const void *base, uint64_t K, uint64_t nrows, uint64_t block) {
+        return tc_encode_map(t, ty, base, 4, {ke, block, nrows / block, K / ke}, {K * eb, K * eb * block, 128},
+                             {ke, 16, 2, 4}, true);
     };
-    auto scales = [&](CUtensorMap *t, const void *base, uint64_t K, uint64_t nrows) {
+    auto codes = [&](CUtensorMap *t, const void *base, uint64_t K, uint64_t nrows, uint64_t block) {
+        return tc_encode_map(t, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, 4, {128, block, nrows / block, (K / 2 + 127) / 128},
+                             {K / 2, K / 2 * block, 128}, {128, 16, 2, 4}, true);
+    };
+    auto scales = [&](CUtensorMap *t, const void *base, uint64_t K, uint64_t nrows, uint64_t block) {
         const uint64_t pitch = (uint64_t)mx4_scale_pitch((int64_t)K);
-        return tc_encode_map(t, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, pitch, nrows, 0, pitch, 0, 32, 16, 0, false);
+        return tc_encode_map(t, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, 3, {pitch, block, nrows / block},
+                             {pitch, pitch * block}, {32, 16, 2}, false);
     };
-    const uint64_t E = (uint64_t)c.E, fs = (uint64_t)c.f_shared, cat = 2 * fs + (c.standard ? 0 : (uint64_t)c.l);
+    const uint64_t E = (uint64_t)c.E, d = (uint64_t)c.d, l = (uint64_t)c.l, f = (uint64_t)c.f, fs = (uint64_t)c.f_shared;
+    const uint64_t cat = 2 * fs + (c.standard ? 0 : l);
     *m = FewMaps{};
-    bool ok = tc_encode_map(&m->router, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, w.Wr, 32, E, (uint64_t)c.d / 32, (uint64_t)c.d * 4,
-                            128, 32, 4, 16, true) &&
-              (c.standard || rows(&m->down, w.Wdown, (uint64_t)c.d, (uint64_t)c.l)) &&
-              rows(&m->shared_gu, w.Wgu_s, (uint64_t)c.d, 4 * fs) && rows(&m->cat, w.Wcat, cat, (uint64_t)c.d);
+    const bool ok = tc_encode_map(&m->router, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, w.Wr, 3, {32, E, d / 32}, {d * 4, 128},
+                                  {32, 4, 32}, true) &&
+                    (c.standard || (one(&m->down, w.Wdown, d, l) && one(&m->up, w.Wcat, cat, d))) &&
+                    two(&m->shared_gu, w.Wgu_s, d, 4 * fs, 64) && two(&m->shared_down, w.Wcat, cat, d, 16);
     if (w.mx4)
-        return ok && codes(&m->routed_gu, w.Wgu, (uint64_t)c.l, E * 2 * c.f) &&
-               codes(&m->routed_down, w.D, (uint64_t)c.f, E * c.l) &&
-               scales(&m->routed_gu_scales, w.Wgu_scales, (uint64_t)c.l, E * 2 * c.f) &&
-               scales(&m->routed_down_scales, w.D_scales, (uint64_t)c.f, E * c.l);
-    return ok && rows(&m->routed_gu, w.Wgu, (uint64_t)c.l, E * 2 * c.f) &&
-           rows(&m->routed_down, w.D, (uint64_t)c.f, E * c.l);
+        return ok && codes(&m->routed_gu, w.Wgu, l, E * 2 * f, 64) && codes(&m->routed_down, w.D, f, E * l, 16) &&
+               scales(&m->routed_gu_scales, w.Wgu_scales, l, E * 2 * f, 64) &&
+               scales(&m->routed_down_scales, w.D_scales, f, E * l, 16);
+    return ok && two(&m->routed_gu, w.Wgu, l, E * 2 * f, 64) && two(&m->routed_down, w.D, f, E * l, 16);
 }
 
 cudaError_t few_launch(const lmoe_config &c, const FewMaps &m, bool mx4, const float *bias, const void *x, int T,
@@ -1414,7 +1369,7 @@ cudaError_t few_launch(const lmoe_config &c, const FewMaps &m, bool mx4, const f
     slot = std::min(slot, 58 * 1024);
     slot = (slot + 1023) / 1024 * 1024;
     p.slot_bytes = slot;
-    const int stage = STAGE_BYTES + (mx4 ? 2 * SCALE_BOX : 0);
+    const int stage = STAGE_BYTES + (mx4 ? SCALE_BYTES : 0);
     p.stages = std::min(MAX_STAGES, (int)((SMEM_MAX - (int)fixed_smem() - 2 * slot) / stage));
     const size_t smem = fixed_smem() + 2 * (size_t)slot + (size_t)p.stages * stage;
     cudaError_t e = cudaMemsetAsync(p.ctl, 0, 4 * C_WORDS, s);

@@ -12,7 +12,7 @@ constexpr int FEW_MAX_SLOTS = 64 * FEW_MAX_T;
 
 // Tensor maps of the weights as the kernel streams them (built once per handle).
 struct FewMaps {
-    CUtensorMap router, down, shared_gu, routed_gu, cat, routed_down, routed_gu_scales, routed_down_scales;
+    CUtensorMap router, down, shared_gu, routed_gu, shared_down, routed_down, up, routed_gu_scales, routed_down_scales;
 };
 
 // Weights of a handle, in its own layouts.

@@ -1433,17 +1433,19 @@ cudaError_t tc_gemm(int mode, const GemmArgs &g, int max_mtiles, int cg, int32_t
 
 int tc_num_sms() { return g_num_sms; }
 
-bool tc_encode_map(CUtensorMap *m, CUtensorMapDataType type, const void *base, uint64_t inner, uint64_t rows,
-                   uint64_t outer, uint64_t row_bytes, uint64_t outer_bytes, uint32_t box_inner, uint32_t box_rows,
-                   uint32_t box_outer, bool swizzle128)
+bool tc_encode_map(CUtensorMap *m, CUtensorMapDataType type, const void *base, int rank, const uint64_t (&dims)[5],
+                   const uint64_t (&strides)[4], const uint32_t (&box)[5], bool swizzle128)
 {
     if (!g_encode) return false;
-    const cuuint64_t dims[3] = {inner, rows, outer};
-    const cuuint64_t strides[2] = {row_bytes, outer_bytes};
-    const cuuint32_t box[3] = {box_inner, box_rows, box_outer};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    return g_encode(m, type, outer ? 3 : 2, const_cast<void *>(base), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE,
+    cuuint64_t d[5], st[4];
+    cuuint32_t b[5], es[5];
+    for (int i = 0; i < 5; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        es[i] = 1;
+        if (i < 4) st[i] = strides[i];
+    }
+    return g_encode(m, type, (cuuint32_t)rank, const_cast<void *>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                     swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

@@ -26,11 +26,10 @@ cudaError_t tc_gemm(int mode, const GemmArgs &g, int max_mtiles, int cg, int32_t
 // Number of SMs of the current device (after tc_check_device).
 int tc_num_sms();
 
-// Tensor map of `rows` rows of `inner` elements, row_bytes apart; with outer > 0
-// a third dimension of that many, outer_bytes apart (the k-blocks of a row).
-bool tc_encode_map(CUtensorMap *m, CUtensorMapDataType type, const void *base, uint64_t inner, uint64_t rows,
-                   uint64_t outer, uint64_t row_bytes, uint64_t outer_bytes, uint32_t box_inner, uint32_t box_rows,
-                   uint32_t box_outer, bool swizzle128);
+// Tensor map of `rank` dimensions, innermost first: sizes in elements, strides
+// of the outer dimensions in bytes, box sizes.
+bool tc_encode_map(CUtensorMap *m, CUtensorMapDataType type, const void *base, int rank, const uint64_t (&dims)[5],
+                   const uint64_t (&strides)[4], const uint32_t (&box)[5], bool swizzle128);
 
 // Failure-detection test hook: the next tensor-core GEMM launch makes its MMA
 // warp wait on a barrier that nothing signals; the bounded wait runs out, the
