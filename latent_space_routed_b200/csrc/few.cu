@@ -8,11 +8,12 @@
 //
 //   router       4 rows of W_r                     -> r = sigmoid(W_r x), in 64 bits
 //   down         16 rows of W_down                 -> z
-//   route        (no weights) top-k, p, the touched experts and their slots
+//   route        (no weights) one token's top-k and p
 //   shared gu    16 gate and 16 up rows            -> shared hidden
 //   routed gu    16 gate and 16 up rows of expert  -> hidden H of each of its slots
-//   shared down  32 rows of one shared expert      -> fp32 partial of y
+//   shared down  32 rows of the first shared expert  -> fp32 partial of y
 //   routed down  32 rows of D of one expert        -> p (D h) of each of its slots
+//   shared down  of the second shared expert (each half streams while the stage before it ends)
 //   combine      (no weights) 32 latent columns    -> u = sum over a token's slots, in slot order
 //   up           16 rows of W_up                   -> y
 //
@@ -65,7 +66,7 @@ constexpr int THREADS = 32 * (CONSUMERS + 2 + LOADERS + 1);
 constexpr int CT = 32 * CONSUMERS, LT = 32 * LOADERS;
 constexpr int STAGE_BYTES = 16384, KBLK_BYTES = 2048;   // a k-block of 16 rows
 constexpr int SCALE_BYTES = 1024;                // 2 x 16 rows of 32 scales (1024 values)
-constexpr int MAX_STAGES = 12, QUEUE = 32, AHEAD = 2;
+constexpr int MAX_STAGES = 12, QUEUE = 32, AHEAD = 3;
 constexpr int MAX_E = 1024;
 constexpr int SMEM_MAX = 232448;
 
@@ -99,9 +100,10 @@ struct FewParams {
     unsigned *ctl;
     double *r64;             // [T, E] biased scores' raw scores
     float *p32;              // [T, k]
-    Touched *tab;
     float *z, *hs, *H, *part, *ysl, *u, *ssq;   // ssq: [T, l / 32] sums of squares of u
     int stages, slot_bytes, scales;
+    const char *wgu, *wd;    // routed weights, and bytes of their rows
+    int64_t gu_row, d_row;
     int stall_test;
 };
 
@@ -283,12 +285,15 @@ struct Shared {
     uint32_t ring, scales, act, full, empty, act_full, act_empty, cons, load;   // shared-memory addresses
     float *red;              // [2][8 warps][16 rows][8 columns]
     Touched *tab;
+    uint32_t *mask;          // [MAX_E], the scheduler's
+    double *rsel;            // [64], of the route items
     Item *queue;
     int *meta;               // per stage: queue index
     float *inv;              // [2 slots][8]: inverse of the activations' scale
     float *lred;             // loaders' sums [4]
     // [0] abort, [1] items published, [2] stages issued, [4] stages consumed,
-    // [8, 16) scan, items passed: [16, 20) by each loader, [20] by the producer, [21] by the signaller; [22] items stored (x 8)
+    // items passed: [16, 20) by each loader, [20] by the producer, [21] by the signaller; [22] items stored (x 8),
+    // [23] touched experts
     int *flags;
 };
 
@@ -328,9 +333,9 @@ struct Decoder {
             it.kind = ROUTER; it.c1 = it.out0 = 4 * i; it.nkb = p.d / 32;
         } else if ((i -= n.router) < n.down) {
             it.kind = DOWN; it.c1 = it.out0 = 16 * i; it.nkb = p.d / KE;
-        } else if ((i -= n.down) < 1) {
-            it.kind = ROUTE;
-        } else if ((i -= 1) < n.shared_gu) {      // gate and up rows interleaved in blocks of 64
+        } else if ((i -= n.down) < p.T) {
+            it.kind = ROUTE; it.ti = i;
+        } else if ((i -= p.T) < n.shared_gu) {      // gate and up rows interleaved in blocks of 64
             it.kind = SHARED_GU; it.out0 = 16 * i; it.nkb = p.d / KE;
             it.c1 = 16 * (i & 3); it.c2 = 2 * (i >> 2);
         } else if ((i -= n.shared_gu) < n.routed_gu) {
@@ -339,17 +344,17 @@ struct Decoder {
             it.out0 = 16 * j;
             it.nkb = WT == W_MX4 ? (p.l + 255) / 256 : p.l / KE;
             it.c1 = 16 * (j & 3); it.c2 = tab[it.ti].expert * (p.f / 32) + 2 * (j >> 2);
-        } else if ((i -= n.routed_gu) < n.shared_down) {
+        } else if ((i -= n.routed_gu) < sd.d || (i >= sd.d + n.routed_down && i < 2 * sd.d + n.routed_down)) {
             it.kind = SHARED_DOWN; it.ti = i >= sd.d;
-            it.out0 = 32 * (i - it.ti * sd.d); it.c2 = it.out0 / 16;
+            it.out0 = 32 * (it.ti ? i - sd.d - n.routed_down : i); it.c2 = it.out0 / 16;
             it.nkb = p.fs / KE; it.kb0 = it.ti * it.nkb;
-        } else if ((i -= n.shared_down) < n.routed_down) {
+        } else if ((i -= sd.d) < n.routed_down) {
             it.kind = ROUTED_DOWN; it.ti = rd.div(i);
             it.out0 = 32 * (i - it.ti * rd.d);
             it.c2 = (tab[it.ti].expert * p.l + it.out0) / 16;
             it.nkb = WT == W_MX4 ? (p.f + 255) / 256 : p.f / KE;
             it.ncol = __popc((unsigned)tab[it.ti].mask);
-        } else if ((i -= n.routed_down) < n.combine) {
+        } else if ((i -= n.routed_down + sd.d) < n.combine) {
             it.kind = COMBINE; it.out0 = 32 * i;
         } else if ((i -= n.combine) < n.up) {
             it.kind = UP; it.c1 = it.out0 = 16 * i; it.nkb = p.l / KE; it.kb0 = 2 * p.fs / KE;
@@ -451,117 +456,106 @@ __device__ __forceinline__ void store_token(void *x, int64_t i, float v)
     else ((bf16 *)x)[i] = __float2bfloat16_rn(v);
 }
 
-// Selection of every token, its weights, and the touched experts in ascending
-// order with their slots.  One warp per token: k rounds of a warp maximum over
-// 64-bit score keys, lowest index first among equals.
+// Selection of one token and its weights, by all consumers: an expert's place is
+// the number of experts ahead of it, counted on the high words of the 64-bit score
+// keys, four per load; the low words and the index decide only between equal high
+// words (rare).  A place below k selects.  The loops stay rolled: few blocks run this
+// once per call, so its instructions come from L2, and an unrolled top-k (32
+// registers of keys per lane) spent 50 us of its 2 us fetching them.
 template <int WT>
-__device__ __noinline__ RoleBarrier route_item(const FewParams &p, float *red, int *scan, RoleBarrier bar, int warp,
-                                               int lane)
+__device__ __noinline__ RoleBarrier route_item(const FewParams &p, int t, uint32_t *hi, double *rsel, RoleBarrier bar,
+                                               int warp, int lane)
+{
+    uint32_t *lo = hi + MAX_E;
+    const int tid = warp * 32 + lane;
+    const double *r = p.r64 + (int64_t)t * p.E;
+    const int E4 = (p.E + 3) & ~3;
+#pragma unroll 1
+    for (int e = tid; e < E4; e += CT) {
+        const unsigned long long key = e < p.E ? key64(__ldcg(r + e) + (double)p.bias[e]) : 0ull;   // real keys > 0
+        hi[e] = (uint32_t)(key >> 32);
+        lo[e] = (uint32_t)key;
+    }
+    if (!bar.sync()) return bar;
+#pragma unroll 1
+    for (int e = tid; e < p.E; e += CT) {
+        const uint32_t mine = hi[e];
+        const uint4 *h4 = reinterpret_cast<const uint4 *>(hi);
+        int ahead = 0, same = 0;
+#pragma unroll 2
+        for (int q = 0; q < E4 / 4; ++q) {
+            const uint4 h = h4[q];
+            ahead += (h.x > mine) + (h.y > mine) + (h.z > mine) + (h.w > mine);
+            same += (h.x == mine) + (h.y == mine) + (h.z == mine) + (h.w == mine);
+        }
+        if (same > 1 && ahead < p.k)
+#pragma unroll 1
+            for (int q = 0; q < p.E; ++q)
+                ahead += hi[q] == mine && (lo[q] > lo[e] || (lo[q] == lo[e] && q < e));
+        if (ahead < p.k) {
+            p.sel[t * p.k + ahead] = e;
+            rsel[ahead] = __ldcg(r + e);
+        }
+    }
+    if (!bar.sync()) return bar;
+    if (warp == 0) {
+        const double r0 = lane < p.k ? rsel[lane] : 0.0, r1 = lane + 32 < p.k ? rsel[lane + 32] : 0.0;
+        double sum = r0 + r1;
+#pragma unroll 1
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#pragma unroll 1
+        for (int j = lane; j < p.k; j += 32) {
+            const float pv = (float)(rsel[j] / sum);
+            p.p32[t * p.k + j] = pv;
+            store_token<WT>(p.p_out, t * p.k + j, pv);
+        }
+    } else if (warp == 1 && WT == W_MX4 && p.standard) {   // the routed experts read x itself: its largest magnitude
+        float m = 0.f;
+#pragma unroll 1
+        for (int c = lane; c < p.d; c += 32) m = fmaxf(m, fabsf(token_value<WT>(p.x, (int64_t)t * p.d + c)));
+#pragma unroll 1
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (lane == 0) p.ctl[C_AMAX_X + t] = __float_as_uint(m);
+    }
+    return bar;
+}
+
+// The touched experts in ascending order with their slots, from the selection of
+// all tokens: every block's scheduler builds its own.  mask [MAX_E]: the tokens that
+// selected an expert; returns the number of touched experts.
+__device__ __noinline__ int touched_experts(const FewParams &p, uint32_t *mask, Touched *tab, int lane)
 {
     constexpr unsigned FULL = 0xffffffffu;
-    uint8_t *slot_of = reinterpret_cast<uint8_t *>(red);       // [8 tokens][MAX_E]: slot + 1
-    const int tid = warp * 32 + lane;
-    for (int i = tid; i < FEW_MAX_T * MAX_E / 4; i += CT) reinterpret_cast<uint32_t *>(slot_of)[i] = 0u;
-    if (!bar.sync()) return bar;
-    if (warp < p.T) {
-        const int t = warp;
-        const double *r = p.r64 + (int64_t)t * p.E;
-        unsigned long long key[MAX_E / 32];
-#pragma unroll
-        for (int j = 0; j < MAX_E / 32; ++j) {
-            const int e = lane + 32 * j;
-            key[j] = e < p.E ? key64(__ldcg(r + e) + (double)p.bias[e]) : 0ull;   // real keys > 0 unless -NaN
+    const int S = p.T * p.k;
+#pragma unroll 1
+    for (int e = lane; e < p.E; e += 32) mask[e] = 0u;
+    __syncwarp();
+#pragma unroll 4
+    for (int i = lane; i < S; i += 32) atomicOr(mask + (__ldcg(p.sel + i) & (MAX_E - 1)), 1u << (i / p.k));
+    __syncwarp();
+    int n = 0;
+#pragma unroll 1
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+        const int e = e0 + lane;
+        const uint32_t m = e < p.E ? mask[e] : 0u;
+        const unsigned b = __ballot_sync(FULL, m != 0u);
+        const int at = n + __popc(b & ((1u << lane) - 1u));
+        if (m) {
+            tab[at].expert = (int16_t)e;
+            tab[at].mask = (int16_t)m;
+            mask[e] = m | (uint32_t)at << 8;
         }
-        unsigned long long best = 0ull;
-        int at = lane;
-        auto rescan = [&]() {
-            best = 0ull;
-            at = MAX_E;
-#pragma unroll
-            for (int j = 0; j < MAX_E / 32; ++j)
-                if (key[j] > best) {
-                    best = key[j];
-                    at = lane + 32 * j;
-                }
-        };
-        rescan();
-        int mine0 = 0, mine1 = 0;
-        for (int i = 0; i < p.k; ++i) {
-            const uint32_t hi = (uint32_t)(best >> 32);
-            const uint32_t mh = __reduce_max_sync(FULL, hi);
-            const uint32_t lo = hi == mh ? (uint32_t)best : 0u;
-            const uint32_t ml = __reduce_max_sync(FULL, lo);
-            const unsigned cand = hi == mh && lo == ml ? (unsigned)at : (unsigned)MAX_E;
-            const int e = (int)__reduce_min_sync(FULL, cand) & (MAX_E - 1);
-            if ((i & 31) == lane) {
-                if (i < 32) mine0 = e;
-                else mine1 = e;
-            }
-            if ((e & 31) == lane) {
-#pragma unroll
-                for (int j = 0; j < MAX_E / 32; ++j)
-                    if (e == lane + 32 * j) key[j] = 0ull;
-                rescan();
-            }
-            if (lane == 0) slot_of[t * MAX_E + e] = (uint8_t)(i + 1);
-        }
-        const double r0 = lane < p.k ? __ldcg(r + mine0) : 0.0, r1 = lane + 32 < p.k ? __ldcg(r + mine1) : 0.0;
-        double sum = r0 + r1;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int j = lane + 32 * h;
-            if (j < p.k) {
-                const float pv = (float)((h ? r1 : r0) / sum);
-                p.sel[t * p.k + j] = h ? mine1 : mine0;
-                p.p32[t * p.k + j] = pv;
-                store_token<WT>(p.p_out, t * p.k + j, pv);
-            }
-        }
-        if (WT == W_MX4 && p.standard) {      // the routed experts read x itself: its largest magnitude
-            float m = 0.f;
-            for (int c = lane; c < p.d; c += 32) m = fmaxf(m, fabsf(token_value<WT>(p.x, (int64_t)t * p.d + c)));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
-            if (lane == 0) p.ctl[C_AMAX_X + t] = __float_as_uint(m);
-        }
+        n += __popc(b);
     }
-    if (!bar.sync()) return bar;
-    // touched experts: thread i takes experts [4 i, 4 i + 4)
-    int mask[4], mine = 0;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        mask[q] = 0;
-        for (int t = 0; t < p.T; ++t) mask[q] |= (slot_of[t * MAX_E + 4 * tid + q] != 0) << t;
-        mine += mask[q] != 0;
+    __syncwarp();
+#pragma unroll 4
+    for (int i = lane; i < S; i += 32) {
+        const uint32_t m = mask[__ldcg(p.sel + i) & (MAX_E - 1)];
+        const int t = i / p.k;
+        tab[m >> 8].slot[__popc(m & 0xffu & ((1u << t) - 1u))] = (int16_t)i;
     }
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(FULL, incl, o);
-        if (lane >= o) incl += v;
-    }
-    if (lane == 31) scan[warp] = incl;
-    if (!bar.sync()) return bar;
-    int at = incl - mine;
-    for (int w = 0; w < warp; ++w) at += scan[w];
-    for (int q = 0; q < 4; ++q)
-        if (mask[q]) {
-            Touched e;
-            e.expert = (int16_t)(4 * tid + q);
-            e.mask = (int16_t)mask[q];
-            int c = 0;
-            for (int t = 0; t < FEW_MAX_T; ++t) e.slot[t] = -1;
-            for (int t = 0; t < p.T; ++t)
-                if (mask[q] >> t & 1) e.slot[c++] = (int16_t)(t * p.k + slot_of[t * MAX_E + 4 * tid + q] - 1);
-            p.tab[at++] = e;
-        }
-    int total = 0;
-    for (int w = 0; w < CONSUMERS; ++w) total += scan[w];
-    if (!bar.sync()) return bar;
-    if (tid == 0) red_release(p.ctl + C_ROUTED, (unsigned)total);   // never 0: T, k >= 1
-    return bar;
+    __syncwarp();
+    return n;
 }
 
 template <int WT>
@@ -610,6 +604,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
     sh.act = base + o; o += 2u * (uint32_t)p.slot_bytes;
     sh.red = reinterpret_cast<float *>(g + o); o += 2 * 8 * 128 * 4;
     sh.tab = reinterpret_cast<Touched *>(g + o); o += sizeof(Touched) * FEW_MAX_SLOTS;
+    sh.mask = reinterpret_cast<uint32_t *>(g + o); o += 4 * MAX_E;
+    sh.rsel = reinterpret_cast<double *>(g + o); o += 8 * 64;
     sh.queue = reinterpret_cast<Item *>(g + o); o += sizeof(Item) * QUEUE;
     uint64_t *bars = reinterpret_cast<uint64_t *>(g + o); o += 8 * (2 * MAX_STAGES + 6);
     sh.meta = reinterpret_cast<int *>(g + o); o += sizeof(int) * MAX_STAGES;
@@ -638,7 +634,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
         }
         mbar_init(sh.cons, CONSUMERS);
         mbar_init(sh.load, LOADERS);
-        for (int i = 0; i < 24; ++i) sh.flags[i] = 0;
+        for (int i = 0; i < 32; ++i) sh.flags[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
@@ -712,27 +708,25 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
         const Decoder<WT> item(p);
         unsigned next = 0;
         if (lane == 0) next = atomicAdd(p.ctl + C_TICKET, 1u);
-        const unsigned fixed = (unsigned)(n.router + n.down + 1 + n.shared_gu);   // tickets that need no selection
+        const unsigned fixed = (unsigned)(n.router + n.down + p.T + n.shared_gu);   // tickets that need no selection
         for (int q = 0;; ++q) {
             const unsigned tk = __shfl_sync(0xffffffffu, next, 0);
             int good = 1;
             if (tk >= fixed && n.touched == 0) {
-                int touched = 0;
-                if (lane == 0) touched = wait_count(p.ctl, C_ROUTED, 1u, abort) ? (int)ld_acquire(p.ctl + C_ROUTED) : 0;
-                touched = __shfl_sync(0xffffffffu, touched, 0);
-                if (touched == 0) {
+                if (lane == 0) good = wait_count(p.ctl, C_ROUTED, (unsigned)p.T, abort);
+                good = __shfl_sync(0xffffffffu, good, 0);
+                if (!good) {
                     if (lane == 0) give_up(0x10);
                     break;
                 }
-                with_touched(touched);
-                const uint32_t *src = reinterpret_cast<const uint32_t *>(p.tab);
-                uint32_t *dst = reinterpret_cast<uint32_t *>(sh.tab);
-                const int words = touched * (int)(sizeof(Touched) / 4);
-                for (int i = lane; i < words; i += 32) dst[i] = __ldcg(src + i);
-                __threadfence_block();
-                __syncwarp();
+                with_touched(touched_experts(p, sh.mask, sh.tab, lane));
+                if (lane == 0) sh.flags[23] = n.touched;
             }
             const Item it = item(p, n, sh.tab, tk);
+            if (lane < 2 && (it.kind == ROUTED_GU || it.kind == ROUTED_DOWN)) {
+                const int64_t row = it.kind == ROUTED_GU ? 64 * (int64_t)(it.c2 + lane) + it.c1 : 16 * (int64_t)(it.c2 + lane);
+                prefetch_l2((it.kind == ROUTED_GU ? p.wgu : p.wd) + row * (it.kind == ROUTED_GU ? p.gu_row : p.d_row));
+            }
             if (lane == 0) {
                 if (it.kind != END) next = atomicAdd(p.ctl + C_TICKET, 1u);   // used in the next round
                 // not far ahead of the producer, and the entry's previous item behind every reader
@@ -786,7 +780,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                         if (it.kind == SHARED_DOWN)
                             good = wait_count(p.ctl, C_HS, n.shared_gu + (p.stall_test ? 1u : 0u), abort);
                         if (it.kind == ROUTED_DOWN)
-                            good = wait_count(p.ctl, C_H, ld_acquire(p.ctl + C_ROUTED) * (p.f / 16), abort);
+                            good = wait_count(p.ctl, C_H, (unsigned)sh.flags[23] * (p.f / 16), abort);
                         if (it.kind == UP)
                             good = wait_count(p.ctl, C_U, n.combine, abort) &&
                                    wait_count(p.ctl, C_PART, n.shared_down, abort);
@@ -906,15 +900,16 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                     if (kind == ROUTE) {
                         good = wait_count(p.ctl, C_ROUTER, (unsigned)n.router, abort);
                     } else {
-                        good = wait_count(p.ctl, C_YS, ld_acquire(p.ctl + C_ROUTED) * (p.l / 32), abort);
+                        good = wait_count(p.ctl, C_YS, (unsigned)sh.flags[23] * (p.l / 32), abort);
                         if (good && p.standard) good = wait_count(p.ctl, C_PART, n.shared_down, abort);
                     }
                 }
                 ok = __shfl_sync(0xffffffffu, good, 0) != 0 && bar.sync();
                 if (!ok) break;
                 if (kind == ROUTE) {
-                    bar = route_item<WT>(p, sh.red, sh.flags + 8, bar, warp, lane);
+                    bar = route_item<WT>(p, it.ti, reinterpret_cast<uint32_t *>(sh.red), sh.rsel, bar, warp, lane);
                     if (!(ok = bar.ok)) break;
+                    done();
                 } else {
                     combine_item<WT>(p, it, warp, lane);
                     done();
@@ -1222,7 +1217,6 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 if (!(ok = wait_published(published, q, abort))) break;
                 const int kind = sh.queue[q % QUEUE].kind;
                 if (kind == END) break;
-                if (kind == ROUTE) continue;
                 counted += CONSUMERS;
                 const uint32_t word = smem_u32(sh.flags + 22);
                 const long long t1 = clock64();
@@ -1232,6 +1226,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 }
                 if (!ok) break;
                 const int at = kind == ROUTER        ? C_ROUTER
+                               : kind == ROUTE       ? C_ROUTED
                                : kind == DOWN        ? C_Z
                                : kind == SHARED_GU   ? C_HS
                                : kind == ROUTED_GU   ? C_H
@@ -1258,12 +1253,12 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
 // ------------------------------------------------------------------ host side
 size_t fixed_smem()
 {
-    return 1024 + 2 * 8 * 128 * 4 + sizeof(Touched) * FEW_MAX_SLOTS + sizeof(Item) * QUEUE + 8 * (2 * MAX_STAGES + 6) +
+    return 1024 + 2 * 8 * 128 * 4 + sizeof(Touched) * FEW_MAX_SLOTS + 4 * MAX_E + 8 * 64 + sizeof(Item) * QUEUE + 8 * (2 * MAX_STAGES + 6) +
            sizeof(int) * MAX_STAGES + 64 + 64 + 128;
 }
 
 struct FewLayout {
-    size_t ctl, r64, p32, tab, z, hs, H, part, ysl, u, ssq, total;
+    size_t ctl, r64, p32, z, hs, H, part, ysl, u, ssq, total;
 };
 
 FewLayout few_layout(const lmoe_config &c, int64_t T)
@@ -1279,7 +1274,6 @@ FewLayout few_layout(const lmoe_config &c, int64_t T)
     L.ctl = take(4 * C_WORDS);
     L.r64 = take(8 * (size_t)T * c.E);
     L.p32 = take(4 * S);
-    L.tab = take(sizeof(Touched) * FEW_MAX_SLOTS);
     L.z = take(c.standard ? 0 : 4 * (size_t)T * c.l);
     L.hs = take(4 * (size_t)T * 2 * c.f_shared);
     L.H = take(4 * S * c.f);
@@ -1342,10 +1336,11 @@ bool few_make_maps(const lmoe_config &c, const FewWeights &w, FewMaps *m)
     return ok && two(&m->routed_gu, w.Wgu, l, E * 2 * f, 64) && two(&m->routed_down, w.D, f, E * l, 16);
 }
 
-cudaError_t few_launch(const lmoe_config &c, const FewMaps &m, bool mx4, const float *bias, const void *x, int T,
+cudaError_t few_launch(const lmoe_config &c, const FewMaps &m, const FewWeights &w, const float *bias, const void *x, int T,
                        void *y, int32_t *sel, void *p_out, void *u_out, void *workspace, bool stall_test,
                        cudaStream_t s)
 {
+    const bool mx4 = w.mx4;
     const FewLayout L = few_layout(c, T);
     char *ws = (char *)workspace;
     FewParams p = {};
@@ -1353,10 +1348,13 @@ cudaError_t few_launch(const lmoe_config &c, const FewMaps &m, bool mx4, const f
     p.standard = c.standard; p.gate_cap = c.gate_cap; p.up_cap = c.up_cap; p.eps = c.eps;
     p.x = x; p.bias = bias; p.y = y; p.p_out = p_out; p.u_out = u_out; p.sel = sel;
     p.ctl = (unsigned *)(ws + L.ctl); p.r64 = (double *)(ws + L.r64); p.p32 = (float *)(ws + L.p32);
-    p.tab = (Touched *)(ws + L.tab); p.z = (float *)(ws + L.z); p.hs = (float *)(ws + L.hs); p.H = (float *)(ws + L.H);
+    p.z = (float *)(ws + L.z); p.hs = (float *)(ws + L.hs); p.H = (float *)(ws + L.H);
     p.part = (float *)(ws + L.part); p.ysl = (float *)(ws + L.ysl); p.u = (float *)(ws + L.u);
     p.ssq = (float *)(ws + L.ssq);
     p.scales = mx4; p.stall_test = stall_test;
+    p.wgu = (const char *)w.Wgu; p.wd = (const char *)w.D;
+    p.gu_row = mx4 ? c.l / 2 : (int64_t)c.l * (c.dtype == LMOE_F32 ? 4 : 2);
+    p.d_row = mx4 ? c.f / 2 : (int64_t)c.f * (c.dtype == LMOE_F32 ? 4 : 2);
     // Activation slots: the longest row set of any item, up to 58 KB (longer ones
     // come in segments); the rest of shared memory is the weight ring.
     const bool f32 = c.dtype == LMOE_F32;

@@ -33,7 +33,7 @@ bool few_make_maps(const lmoe_config &c, const FewWeights &w, FewMaps *m);
 size_t few_workspace_bytes(const lmoe_config &c, int64_t T);
 constexpr size_t FEW_STATUS_OFFSET = 0;
 
-cudaError_t few_launch(const lmoe_config &c, const FewMaps &m, bool mx4, const float *bias, const void *x, int T,
+cudaError_t few_launch(const lmoe_config &c, const FewMaps &m, const FewWeights &w, const float *bias, const void *x, int T,
                        void *y, int32_t *sel, void *p_out, void *u_out, void *workspace, bool stall_test,
                        cudaStream_t s);
 

@@ -112,6 +112,7 @@ struct lmoe_handle {
     uint8_t *Wgu_scales = nullptr;   // [E, 2f, mx4_scale_pitch(l)]
     uint8_t *D_scales = nullptr;     // [E, l, mx4_scale_pitch(f)]
     FewMaps few;                     // few-token layer: tensor maps of the weights above
+    FewWeights few_w;
     bool few_ok = false;
     void *Wgu_s;      // [4 f_s, d] interleaved (both shared experts as one of width 2 f_s)
     void *Wcat;       // [d, 2 f_s + l]
@@ -423,8 +424,8 @@ static lmoe_status create_handle(const lmoe_config *cfg, const lmoe_weights *w, 
     STEP(cudaStreamCreateWithFlags(&h->copy_out, cudaStreamNonBlocking));
     for (cudaEvent_t &e : h->ev_host) STEP(cudaEventCreateWithFlags(&e, cudaEventDisableTiming));
     if (few_ok) {
-        const FewWeights fw = {h->Wr, h->Wdown, h->Wgu_s, h->Wcat, h->Wgu, h->D, h->Wgu_scales, h->D_scales, h->mx4};
-        h->few_ok = few_make_maps(c, fw, &h->few);
+        h->few_w = {h->Wr, h->Wdown, h->Wgu_s, h->Wcat, h->Wgu, h->D, h->Wgu_scales, h->D_scales, h->mx4};
+        h->few_ok = few_make_maps(c, h->few_w, &h->few);
     }
     STEP(cudaStreamSynchronize(s));
 #undef ALLOC
@@ -486,7 +487,7 @@ lmoe_status lmoe_forward_few(lmoe_handle *h, const void *x, int64_t T, void *out
     if (!h->few_ok) return fail(LMOE_ERR_UNSUPPORTED, "the few-token layer needs an sm_100 device");
     const lmoe_status st = check_current_device(h);
     if (st != LMOE_OK) return st;
-    LMOE_CUDA(few_launch(h->cfg, h->few, h->mx4, h->b, x, (int)T, output, selected_experts, mixture_weights,
+    LMOE_CUDA(few_launch(h->cfg, h->few, h->few_w, h->b, x, (int)T, output, selected_experts, mixture_weights,
                          latent_routed_aggregate, workspace, g_stall_few.exchange(0) != 0, (cudaStream_t)stream));
     return LMOE_OK;
 }
