@@ -27,7 +27,11 @@
 // still wait for the activations: HBM does not idle between the stages.
 //
 // Roles (15 warps, one block per SM):
-//   warps 0-7   consumers: products from shared memory, sums over the warps, epilogues
+//   warps 0-7   consumers: products from shared memory, sums over the warps, epilogues.  Two
+//               teams of four warps, each with half of the ring, take the stages in turn: a stage costs a warp 500 to 700 cycles
+//               of latency (barrier, loads, products, release) against 700 of HBM time, and two
+//               stages at once keep the weight stream the only limit (all eight warps on each
+//               stage: 866 us against 712 without products, 8 tokens, d = 7168)
 //   warp 8      producer: one thread keeps a ring of 16 KB stages full, one TMA copy each (measured:
 //               one thread issuing 16 KB boxes streams 7.3 TB/s, as 8 KB boxes 6.4 TB/s).  A box is
 //               four 128-byte k-blocks of two groups of 16 rows (gate and up, or 32 rows), eight
@@ -265,6 +269,13 @@ __device__ __forceinline__ unsigned long long key64(double v)
     return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
 }
 
+// mbar_wait by a whole warp: one answer for all lanes, and the lanes together again,
+// as the warp-wide loads and products that follow need them.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int *abort)
+{
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+}
+
 // Barrier of the warps of one role (an mbarrier with one arrival per warp):
 // bounded, unlike bar.sync, so that a role whose peer gave up still ends.
 struct RoleBarrier {
@@ -275,25 +286,24 @@ struct RoleBarrier {
     {
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-        ok = mbar_wait(bar, parity, abort);
+        ok = warp_wait(bar, parity, abort);
         parity ^= 1u;
         return ok;
     }
 };
 
 struct Shared {
-    uint32_t ring, scales, act, full, empty, act_full, act_empty, cons, load;   // shared-memory addresses
-    float *red;              // [2][8 warps][16 rows][8 columns]
+    uint32_t ring, scales, act, full, empty, act_full, act_empty, cons, load, red_free;   // shared-memory addresses
+    float *red;              // [RED_FLOATS]
     Touched *tab;
     uint32_t *mask;          // [MAX_E], the scheduler's
     double *rsel;            // [64], of the route items
     Item *queue;
-    int *meta;               // per stage: queue index
     float *inv;              // [2 slots][8]: inverse of the activations' scale
     float *lred;             // loaders' sums [4]
-    // [0] abort, [1] items published, [2] stages issued, [4] stages consumed,
-    // items passed: [16, 20) by each loader, [20] by the producer, [21] by the signaller; [22] items stored (x 8),
-    // [23] touched experts
+    // [0] abort, [1] items published, [3] sets of x issued, [26, 28) stages issued to each team; items passed: [16, 20) by each
+    // loader, [20] by the producer, [21] by the signaller, [22] by consumer warp 0;
+    // [24] items stored (x 8), [25] touched experts
     int *flags;
 };
 
@@ -370,48 +380,62 @@ __device__ __forceinline__ bool two_groups(int kind)
 }
 // k-blocks per stage: 4, 8 or 32
 __device__ __forceinline__ int stage_kb_log2(int kind) { return kind == ROUTER ? 5 : two_groups(kind) ? 2 : 3; }
+// Team of an item's first stage (its stages alternate): from the item alone, so that
+// the sums are the same in every run; items of a single stage alternate by their place.
+__device__ __forceinline__ int first_team(int kind, int out0)
+{
+    return (out0 >> (kind == ROUTER ? 2 : kind == SHARED_DOWN || kind == ROUTED_DOWN ? 5 : 4)) & 1;
+}
 __device__ __forceinline__ int chunks(const Item &it)
 {
     const int sh = stage_kb_log2(it.kind);
-    return weightless(it.kind) ? 1 : (it.nkb + (1 << sh) - 1) >> sh;
+    return (it.nkb + (1 << sh) - 1) >> sh;
 }
 
 // ------------------------------------------------------------------ consumers
-// Sum of the warps' partial products: thread (row, column) of 16 x 8, warps [w0, w0 + n).
-// `packed`: the lo terms' sums are four columns further.
-__device__ __forceinline__ float red_sum(const float *red, int w0, int n, int cell, bool packed)
+// Partial products of an item: per warp two groups of 16 rows x 8 columns, the groups
+// RED_GROUP floats apart (16 more than a group, so that both are read without conflicts).
+constexpr int RED_GROUP = 144, RED_WARP = 2 * RED_GROUP, RED_FLOATS = CONSUMERS * RED_WARP;
+// Sum over the warps of one cell; `packed`: the lo terms' sums are four columns further.
+__device__ __forceinline__ float red_sum(const float *cell, bool packed)
 {
     float v = 0.f;
-    for (int w = w0; w < w0 + n; ++w) v += red[w * 128 + cell];
-    if (packed && (cell & 4) == 0)
-        for (int w = w0; w < w0 + n; ++w) v += red[w * 128 + cell + 4];
+#pragma unroll
+    for (int w = 0; w < CONSUMERS; ++w) v += cell[w * RED_WARP];
+    if (packed)
+#pragma unroll
+        for (int w = 0; w < CONSUMERS; ++w) v += cell[w * RED_WARP + 4];
     return v;
 }
 
-// Four blocks of 32 values (half 0 or 1 of a 128-byte k-block) of 16 rows of 4-bit
-// weights against eight columns: acc += scale of the row's block * partial sum.
-template <bool PACKED>
-__device__ __forceinline__ void mx4_blocks(float (&acc)[4], uint32_t tile, uint32_t arow, uint32_t plane, uint2 sa,
-                                           uint2 sb, int gid, int c4, int half, int nb)
+// N blocks of 32 values, from block j0 on, of a 128-byte k-block of two groups of 16
+// rows of 4-bit weights against eight columns: acc += scale of the row's block *
+// partial sum.  No branch inside: the blocks' loads, conversions and products overlap.
+// e[g][h]: the blocks' scales (a byte each) of rows gid + 8 h of group g.
+template <bool PACKED, int N>
+__device__ __forceinline__ void mx4_blocks(float (&acc)[2][4], uint32_t tile, uint32_t arow, uint32_t plane,
+                                           const uint32_t (&e)[2][2], int gid, int c4, int j0)
 {
-    uint32_t a[4], b[4];
-    uint4 h[4], lo[4];
+    uint32_t w[2][2][N];
+    uint4 h[N], lo[N];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (4 * half + j < nb) {
-            const uint32_t off = (uint32_t)((((4 * half + j) ^ gid) << 4) + 4 * c4);
-            a[j] = lds32(tile + off);
-            b[j] = lds32(tile + 1024 + off);
-            h[j] = lds128(arow + 64u * (4 * half + j));
-            if (!PACKED) lo[j] = lds128(arow + plane + 64u * (4 * half + j));
+    for (int j = 0; j < N; ++j) {
+        const uint32_t off = (uint32_t)((((j0 + j) ^ gid) << 4) + 4 * c4);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            w[g][0][j] = lds32(tile + KBLK_BYTES * g + off);
+            w[g][1][j] = lds32(tile + KBLK_BYTES * g + 1024 + off);
         }
-    const uint32_t ea = half ? sa.y : sa.x, eb = half ? sb.y : sb.x;
+        h[j] = lds128(arow + 64u * (j0 + j));
+        if (!PACKED) lo[j] = lds128(arow + plane + 64u * (j0 + j));
+    }
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (4 * half + j < nb) {
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
             uint32_t wa[4], wb[4];
-            e2m1x8_to_f16(wa, a[j]);
-            e2m1x8_to_f16(wb, b[j]);
+            e2m1x8_to_f16(wa, w[g][0][j]);
+            e2m1x8_to_f16(wb, w[g][1][j]);
             float t[4] = {0.f, 0.f, 0.f, 0.f};
             mma_f16(t, wa[0], wb[0], wa[1], wb[1], h[j].x, h[j].y);
             mma_f16(t, wa[2], wb[2], wa[3], wb[3], h[j].z, h[j].w);
@@ -420,14 +444,46 @@ __device__ __forceinline__ void mx4_blocks(float (&acc)[4], uint32_t tile, uint3
                 mma_f16(t, wa[2], wb[2], wa[3], wb[3], lo[j].z, lo[j].w);
             }
             // 2^(e - 127); e = 0 counts as zero (below fp32's normal range), 255 is NaN
-            const uint32_t xa = (ea >> (8 * j)) & 255u, xb = (eb >> (8 * j)) & 255u;
+            const uint32_t xa = (e[g][0] >> (8 * j)) & 255u, xb = (e[g][1] >> (8 * j)) & 255u;
             const float fa = __uint_as_float(xa == 255u ? 0x7fffffffu : xa << 23);
             const float fb = __uint_as_float(xb == 255u ? 0x7fffffffu : xb << 23);
-            acc[0] = fmaf(t[0], fa, acc[0]);
-            acc[1] = fmaf(t[1], fa, acc[1]);
-            acc[2] = fmaf(t[2], fb, acc[2]);
-            acc[3] = fmaf(t[3], fb, acc[3]);
+            acc[g][0] = fmaf(t[0], fa, acc[g][0]);
+            acc[g][1] = fmaf(t[1], fa, acc[g][1]);
+            acc[g][2] = fmaf(t[2], fb, acc[g][2]);
+            acc[g][3] = fmaf(t[3], fb, acc[g][3]);
         }
+}
+// All blocks of a k-block, nb <= 8 of them real.
+template <bool PACKED>
+__device__ __forceinline__ void mx4_kblock(float (&acc)[2][4], uint32_t tile, uint32_t arow, uint32_t plane,
+                                           uint32_t scales, int gid, int c4, int nb)
+{
+    uint2 e[2][2];
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) e[g][h] = lds64(scales + (uint32_t)(512 * g + 256 * h));
+    if (nb == 8) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            uint32_t f[2][2];
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) f[g][h] = (j < 4 ? e[g][h].x : e[g][h].y) >> (8 * (j & 3));
+            mx4_blocks<PACKED, 2>(acc, tile, arow, plane, f, gid, c4, j);
+        }
+    } else {
+#pragma unroll 1
+        for (int j = 0; j < nb; ++j) {
+            uint32_t f[2][2];
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) f[g][h] = (j < 4 ? e[g][h].x : e[g][h].y) >> (8 * (j & 3));
+            mx4_blocks<PACKED, 1>(acc, tile, arow, plane, f, gid, c4, j);
+        }
+    }
 }
 
 // Wait until item q is in the queue.
@@ -602,13 +658,12 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
     sh.ring = base; o += (uint32_t)p.stages * STAGE_BYTES;
     sh.scales = base + o; o += p.scales ? (uint32_t)p.stages * SCALE_BYTES : 0u;
     sh.act = base + o; o += 2u * (uint32_t)p.slot_bytes;
-    sh.red = reinterpret_cast<float *>(g + o); o += 2 * 8 * 128 * 4;
+    sh.red = reinterpret_cast<float *>(g + o); o += 4 * RED_FLOATS;
     sh.tab = reinterpret_cast<Touched *>(g + o); o += sizeof(Touched) * FEW_MAX_SLOTS;
     sh.mask = reinterpret_cast<uint32_t *>(g + o); o += 4 * MAX_E;
     sh.rsel = reinterpret_cast<double *>(g + o); o += 8 * 64;
     sh.queue = reinterpret_cast<Item *>(g + o); o += sizeof(Item) * QUEUE;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(g + o); o += 8 * (2 * MAX_STAGES + 6);
-    sh.meta = reinterpret_cast<int *>(g + o); o += sizeof(int) * MAX_STAGES;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(g + o); o += 8 * (2 * MAX_STAGES + 8);
     sh.inv = reinterpret_cast<float *>(g + o); o += 64;
     sh.lred = reinterpret_cast<float *>(g + o); o += 64;
     sh.flags = reinterpret_cast<int *>(g + o);
@@ -618,15 +673,16 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
     sh.act_empty = sh.act_full + 16u;
     sh.cons = sh.act_empty + 16u;
     sh.load = sh.cons + 8u;
+    sh.red_free = sh.load + 8u;
     volatile int *abort = sh.flags;
     volatile int *published = sh.flags + 1, *passed = sh.flags + 16;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int S = p.stages;
+    const int S = p.stages, half = (S + 1) / 2;      // team 0's slots are [0, half), team 1's [half, S)
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(sh.full + 8u * s, 1);
-            mbar_init(sh.empty + 8u * s, CONSUMERS);
+            mbar_init(sh.empty + 8u * s, CONSUMERS / 2);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(sh.act_full + 8u * s, LOADERS);
@@ -634,6 +690,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
         }
         mbar_init(sh.cons, CONSUMERS);
         mbar_init(sh.load, LOADERS);
+        mbar_init(sh.red_free, CONSUMERS);
         for (int i = 0; i < 32; ++i) sh.flags[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -661,15 +718,17 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
     if (warp == CONSUMERS) {
         // ------------------------------------------------------------ producer
         if (lane == 0) {
-            int s = 0, issued = 0;
-            uint32_t ph = 0;
+            int slot0 = 0, slot1 = half, issued0 = 0, issued1 = 0;     // next slot of each team
+            uint32_t ph0 = 0, ph1 = 0;
             bool ok = true;
             for (int q = 0; ok; ++q) {
                 passed[LOADERS] = q;
                 if (!(ok = wait_published(published, q, abort))) break;
                 const Item it = sh.queue[q % QUEUE];
+                if (it.kind == END) break;
+                if (weightless(it.kind)) continue;
                 const int nc = chunks(it), kb = 1 << stage_kb_log2(it.kind);
-                const bool light = weightless(it.kind), two = two_groups(it.kind);
+                const bool two = two_groups(it.kind);
                 const bool mx4 = WT == W_MX4 && (it.kind == ROUTED_GU || it.kind == ROUTED_DOWN);
                 const uint32_t bytes = STAGE_BYTES + (mx4 ? SCALE_BYTES : 0);
                 const CUtensorMap *map = it.kind == ROUTER        ? &maps.router
@@ -680,26 +739,30 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                                          : it.kind == ROUTED_DOWN ? &maps.routed_down
                                                                   : &maps.up;
                 const CUtensorMap *smap = it.kind == ROUTED_GU ? &maps.routed_gu_scales : &maps.routed_down_scales;
+                const int first = first_team(it.kind, it.out0);
                 for (int c = 0; c < nc; ++c) {
+                    const int team = (c ^ first) & 1, s = team ? slot1 : slot0;
                     const uint32_t fb = sh.full + 8u * s;
-                    if (!(ok = mbar_wait(sh.empty + 8u * s, ph ^ 1u, abort))) break;
-                    sh.meta[s] = q;
-                    if (light) {
-                        mbar_arrive(fb);
+                    if (!(ok = mbar_wait(sh.empty + 8u * s, (team ? ph1 : ph0) ^ 1u, abort))) break;
+                    mbar_expect_tx(fb, bytes);
+                    const uint32_t dst = sh.ring + (uint32_t)s * STAGE_BYTES;
+                    if (two) tma_load_4d(dst, map, fb, it.c1, it.c2, it.kb0 + c * kb);
+                    else tma_load_3d(dst, map, fb, it.c1, it.kb0 + c * kb);
+                    if (mx4) tma_load_3d_at(sh.scales + (uint32_t)s * SCALE_BYTES, smap, fb, 32 * c, it.c1, it.c2);
+                    if (team) {
+                        sh.flags[27] = ++issued1;
+                        if (++slot1 == S) {
+                            slot1 = half;
+                            ph1 ^= 1u;
+                        }
                     } else {
-                        mbar_expect_tx(fb, bytes);
-                        const uint32_t dst = sh.ring + (uint32_t)s * STAGE_BYTES;
-                        if (two) tma_load_4d(dst, map, fb, it.c1, it.c2, it.kb0 + c * kb);
-                        else tma_load_3d(dst, map, fb, it.c1, it.kb0 + c * kb);
-                        if (mx4) tma_load_3d_at(sh.scales + (uint32_t)s * SCALE_BYTES, smap, fb, 32 * c, it.c1, it.c2);
-                    }
-                    sh.flags[2] = ++issued;
-                    if (++s == S) {
-                        s = 0;
-                        ph ^= 1u;
+                        sh.flags[26] = ++issued0;
+                        if (++slot0 == half) {
+                            slot0 = 0;
+                            ph0 ^= 1u;
+                        }
                     }
                 }
-                if (it.kind == END) break;
             }
             if (!ok) give_up(0x1);
         }
@@ -720,7 +783,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                     break;
                 }
                 with_touched(touched_experts(p, sh.mask, sh.tab, lane));
-                if (lane == 0) sh.flags[23] = n.touched;
+                if (lane == 0) sh.flags[25] = n.touched;
             }
             const Item it = item(p, n, sh.tab, tk);
             if (lane < 2 && (it.kind == ROUTED_GU || it.kind == ROUTED_DOWN)) {
@@ -731,8 +794,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 if (it.kind != END) next = atomicAdd(p.ctl + C_TICKET, 1u);   // used in the next round
                 // not far ahead of the producer, and the entry's previous item behind every reader
                 const long long t0 = clock64();
-                for (int r = 0; r < LOADERS + 2 && good; ++r)
-                    while (q - passed[r] >= (r == LOADERS ? AHEAD : QUEUE) && good) {
+                for (int r = 0; r < LOADERS + 3 && good; ++r)
+                    while (q - passed[r] >= (r == LOADERS ? AHEAD : QUEUE - 2) && good) {
                         __nanosleep(20);
                         if (*abort || clock64() - t0 > 2 * WAIT_LIMIT_CYCLES) good = 0;
                     }
@@ -780,7 +843,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                         if (it.kind == SHARED_DOWN)
                             good = wait_count(p.ctl, C_HS, n.shared_gu + (p.stall_test ? 1u : 0u), abort);
                         if (it.kind == ROUTED_DOWN)
-                            good = wait_count(p.ctl, C_H, (unsigned)sh.flags[23] * (p.f / 16), abort);
+                            good = wait_count(p.ctl, C_H, (unsigned)sh.flags[25] * (p.f / 16), abort);
                         if (it.kind == UP)
                             good = wait_count(p.ctl, C_U, n.combine, abort) &&
                                    wait_count(p.ctl, C_PART, n.shared_down, abort);
@@ -800,6 +863,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 if (x_rows && !mx4) {
                     // x as it is: one bulk copy per row
                     if (tid == 0) {
+                        sh.flags[3] = set + 1;
                         const uint32_t bytes = (uint32_t)(kn * a.eb);
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         mbar_expect_tx(sh.act_full + 8u * slot, bytes * (uint32_t)it.ncol);
@@ -865,42 +929,39 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
     } else if (warp < CONSUMERS) {
         // ------------------------------------------------------------ consumers
         RoleBarrier bar = {sh.cons, 0u, abort, true};
-        int s = 0, set = -1, cur_key = -1, cur_seg = -1, par = 0, consumed = 0;
-        uint32_t ph = 0;
-        const int box = warp >> 2, sub = warp & 3;
+        const int team = warp >> 2, sub = warp & 3;      // this team takes every second stage
         const int gid = lane >> 2, c4 = lane & 3;
+        int s = team ? half : 0;                         // slot and phase of this team's next stage
+        uint32_t ph = 0, red_ph = 1;
+        int set = -1, cur_key = -1, cur_seg = -1;
         bool ok = true;
-        auto release = [&]() {           // this warp is done with the current stage
+        // Products with the team's next stage follow; then this warp is done with it.
+        auto full = [&]() -> bool { return warp_wait(sh.full + 8u * s, ph, abort); };
+        auto release = [&]() {
             __syncwarp();
             if (lane == 0) mbar_arrive(sh.empty + 8u * s);
-            if (threadIdx.x == 0) sh.flags[4] = ++consumed;
-            if (++s == S) {
-                s = 0;
+            if (++s == (team ? S : half)) {
+                s = team ? half : 0;
                 ph ^= 1u;
             }
         };
         auto done = [&]() {              // this warp's part of the item is stored
             __syncwarp();
-            if (lane == 0) red_shared_release(smem_u32(sh.flags + 22), 1u);
+            if (lane == 0) red_shared_release(smem_u32(sh.flags + 24), 1u);
         };
-        for (;;) {
-            if (!mbar_wait(sh.full + 8u * s, ph, abort)) {
-                ok = false;
-                break;
-            }
-            const Item it = sh.queue[sh.meta[s] % QUEUE];
+        for (int q = 0;; ++q) {
+            if (threadIdx.x == 0) passed[LOADERS + 2] = q;
+            if (!(ok = __all_sync(0xffffffffu, wait_published(published, q, abort)))) break;
+            const Item it = sh.queue[q % QUEUE];
             const int kind = it.kind;
-            if (kind == END) {
-                release();
-                break;
-            }
+            if (kind == END) break;
             if (weightless(kind)) {
                 int good = 1;
                 if (lane == 0) {
                     if (kind == ROUTE) {
                         good = wait_count(p.ctl, C_ROUTER, (unsigned)n.router, abort);
                     } else {
-                        good = wait_count(p.ctl, C_YS, (unsigned)sh.flags[23] * (p.l / 32), abort);
+                        good = wait_count(p.ctl, C_YS, (unsigned)sh.flags[25] * (p.l / 32), abort);
                         if (good && p.standard) good = wait_count(p.ctl, C_PART, n.shared_down, abort);
                     }
                 }
@@ -909,29 +970,26 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 if (kind == ROUTE) {
                     bar = route_item<WT>(p, it.ti, reinterpret_cast<uint32_t *>(sh.red), sh.rsel, bar, warp, lane);
                     if (!(ok = bar.ok)) break;
-                    done();
                 } else {
                     combine_item<WT>(p, it, warp, lane);
-                    done();
                 }
-                release();
+                done();
                 continue;
             }
 
             const ActPlan a = act_plan<WT>(p, it);
             const bool two = two_groups(kind);
             const int nc = chunks(it), nkb = it.nkb;
-            // this warp's k-block of a stage and where its 16 rows lie
-            const int mykb = two ? sub : warp, perkb = two ? 4 : 8;
-            const uint32_t mytile = (uint32_t)((two ? 2 * sub + box : warp) * KBLK_BYTES);
             const uint32_t plane = (uint32_t)(it.ncol * a.stride);
             // Four columns or fewer of two terms: hi in columns 0-3, lo in 4-7 of one product
             const bool packed = a.planes == 2 && it.ncol <= 4;
-            uint32_t act = 0;                 // the current segment's rows
-            // Stage c of the item and the activations for its values from k on; false when a wait gave up.
-            auto stage_ready = [&](int c, int k) -> bool {
-                if (c > 0 && !mbar_wait(sh.full + 8u * s, ph, abort)) return false;
-                const int seg = a.nseg == 1 ? 0 : k / a.kseg;
+            const bool mx4 = WT == W_MX4 && (kind == ROUTED_GU || kind == ROUTED_DOWN);
+            // values of K per stage
+            const int kshift = kind == ROUTER ? 10 : mx4 ? 10 : (WT == W_F32 ? 5 : 6) + (two ? 2 : 3);
+            const uint32_t mytile = (uint32_t)(2 * sub * KBLK_BYTES);   // this warp's two tiles of 16 rows
+            uint32_t act = 0;
+            // The activations of segment `seg`; false when a wait gave up.
+            auto take = [&](int seg) -> bool {
                 if (a.key != cur_key || seg != cur_seg) {
                     if (set >= 0) {
                         __syncwarp();
@@ -940,30 +998,47 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                     ++set;
                     cur_key = a.key;
                     cur_seg = seg;
-                    if (!mbar_wait(sh.act_full + 8u * (set & 1), (uint32_t)(set >> 1) & 1u, abort)) return false;
-                    act = sh.act + (uint32_t)((set & 1) * p.slot_bytes);
+                    if (!warp_wait(sh.act_full + 8u * (set & 1), (uint32_t)(set >> 1) & 1u, abort)) return false;
+                }
+                act = sh.act + (uint32_t)((set & 1) * p.slot_bytes);
+                return true;
+            };
+            // The item's stages: body(c, k0) for this team's ones, k0 the segment's first value.
+            auto stages = [&](auto body) -> bool {
+                int c = first_team(kind, it.out0) ^ team;      // this team's first stage
+                for (int seg = 0; seg < a.nseg; ++seg) {
+                    if (!take(seg)) return false;
+                    const int end = seg + 1 < a.nseg ? ((seg + 1) * a.kseg) >> kshift : nc;
+                    for (; c < end; c += 2) {
+                        if (!full()) return false;
+                        body(c, seg * a.kseg);
+                        release();
+                    }
                 }
                 return true;
             };
-            act = sh.act + (uint32_t)((set & 1) * p.slot_bytes);
-            float *red = sh.red + par * 1024;
+            float *const mine = sh.red + warp * RED_WARP;
+            auto red_writable = [&]() -> bool {          // everyone has read the last item's sums
+                const bool good = warp_wait(sh.red_free, red_ph, abort);
+                red_ph ^= 1u;
+                return good;
+            };
 
             if (kind == ROUTER) {
                 // ---- 4 rows, 64-bit products: lane (row, 4-value piece)
                 double acc[FEW_MAX_T] = {};
                 const int row = lane >> 3, piece = lane & 7;
-                for (int c = 0; c < nc; ++c) {
-                    if (!(ok = stage_ready(c, c * 1024))) break;
-                    const uint32_t tile = sh.ring + (uint32_t)s * STAGE_BYTES + (uint32_t)(warp * KBLK_BYTES);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int kblk = c * 32 + warp * 4 + i;      // 512 bytes each: 4 rows
+                ok = stages([&](int c, int k0) {
+                    const uint32_t tile = sh.ring + (uint32_t)s * STAGE_BYTES + mytile;
+#pragma unroll 2
+                    for (int i = 0; i < 8; ++i) {
+                        const int kblk = c * 32 + sub * 8 + i;      // 512 bytes each: 4 rows
                         if (kblk >= nkb) break;
                         const int R = i * 4 + row;
                         const uint4 w = lds128(tile + (uint32_t)(R * 128 + ((piece ^ (R & 7)) << 4)));
                         const double w0 = __uint_as_float(w.x), w1 = __uint_as_float(w.y), w2 = __uint_as_float(w.z),
                                      w3 = __uint_as_float(w.w);
-                        const int k = kblk * 32 + 4 * piece - cur_seg * a.kseg;
+                        const int k = kblk * 32 + 4 * piece - k0;
 #pragma unroll
                         for (int t = 0; t < FEW_MAX_T; ++t)
                             if (t < p.T) {
@@ -983,10 +1058,9 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                                 acc[t] = fma(w3, (double)x3, acc[t]);
                             }
                     }
-                    release();
-                }
-                if (!ok) break;
-                double *rd = reinterpret_cast<double *>(red);      // [8 warps][4 rows][8 tokens]
+                });
+                if (!ok || !(ok = red_writable())) break;
+                double *rd = reinterpret_cast<double *>(sh.red);      // [8 warps][4 rows][8 tokens]
 #pragma unroll
                 for (int t = 0; t < FEW_MAX_T; ++t)
                     if (t < p.T) {
@@ -1002,60 +1076,63 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                         for (int w = 0; w < CONSUMERS; ++w) v += rd[w * 32 + lane];
                         p.r64[(int64_t)t * p.E + e] = 1.0 / (1.0 + exp(-v));
                     }
+                    __syncwarp();
                 }
+                if (lane == 0) mbar_arrive(sh.red_free);
                 done();
-                par ^= 1;
                 continue;
             }
 
-            const bool mx4 = WT == W_MX4 && (kind == ROUTED_GU || kind == ROUTED_DOWN);
             if (WT == W_F32) {
-                // ---- fp32: lane (4-value piece, rows rq + 4 i)
-                float acc[4][FEW_MAX_T] = {};
+                // ---- fp32: lane (4-value piece, rows rq + 4 i); two tiles, of one k-block or of two
+                float acc[2][4][FEW_MAX_T] = {};
                 const int piece = lane & 7, rq = lane >> 3;
-                for (int c = 0; c < nc; ++c) {
-                    if (!(ok = stage_ready(c, c * (two ? 128 : 256)))) break;
+                ok = stages([&](int c, int k0) {
                     const uint32_t tile = sh.ring + (uint32_t)s * STAGE_BYTES + mytile;
-                    const int kblk = c * perkb + mykb;
-                    if (kblk < nkb) {
-                        const int k = kblk * 32 + 4 * piece - cur_seg * a.kseg;
-                        float4 w[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int R = rq + 4 * i;
-                            const uint4 v = lds128(tile + (uint32_t)(R * 128 + ((piece ^ (R & 7)) << 4)));
-                            w[i] = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
-                                               __uint_as_float(v.w));
-                        }
+                    for (int g = 0; g < 2; ++g) {
+                        const int kblk = two ? c * 4 + sub : c * 8 + 2 * sub + g;
+                        if (kblk < nkb) {
+                            const int k = kblk * 32 + 4 * piece - k0;
+                            float4 w[4];
 #pragma unroll
-                        for (int t = 0; t < FEW_MAX_T; ++t)
-                            if (t < it.ncol) {
-                                const uint4 v = lds128(act + (uint32_t)(t * a.stride + 4 * k));
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    acc[i][t] = fmaf(w[i].x, __uint_as_float(v.x), acc[i][t]);
-                                    acc[i][t] = fmaf(w[i].y, __uint_as_float(v.y), acc[i][t]);
-                                    acc[i][t] = fmaf(w[i].z, __uint_as_float(v.z), acc[i][t]);
-                                    acc[i][t] = fmaf(w[i].w, __uint_as_float(v.w), acc[i][t]);
-                                }
+                            for (int i = 0; i < 4; ++i) {
+                                const int R = rq + 4 * i;
+                                const uint4 v = lds128(tile + (uint32_t)(g * KBLK_BYTES + R * 128 + ((piece ^ (R & 7)) << 4)));
+                                w[i] = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                                                   __uint_as_float(v.w));
                             }
+#pragma unroll
+                            for (int t = 0; t < FEW_MAX_T; ++t)
+                                if (t < it.ncol) {
+                                    const uint4 v = lds128(act + (uint32_t)(t * a.stride + 4 * k));
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        acc[g][i][t] = fmaf(w[i].x, __uint_as_float(v.x), acc[g][i][t]);
+                                        acc[g][i][t] = fmaf(w[i].y, __uint_as_float(v.y), acc[g][i][t]);
+                                        acc[g][i][t] = fmaf(w[i].z, __uint_as_float(v.z), acc[g][i][t]);
+                                        acc[g][i][t] = fmaf(w[i].w, __uint_as_float(v.w), acc[g][i][t]);
+                                    }
+                                }
+                        }
                     }
-                    release();
-                }
-                if (!ok) break;
+                });
+                if (!ok || !(ok = red_writable())) break;
 #pragma unroll
                 for (int t = 0; t < FEW_MAX_T; ++t)
                     if (t < it.ncol) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int g = 0; g < 2; ++g)
 #pragma unroll
-                            for (int off = 1; off < 8; off <<= 1)
-                                acc[i][t] += __shfl_xor_sync(0xffffffffu, acc[i][t], off);
-                            if (piece == 0) red[warp * 128 + (rq + 4 * i) * 8 + t] = acc[i][t];
-                        }
+                            for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                                for (int off = 1; off < 8; off <<= 1)
+                                    acc[g][i][t] += __shfl_xor_sync(0xffffffffu, acc[g][i][t], off);
+                                if (piece == 0) mine[g * RED_GROUP + (rq + 4 * i) * 8 + t] = acc[g][i][t];
+                            }
                     }
             } else {
-                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                float acc[2][4] = {};
                 // the activation row of one of the eight columns (columns past the tokens repeat the last)
                 auto column = [&](int r) -> uint32_t {
                     const int t = packed ? (r & 3) : r;
@@ -1063,92 +1140,97 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 };
                 if (mx4) {
                     // ---- 4-bit rows: a 16-byte piece of a row is one block of 32 values, eight of
-                    // them (a word) per lane; the block's partial sum times its row's scale
+                    // them (a word) per lane
                     const int nblk = (kind == ROUTED_GU ? p.l : p.f) / 32;
                     const uint32_t mycol = column(gid) + 16u * c4;
-                    for (int c = 0; c < nc; ++c) {
-                        if (!(ok = stage_ready(c, c * 1024))) break;
-                        const uint32_t tile = sh.ring + (uint32_t)s * STAGE_BYTES + mytile + 128u * gid;
+                    ok = stages([&](int c, int k0) {
                         const int kblk = c * 4 + sub;
                         const int nb = min(nblk - kblk * 8, 8);
                         if (nb > 0) {
-                            const uint32_t sc = sh.scales + (uint32_t)(s * SCALE_BYTES + box * (SCALE_BYTES / 2) + 32 * gid + 8 * sub);
-                            const uint2 sa = lds64(sc), sb = lds64(sc + 8 * 32);
-                            const uint32_t arow = act + mycol + (uint32_t)(2 * (kblk * 256 - cur_seg * a.kseg));
-                            if (packed) {
-#pragma unroll
-                                for (int half = 0; half < 2; ++half)
-                                    mx4_blocks<true>(acc, tile, arow, 0u, sa, sb, gid, c4, half, nb);
-                            } else {
-#pragma unroll
-                                for (int half = 0; half < 2; ++half)
-                                    mx4_blocks<false>(acc, tile, arow, plane, sa, sb, gid, c4, half, nb);
-                            }
+                            const uint32_t tile = sh.ring + (uint32_t)s * STAGE_BYTES + mytile + 128u * gid;
+                            const uint32_t sc = sh.scales + (uint32_t)(s * SCALE_BYTES + 32 * gid + 8 * sub);
+                            const uint32_t arow = act + mycol + (uint32_t)(2 * (kblk * 256 - k0));
+                            if (packed) mx4_kblock<true>(acc, tile, arow, 0u, sc, gid, c4, nb);
+                            else mx4_kblock<false>(acc, tile, arow, plane, sc, gid, c4, nb);
                         }
-                        release();
-                    }
+                    });
                 } else {
-                    // ---- bf16 rows: 64 values of 16 rows per k-block, two chains of sums
+                    // ---- bf16 rows: 64 values of 16 rows per tile
                     const int lrow = (lane & 7) + ((lane >> 3) & 1) * 8;
                     const uint32_t mycol = column(lane & 7) + 16u * (lane >> 3);
-                    const uint32_t wrow = mytile + (uint32_t)(lrow * 128);
                     uint32_t piece[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) piece[i] = wrow + (uint32_t)(((2 * i + (lane >> 4)) ^ (lrow & 7)) << 4);
+                    for (int i = 0; i < 4; ++i)
+                        piece[i] = mytile + (uint32_t)(lrow * 128 + (((2 * i + (lane >> 4)) ^ (lrow & 7)) << 4));
                     const bool lo_too = a.planes == 2 && !packed;
-                    float acc2[4] = {0.f, 0.f, 0.f, 0.f};
-                    for (int c = 0; c < nc; ++c) {
-                        if (!(ok = stage_ready(c, c * (two ? 256 : 512)))) break;
+                    ok = stages([&](int c, int k0) {
                         const uint32_t tile = sh.ring + (uint32_t)s * STAGE_BYTES;
-                        const int kblk = c * perkb + mykb;
+                        const int kblk = two ? c * 4 + sub : c * 8 + 2 * sub;
                         if (kblk < nkb) {
-                            const uint32_t arow = act + mycol + (uint32_t)(2 * (kblk * 64 - cur_seg * a.kseg));
-                            uint32_t w[4][4], b0[4], b1[4];
-                            ldmatrix_x4(b0, arow);
-                            ldmatrix_x4(b1, arow + 64u);
+                            const uint32_t arow = act + mycol + (uint32_t)(2 * (kblk * 64 - k0));
+                            uint32_t w[2][4][4], b[2][4];
+                            ldmatrix_x4(b[0], arow);
+                            ldmatrix_x4(b[1], arow + 64u);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) ldmatrix_x4(w[i], tile + piece[i]);
-                            if (lo_too) {
-                                uint32_t c0[4], c1[4];
-                                ldmatrix_x4(c0, arow + plane);
-                                ldmatrix_x4(c1, arow + plane + 64u);
-                                mma_bf16(acc2, w[0], c0[0], c0[1]);
-                                mma_bf16(acc, w[0], b0[0], b0[1]);
-                                mma_bf16(acc2, w[1], c0[2], c0[3]);
-                                mma_bf16(acc, w[1], b0[2], b0[3]);
-                                mma_bf16(acc2, w[2], c1[0], c1[1]);
-                                mma_bf16(acc, w[2], b1[0], b1[1]);
-                                mma_bf16(acc2, w[3], c1[2], c1[3]);
-                                mma_bf16(acc, w[3], b1[2], b1[3]);
+                            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) ldmatrix_x4(w[g][i], tile + piece[i] + (uint32_t)(g * KBLK_BYTES));
+                            auto times = [&](float (&to)[4], const uint32_t (&wt)[4][4]) {
+                                mma_bf16(to, wt[0], b[0][0], b[0][1]);
+                                mma_bf16(to, wt[1], b[0][2], b[0][3]);
+                                mma_bf16(to, wt[2], b[1][0], b[1][1]);
+                                mma_bf16(to, wt[3], b[1][2], b[1][3]);
+                            };
+                            times(acc[0], w[0]);
+                            if (two) {
+                                times(acc[1], w[1]);
+                                if (lo_too) {
+                                    ldmatrix_x4(b[0], arow + plane);
+                                    ldmatrix_x4(b[1], arow + plane + 64u);
+                                    times(acc[0], w[0]);
+                                    times(acc[1], w[1]);
+                                }
                             } else {
-                                mma_bf16(acc, w[0], b0[0], b0[1]);
-                                mma_bf16(acc2, w[1], b0[2], b0[3]);
-                                mma_bf16(acc, w[2], b1[0], b1[1]);
-                                mma_bf16(acc2, w[3], b1[2], b1[3]);
+                                if (lo_too) {
+                                    ldmatrix_x4(b[0], arow + plane);
+                                    ldmatrix_x4(b[1], arow + plane + 64u);
+                                    times(acc[0], w[0]);
+                                }
+                                if (kblk + 1 < nkb) {      // the second tile is the next k-block
+                                    ldmatrix_x4(b[0], arow + 128u);
+                                    ldmatrix_x4(b[1], arow + 192u);
+                                    times(acc[1], w[1]);
+                                    if (lo_too) {
+                                        ldmatrix_x4(b[0], arow + plane + 128u);
+                                        ldmatrix_x4(b[1], arow + plane + 192u);
+                                        times(acc[1], w[1]);
+                                    }
+                                }
                             }
                         }
-                        release();
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[i] += acc2[i];
+                    });
                 }
-                if (!ok) break;
-                float2 *r = reinterpret_cast<float2 *>(red + warp * 128 + gid * 8 + 2 * c4);
-                r[0] = make_float2(acc[0], acc[1]);
-                r[32] = make_float2(acc[2], acc[3]);
+                if (!ok || !(ok = red_writable())) break;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    float2 *r = reinterpret_cast<float2 *>(mine + g * RED_GROUP + gid * 8 + 2 * c4);
+                    r[0] = make_float2(acc[g][0], acc[g][1]);
+                    r[32] = make_float2(acc[g][2], acc[g][3]);
+                }
             }
 
-            // ---- sums over the warps, and what becomes of them: thread (row, token) of 16 x 8.
-            // What the epilogue reads from global memory is asked for before the barrier.
-            const int cell = threadIdx.x & 127, row = cell >> 3, t = cell & 7, grp = threadIdx.x >> 7;
+            // ---- sums over the warps, and what becomes of them: thread (row, token, group) of
+            // 16 x 8 x 2, the groups in neighbouring lanes.  What the epilogue reads from global
+            // memory is asked for before the barrier.
+            const int grp = threadIdx.x & 1, cell = threadIdx.x >> 1, row = cell >> 3, t = cell & 7;
             const bool real = t < it.ncol;
-            const int r = it.out0 + (two && kind != SHARED_GU && kind != ROUTED_GU ? 16 * grp : 0) + row;
+            const int r = it.out0 + (kind == SHARED_DOWN || kind == ROUTED_DOWN ? 16 * grp : 0) + row;
             float add = 0.f;
             int slot = -1;
             if (kind == UP) {
                 if (real && grp == 0) {
-                    const float *q = p.part + (int64_t)t * p.d + r;
-                    add = __ldcg(q) + __ldcg(q + (int64_t)p.T * p.d);
+                    const float *q2 = p.part + (int64_t)t * p.d + r;
+                    add = __ldcg(q2) + __ldcg(q2 + (int64_t)p.T * p.d);
                 }
             } else if (kind == ROUTED_DOWN) {
                 if (real) {
@@ -1161,48 +1243,38 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
             }
             const float back = mx4 && real ? sh.inv[8 * (set & 1) + t] : 1.f;
             if (!(ok = bar.sync())) break;
-            auto sum = [&](int w0, int nw) { return red_sum(red, w0, nw, cell, packed) * back; };
+            const float v = red_sum(sh.red + grp * RED_GROUP + cell, packed && t < 4) * back;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sh.red_free);
+            const float other = __shfl_xor_sync(0xffffffffu, v, 1);     // the other group's sum
             if (kind == SHARED_GU || kind == ROUTED_GU) {
-                if (grp == 0) {
-                    const float gv = sum(0, 4), uv = sum(4, 4);
-                    const float h = glu_act(p.act, gv, uv, p.gate_cap, p.up_cap);
-                    if (kind == SHARED_GU) {
-                        if (real) p.hs[(int64_t)t * 2 * p.fs + r] = h;
-                    } else {
-                        if (slot >= 0) p.H[(int64_t)slot * p.f + r] = h;
-                        if (WT == W_MX4) {
-                            float m = slot >= 0 ? fabsf(h) : 0.f;
-                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                            if (lane < 8 && slot >= 0) atomicMax(p.ctl + C_AMAX_H + slot, __float_as_uint(m));
-                        }
+                const float h = grp == 0 ? glu_act(p.act, v, other, p.gate_cap, p.up_cap) : 0.f;
+                if (kind == SHARED_GU) {
+                    if (real && grp == 0) p.hs[(int64_t)t * 2 * p.fs + r] = h;
+                } else {
+                    if (slot >= 0 && grp == 0) p.H[(int64_t)slot * p.f + r] = h;
+                    if (WT == W_MX4) {      // rows of a warp: lane bit 4
+                        float m = slot >= 0 ? fabsf(h) : 0.f;
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                        if (lane < 16 && grp == 0 && slot >= 0) atomicMax(p.ctl + C_AMAX_H + slot, __float_as_uint(m));
                     }
                 }
-            } else if (kind == DOWN || kind == UP) {
-                if (grp == 0) {
-                    const float v = sum(0, 8);
-                    if (kind == DOWN) {
-                        if (real) p.z[(int64_t)t * p.l + r] = v;
-                        if (WT == W_MX4) {
-                            float m = real ? fabsf(v) : 0.f;
-                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                            if (lane < 8 && real) atomicMax(p.ctl + C_AMAX_Z + t, __float_as_uint(m));
-                        }
-                    } else if (real) {
-                        store_token<WT>(p.y, (int64_t)t * p.d + r, v + add);
-                    }
+            } else if (kind == DOWN) {
+                const float z = v + other;
+                if (real && grp == 0) p.z[(int64_t)t * p.l + r] = z;
+                if (WT == W_MX4) {
+                    float m = real ? fabsf(z) : 0.f;
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                    if (lane < 16 && grp == 0 && real) atomicMax(p.ctl + C_AMAX_Z + t, __float_as_uint(m));
                 }
-            } else {
-                const float v = sum(4 * grp, 4);
-                if (kind == SHARED_DOWN) {
-                    if (real) p.part[((int64_t)it.ti * p.T + t) * p.d + r] = v;
-                } else if (real) {
-                    p.ysl[(int64_t)slot * p.l + r] = add * v;
-                }
+            } else if (kind == UP) {
+                if (real && grp == 0) store_token<WT>(p.y, (int64_t)t * p.d + r, v + other + add);
+            } else if (kind == SHARED_DOWN) {
+                if (real) p.part[((int64_t)it.ti * p.T + t) * p.d + r] = v;
+            } else if (real) {
+                p.ysl[(int64_t)slot * p.l + r] = add * v;
             }
             done();
-            par ^= 1;
         }
         if (!ok && lane == 0) give_up(0x8);
     } else {
@@ -1218,7 +1290,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 const int kind = sh.queue[q % QUEUE].kind;
                 if (kind == END) break;
                 counted += CONSUMERS;
-                const uint32_t word = smem_u32(sh.flags + 22);
+                const uint32_t word = smem_u32(sh.flags + 24);
                 const long long t1 = clock64();
                 while (lds_acquire(word) < counted && ok) {
                     __nanosleep(20);
@@ -1242,19 +1314,25 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
 
     __syncthreads();
     if (*abort && threadIdx.x == 0) {
-        // copies issued but not consumed must land before the block's memory goes away
-        const int issued = sh.flags[2];
+        // copies in flight must land before the block's memory goes away: the last
+        // use of every stage, and the last two sets of x (each wait bounded)
         int none = 0;
-        for (int i = sh.flags[4]; i < issued; ++i)
-            if (!mbar_wait(sh.full + 8u * (i % S), (uint32_t)(i / S) & 1u, &none)) break;
+        const int sets = sh.flags[3];
+        for (int team = 0; team < 2; ++team) {
+            const int issued = sh.flags[26 + team], n2 = team ? S - half : half, at = team ? half : 0;
+            for (int i = max(0, issued - n2); i < issued; ++i)
+                mbar_wait(sh.full + 8u * (at + i % n2), (uint32_t)(i / n2) & 1u, &none);
+        }
+        for (int i = max(0, sets - 2); i < sets; ++i)
+            if (!mbar_wait(sh.act_full + 8u * (i & 1), (uint32_t)(i >> 1) & 1u, &none)) break;
     }
 }
 
 // ------------------------------------------------------------------ host side
 size_t fixed_smem()
 {
-    return 1024 + 2 * 8 * 128 * 4 + sizeof(Touched) * FEW_MAX_SLOTS + 4 * MAX_E + 8 * 64 + sizeof(Item) * QUEUE + 8 * (2 * MAX_STAGES + 6) +
-           sizeof(int) * MAX_STAGES + 64 + 64 + 128;
+    return 1024 + 4 * RED_FLOATS + sizeof(Touched) * FEW_MAX_SLOTS + 4 * MAX_E + 8 * 64 + sizeof(Item) * QUEUE + 8 * (2 * MAX_STAGES + 8) +
+           64 + 64 + 128;
 }
 
 struct FewLayout {
