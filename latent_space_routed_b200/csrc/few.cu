@@ -408,81 +408,59 @@ __device__ __forceinline__ float red_sum(const float *cell, bool packed)
     return v;
 }
 
-// N blocks of 32 values, from block j0 on, of a 128-byte k-block of two groups of 16
+// A 128-byte k-block (eight blocks of 32 values, nb of them real) of two groups of 16
 // rows of 4-bit weights against eight columns: acc += scale of the row's block *
-// partial sum.  No branch inside: the blocks' loads, conversions and products overlap.
-// e[g][h]: the blocks' scales (a byte each) of rows gid + 8 h of group g.
-template <bool PACKED, int N>
-__device__ __forceinline__ void mx4_blocks(float (&acc)[2][4], uint32_t tile, uint32_t arow, uint32_t plane,
-                                           const uint32_t (&e)[2][2], int gid, int c4, int j0)
-{
-    uint32_t w[2][2][N];
-    uint4 h[N], lo[N];
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-        const uint32_t off = (uint32_t)((((j0 + j) ^ gid) << 4) + 4 * c4);
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            w[g][0][j] = lds32(tile + KBLK_BYTES * g + off);
-            w[g][1][j] = lds32(tile + KBLK_BYTES * g + 1024 + off);
-        }
-        h[j] = lds128(arow + 64u * (j0 + j));
-        if (!PACKED) lo[j] = lds128(arow + plane + 64u * (j0 + j));
-    }
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            uint32_t wa[4], wb[4];
-            e2m1x8_to_f16(wa, w[g][0][j]);
-            e2m1x8_to_f16(wb, w[g][1][j]);
-            float t[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16(t, wa[0], wb[0], wa[1], wb[1], h[j].x, h[j].y);
-            mma_f16(t, wa[2], wb[2], wa[3], wb[3], h[j].z, h[j].w);
-            if (!PACKED) {
-                mma_f16(t, wa[0], wb[0], wa[1], wb[1], lo[j].x, lo[j].y);
-                mma_f16(t, wa[2], wb[2], wa[3], wb[3], lo[j].z, lo[j].w);
-            }
-            // 2^(e - 127); e = 0 counts as zero (below fp32's normal range), 255 is NaN
-            const uint32_t xa = (e[g][0] >> (8 * j)) & 255u, xb = (e[g][1] >> (8 * j)) & 255u;
-            const float fa = __uint_as_float(xa == 255u ? 0x7fffffffu : xa << 23);
-            const float fb = __uint_as_float(xb == 255u ? 0x7fffffffu : xb << 23);
-            acc[g][0] = fmaf(t[0], fa, acc[g][0]);
-            acc[g][1] = fmaf(t[1], fa, acc[g][1]);
-            acc[g][2] = fmaf(t[2], fb, acc[g][2]);
-            acc[g][3] = fmaf(t[3], fb, acc[g][3]);
-        }
-}
-// All blocks of a k-block, nb <= 8 of them real.
-template <bool PACKED>
+// partial sum.  All words and scales come into registers first, then `release` gives
+// the stage back; the blocks' conversions and products overlap, two blocks at a time.
+template <bool PACKED, typename Release>
 __device__ __forceinline__ void mx4_kblock(float (&acc)[2][4], uint32_t tile, uint32_t arow, uint32_t plane,
-                                           uint32_t scales, int gid, int c4, int nb)
+                                           uint32_t scales, int gid, int c4, int nb, Release release)
 {
+    uint32_t w[8][2][2];     // block, group, row gid + 8 h
     uint2 e[2][2];
 #pragma unroll
     for (int g = 0; g < 2; ++g)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) e[g][h] = lds64(scales + (uint32_t)(512 * g + 256 * h));
-    if (nb == 8) {
+        for (int h = 0; h < 2; ++h) {
+            e[g][h] = lds64(scales + (uint32_t)(512 * g + 256 * h));
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            uint32_t f[2][2];
-#pragma unroll
-            for (int g = 0; g < 2; ++g)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) f[g][h] = (j < 4 ? e[g][h].x : e[g][h].y) >> (8 * (j & 3));
-            mx4_blocks<PACKED, 2>(acc, tile, arow, plane, f, gid, c4, j);
+            for (int j = 0; j < 8; ++j)
+                w[j][g][h] = lds32(tile + (uint32_t)(KBLK_BYTES * g + 1024 * h + ((j ^ gid) << 4) + 4 * c4));
         }
-    } else {
-#pragma unroll 1
-        for (int j = 0; j < nb; ++j) {
-            uint32_t f[2][2];
+    release();
 #pragma unroll
-            for (int g = 0; g < 2; ++g)
+    for (int j0 = 0; j0 < 8; j0 += 2) {
+        if (j0 >= nb) break;         // nb is even: K is a multiple of 64
+        uint4 x[2], y[2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) f[g][h] = (j < 4 ? e[g][h].x : e[g][h].y) >> (8 * (j & 3));
-            mx4_blocks<PACKED, 1>(acc, tile, arow, plane, f, gid, c4, j);
+        for (int j = 0; j < 2; ++j) {
+            x[j] = lds128(arow + 64u * (j0 + j));
+            if (!PACKED) y[j] = lds128(arow + plane + 64u * (j0 + j));
         }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                uint32_t wa[4], wb[4];
+                e2m1x8_to_f16(wa, w[j0 + j][g][0]);
+                e2m1x8_to_f16(wb, w[j0 + j][g][1]);
+                float t[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_f16(t, wa[0], wb[0], wa[1], wb[1], x[j].x, x[j].y);
+                mma_f16(t, wa[2], wb[2], wa[3], wb[3], x[j].z, x[j].w);
+                if (!PACKED) {
+                    mma_f16(t, wa[0], wb[0], wa[1], wb[1], y[j].x, y[j].y);
+                    mma_f16(t, wa[2], wb[2], wa[3], wb[3], y[j].z, y[j].w);
+                }
+                // 2^(e - 127); e = 0 counts as zero (below fp32's normal range), 255 is NaN
+                const uint32_t ea = j0 < 4 ? e[g][0].x : e[g][0].y, eb = j0 < 4 ? e[g][1].x : e[g][1].y;
+                const uint32_t xa = (ea >> (8 * ((j0 + j) & 3))) & 255u, xb = (eb >> (8 * ((j0 + j) & 3))) & 255u;
+                const float fa = __uint_as_float(xa == 255u ? 0x7fffffffu : xa << 23);
+                const float fb = __uint_as_float(xb == 255u ? 0x7fffffffu : xb << 23);
+                acc[g][0] = fmaf(t[0], fa, acc[g][0]);
+                acc[g][1] = fmaf(t[1], fa, acc[g][1]);
+                acc[g][2] = fmaf(t[2], fb, acc[g][2]);
+                acc[g][3] = fmaf(t[3], fb, acc[g][3]);
+            }
     }
 }
 
@@ -1003,7 +981,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 act = sh.act + (uint32_t)((set & 1) * p.slot_bytes);
                 return true;
             };
-            // The item's stages: body(c, k0) for this team's ones, k0 the segment's first value.
+            // The item's stages: body(c, k0) for this team's ones, k0 the segment's first value.  body
+            // calls release() as soon as its tiles are in registers, before the products.
             auto stages = [&](auto body) -> bool {
                 int c = first_team(kind, it.out0) ^ team;      // this team's first stage
                 for (int seg = 0; seg < a.nseg; ++seg) {
@@ -1011,8 +990,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                     const int end = seg + 1 < a.nseg ? ((seg + 1) * a.kseg) >> kshift : nc;
                     for (; c < end; c += 2) {
                         if (!full()) return false;
-                        body(c, seg * a.kseg);
-                        release();
+                        body(c, seg * a.kseg);       // releases the stage once it has loaded what it needs
                     }
                 }
                 return true;
@@ -1058,6 +1036,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                                 acc[t] = fma(w3, (double)x3, acc[t]);
                             }
                     }
+                    release();
                 });
                 if (!ok || !(ok = red_writable())) break;
                 double *rd = reinterpret_cast<double *>(sh.red);      // [8 warps][4 rows][8 tokens]
@@ -1116,6 +1095,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                                 }
                         }
                     }
+                    release();
                 });
                 if (!ok || !(ok = red_writable())) break;
 #pragma unroll
@@ -1150,8 +1130,10 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                             const uint32_t tile = sh.ring + (uint32_t)s * STAGE_BYTES + mytile + 128u * gid;
                             const uint32_t sc = sh.scales + (uint32_t)(s * SCALE_BYTES + 32 * gid + 8 * sub);
                             const uint32_t arow = act + mycol + (uint32_t)(2 * (kblk * 256 - k0));
-                            if (packed) mx4_kblock<true>(acc, tile, arow, 0u, sc, gid, c4, nb);
-                            else mx4_kblock<false>(acc, tile, arow, plane, sc, gid, c4, nb);
+                            if (packed) mx4_kblock<true>(acc, tile, arow, 0u, sc, gid, c4, nb, release);
+                            else mx4_kblock<false>(acc, tile, arow, plane, sc, gid, c4, nb, release);
+                        } else {
+                            release();
                         }
                     });
                 } else {
@@ -1169,44 +1151,46 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                         if (kblk < nkb) {
                             const uint32_t arow = act + mycol + (uint32_t)(2 * (kblk * 64 - k0));
                             uint32_t w[2][4][4], b[2][4];
-                            ldmatrix_x4(b[0], arow);
-                            ldmatrix_x4(b[1], arow + 64u);
 #pragma unroll
                             for (int g = 0; g < 2; ++g)
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) ldmatrix_x4(w[g][i], tile + piece[i] + (uint32_t)(g * KBLK_BYTES));
+                            release();
+                            auto columns = [&](uint32_t at) {
+                                ldmatrix_x4(b[0], at);
+                                ldmatrix_x4(b[1], at + 64u);
+                            };
                             auto times = [&](float (&to)[4], const uint32_t (&wt)[4][4]) {
                                 mma_bf16(to, wt[0], b[0][0], b[0][1]);
                                 mma_bf16(to, wt[1], b[0][2], b[0][3]);
                                 mma_bf16(to, wt[2], b[1][0], b[1][1]);
                                 mma_bf16(to, wt[3], b[1][2], b[1][3]);
                             };
+                            columns(arow);
                             times(acc[0], w[0]);
                             if (two) {
                                 times(acc[1], w[1]);
                                 if (lo_too) {
-                                    ldmatrix_x4(b[0], arow + plane);
-                                    ldmatrix_x4(b[1], arow + plane + 64u);
+                                    columns(arow + plane);
                                     times(acc[0], w[0]);
                                     times(acc[1], w[1]);
                                 }
                             } else {
                                 if (lo_too) {
-                                    ldmatrix_x4(b[0], arow + plane);
-                                    ldmatrix_x4(b[1], arow + plane + 64u);
+                                    columns(arow + plane);
                                     times(acc[0], w[0]);
                                 }
                                 if (kblk + 1 < nkb) {      // the second tile is the next k-block
-                                    ldmatrix_x4(b[0], arow + 128u);
-                                    ldmatrix_x4(b[1], arow + 192u);
+                                    columns(arow + 128u);
                                     times(acc[1], w[1]);
                                     if (lo_too) {
-                                        ldmatrix_x4(b[0], arow + plane + 128u);
-                                        ldmatrix_x4(b[1], arow + plane + 192u);
+                                        columns(arow + plane + 128u);
                                         times(acc[1], w[1]);
                                     }
                                 }
                             }
+                        } else {
+                            release();
                         }
                     });
                 }
