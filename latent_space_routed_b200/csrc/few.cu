@@ -1145,47 +1145,55 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                     for (int i = 0; i < 4; ++i)
                         piece[i] = mytile + (uint32_t)(lrow * 128 + (((2 * i + (lane >> 4)) ^ (lrow & 7)) << 4));
                     const bool lo_too = a.planes == 2 && !packed;
+                    float acl[2][4] = {};
                     ok = stages([&](int c, int k0) {
                         const uint32_t tile = sh.ring + (uint32_t)s * STAGE_BYTES;
                         const int kblk = two ? c * 4 + sub : c * 8 + 2 * sub;
                         if (kblk < nkb) {
                             const uint32_t arow = act + mycol + (uint32_t)(2 * (kblk * 64 - k0));
-                            uint32_t w[2][4][4], b[2][4];
+                            uint32_t w[2][4][4];
 #pragma unroll
                             for (int g = 0; g < 2; ++g)
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) ldmatrix_x4(w[g][i], tile + piece[i] + (uint32_t)(g * KBLK_BYTES));
                             release();
-                            auto columns = [&](uint32_t at) {
-                                ldmatrix_x4(b[0], at);
-                                ldmatrix_x4(b[1], at + 64u);
+                            // neighbouring products go to different sums: a chain on one costs its latency
+                            auto columns = [&](uint32_t (&x)[8], uint32_t at) {
+                                uint32_t y[4];
+                                ldmatrix_x4(y, at);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) x[i] = y[i];
+                                ldmatrix_x4(y, at + 64u);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) x[4 + i] = y[i];
                             };
-                            auto times = [&](float (&to)[4], const uint32_t (&wt)[4][4]) {
-                                mma_bf16(to, wt[0], b[0][0], b[0][1]);
-                                mma_bf16(to, wt[1], b[0][2], b[0][3]);
-                                mma_bf16(to, wt[2], b[1][0], b[1][1]);
-                                mma_bf16(to, wt[3], b[1][2], b[1][3]);
-                            };
-                            columns(arow);
-                            times(acc[0], w[0]);
+                            uint32_t b0[8], b1[8];
+                            columns(b0, arow);
                             if (two) {
-                                times(acc[1], w[1]);
-                                if (lo_too) {
-                                    columns(arow + plane);
-                                    times(acc[0], w[0]);
-                                    times(acc[1], w[1]);
-                                }
-                            } else {
-                                if (lo_too) {
-                                    columns(arow + plane);
-                                    times(acc[0], w[0]);
-                                }
-                                if (kblk + 1 < nkb) {      // the second tile is the next k-block
-                                    columns(arow + 128u);
-                                    times(acc[1], w[1]);
+                                if (lo_too) columns(b1, arow + plane);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    mma_bf16(acc[0], w[0][i], b0[2 * i], b0[2 * i + 1]);
+                                    mma_bf16(acc[1], w[1][i], b0[2 * i], b0[2 * i + 1]);
                                     if (lo_too) {
-                                        columns(arow + plane + 128u);
-                                        times(acc[1], w[1]);
+                                        mma_bf16(acl[0], w[0][i], b1[2 * i], b1[2 * i + 1]);
+                                        mma_bf16(acl[1], w[1][i], b1[2 * i], b1[2 * i + 1]);
+                                    }
+                                }
+                            } else {                       // the second tile is the next k-block
+                                if (kblk + 1 < nkb) columns(b1, arow + 128u);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    mma_bf16(acc[0], w[0][i], b0[2 * i], b0[2 * i + 1]);
+                                    if (kblk + 1 < nkb) mma_bf16(acc[1], w[1][i], b1[2 * i], b1[2 * i + 1]);
+                                }
+                                if (lo_too) {
+                                    columns(b0, arow + plane);
+                                    if (kblk + 1 < nkb) columns(b1, arow + plane + 128u);
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        mma_bf16(acl[0], w[0][i], b0[2 * i], b0[2 * i + 1]);
+                                        if (kblk + 1 < nkb) mma_bf16(acl[1], w[1][i], b1[2 * i], b1[2 * i + 1]);
                                     }
                                 }
                             }
@@ -1193,6 +1201,11 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                             release();
                         }
                     });
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        acc[0][i] += acl[0][i];
+                        acc[1][i] += acl[1][i];
+                    }
                 }
                 if (!ok || !(ok = red_writable())) break;
 #pragma unroll
