@@ -161,6 +161,34 @@ LMOE_API lmoe_status lmoe_mx4_quantize(const void *x, int32_t dtype, int64_t row
 LMOE_API lmoe_status lmoe_mx4_dequantize(const void *codes, const void *scales, int64_t rows, int64_t cols,
                                          int32_t dtype, void *y, int64_t ld, void *stream);
 
+/* Workspace of lmoe_mx4_gemm: its device status word. */
+#define LMOE_MX4_GEMM_WORKSPACE_BYTES ((size_t)256)
+
+/* out[m, n] = sum_k A[m, k] W[n, k] of 4-bit matrices, summed in fp32 on the
+ * tensor cores and rounded once, enqueued on `stream`:
+ *  a_codes, a_scales   A [M, K]
+ *  w_codes, w_scales   W [N, K]; with offsets [E, N, K]
+ *  offsets             NULL: dense.  Otherwise [E + 1] (device int32): rows
+ *                      [offsets[e], offsets[e + 1]) of A are those of expert e;
+ *                      values are taken ascending and clamped to [0, M]; rows
+ *                      of out that belong to no expert are left as they were
+ *  out                 [M, N] dtype, row stride ldo elements
+ *  workspace           LMOE_MX4_GEMM_WORKSPACE_BYTES, 256-byte aligned; calls
+ *                      that may overlap need one each
+ * K is a multiple of 64, codes are 16-byte aligned, E <= 1024.  M or N 0 is a
+ * no-op.  Runs on the current device, which must be the tensors'.
+ * INVALID_ARG: NULL pointer, negative size, unknown dtype, E < 1, ldo < N.
+ * UNSUPPORTED: K, alignment, E > 1024, sizes past 2^31, no sm_100 device.
+ * WORKSPACE: too small or misaligned. */
+LMOE_API lmoe_status lmoe_mx4_gemm(const void *a_codes, const void *a_scales, int64_t M, const void *w_codes,
+                                   const void *w_scales, int64_t N, int64_t K, const int32_t *offsets, int32_t E,
+                                   int32_t dtype, void *out, int64_t ldo, void *workspace, size_t ws_bytes,
+                                   void *stream);
+
+/* Synchronise `stream`, then read and clear the status word of the last
+ * lmoe_mx4_gemm on this workspace: LMOE_OK or LMOE_ERR_DEVICE_TIMEOUT. */
+LMOE_API lmoe_status lmoe_mx4_gemm_check(void *workspace, void *stream);
+
 /* Routed experts in 4 bits (device pointers, read only during the create call):
  * G, U codes of [E, f, l], D codes of [E, l, f], with their scales; quantised
  * along the last dimension. */

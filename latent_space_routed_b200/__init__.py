@@ -34,7 +34,7 @@ REGION = {"scores": 0, "p32": 1, "counts": 2, "offsets": 3, "slot_of": 4, "perm_
 
 EXPORTS = ("lmoe_config_from_base", "lmoe_create", "lmoe_workspace_size", "lmoe_forward", "lmoe_host_workspace_size",
            "lmoe_forward_host", "lmoe_forward_noalloc", "lmoe_create_mx4", "lmoe_few_workspace_size", "lmoe_forward_few",
-           "lmoe_mx4_quantize", "lmoe_mx4_dequantize", "lmoe_debug_inject", "lmoe_set_bias", "lmoe_qb_histogram", "lmoe_qb_bias_update", "lmoe_set_stage_events", "lmoe_launch_count", "lmoe_workspace_region", "lmoe_check_device", "lmoe_check_device_host",
+           "lmoe_mx4_quantize", "lmoe_mx4_dequantize", "lmoe_mx4_gemm", "lmoe_mx4_gemm_check", "lmoe_debug_inject", "lmoe_set_bias", "lmoe_qb_histogram", "lmoe_qb_bias_update", "lmoe_set_stage_events", "lmoe_launch_count", "lmoe_workspace_region", "lmoe_check_device", "lmoe_check_device_host",
            "lmoe_last_error", "lmoe_destroy")
 
 
@@ -73,6 +73,8 @@ def _load() -> ctypes.CDLL:
         "lmoe_few_workspace_size": (I32, [P, I64, ctypes.POINTER(SZ)]),
         "lmoe_forward_few": (I32, [P, P, I64, P, P, P, P, P, SZ, P]),
         "lmoe_mx4_quantize": (I32, [P, I32, I64, I64, I64, P, P, P]),
+        "lmoe_mx4_gemm": (I32, [P, P, I64, P, P, I64, I64, P, I32, I32, P, I64, P, SZ, P]),
+        "lmoe_mx4_gemm_check": (I32, [P, P]),
         "lmoe_mx4_dequantize": (I32, [P, P, I64, I64, I32, P, I64, P]),
         "lmoe_workspace_size": (I32, [P, I64, ctypes.POINTER(SZ)]),
         "lmoe_forward": (I32, [P, P, I64, P, P, P, P, P, SZ, P]),
@@ -170,6 +172,19 @@ def lmoe_mx4_quantize(x, dtype, rows, cols, ld, codes, scales, stream=None):
 
 def lmoe_mx4_dequantize(codes, scales, rows, cols, dtype, y, ld, stream=None):
     _check(_lib.lmoe_mx4_dequantize(_ptr(codes), _ptr(scales), rows, cols, dtype, _ptr(y), ld, _stream(stream)))
+
+
+LMOE_MX4_GEMM_WORKSPACE_BYTES = 256
+
+
+def lmoe_mx4_gemm(a_codes, a_scales, M, w_codes, w_scales, N, K, offsets, E, dtype, out, ldo, workspace, ws_bytes,
+                  stream=None):
+    _check(_lib.lmoe_mx4_gemm(_ptr(a_codes), _ptr(a_scales), M, _ptr(w_codes), _ptr(w_scales), N, K, _ptr(offsets), E,
+                              dtype, _ptr(out), ldo, _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def lmoe_mx4_gemm_check(workspace, stream=None):
+    _check(_lib.lmoe_mx4_gemm_check(_ptr(workspace), _stream(stream)))
 
 
 def lmoe_destroy(h: int):
@@ -335,6 +350,45 @@ def mx4_dequantize(q: Mx4, dtype: torch.dtype = torch.bfloat16, stream=None) -> 
             lmoe_mx4_dequantize(q.codes, q.scales, y.numel() // cols, cols, _LM_DT[dtype], y, cols,
                                 _on(y.device, stream))
     return y
+
+
+def mx4_gemm_workspace(device=None) -> torch.Tensor:
+    """A workspace for mx4_gemm calls that follow one another on one stream."""
+    return torch.empty(LMOE_MX4_GEMM_WORKSPACE_BYTES, dtype=torch.uint8,
+                       device=torch.device("cuda", torch.cuda.current_device()) if device is None else device)
+
+
+def mx4_gemm(a: Mx4, w: Mx4, offsets: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16,
+             out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """a [M, K] times w [N, K] transposed, in 4 bits with fp32 sums; with offsets [E + 1] (int32, on the device)
+    rows offsets[e] to offsets[e + 1] of a times w[e] of w [E, N, K].  ``out`` [M, N] (its dtype counts then) may
+    have a row stride; without it, rows that belong to no expert are zero."""
+    a.check("a"), w.check("w")
+    if a.codes.dim() != 2 or w.codes.dim() != (2 if offsets is None else 3):
+        raise ValueError("a must be [M, K] and w [N, K], or [E, N, K] with offsets")
+    M, K = a.shape
+    N = w.shape[-2]
+    if w.shape[-1] != K:
+        raise ValueError(f"K differs: {K} and {w.shape[-1]}")
+    dev = a.codes.device
+    E = 1 if offsets is None else w.shape[0]
+    if offsets is not None and (offsets.dtype != torch.int32 or offsets.shape != (E + 1,) or offsets.device != dev
+                                or not offsets.is_contiguous()):
+        raise ValueError(f"offsets must be a contiguous int32 tensor [{E + 1}] on {dev}")
+    if out is None:
+        make = torch.empty if offsets is None else torch.zeros
+        out = make(M, N, dtype=dtype, device=dev)
+    if out.dtype not in _LM_DT:
+        raise TypeError(f"fp32 or bf16 expected, got {out.dtype}")
+    if out.shape != (M, N) or (N > 1 and out.stride(1) != 1) or (M > 1 and out.stride(0) < N):
+        raise ValueError(f"out must be [{M}, {N}] with whole rows")
+    if w.codes.device != dev or out.device != dev or (workspace is not None and workspace.device != dev):
+        raise ValueError(f"all tensors must be on {dev}")
+    with torch.cuda.device(dev):
+        ws = mx4_gemm_workspace(dev) if workspace is None else workspace
+        lmoe_mx4_gemm(a.codes, a.scales, M, w.codes, w.scales, N, K, offsets, E, _LM_DT[out.dtype], out,
+                      out.stride(0) if M > 1 else N, ws, ws.numel() * ws.element_size(), _on(dev, stream))
+    return out
 
 
 class LatentMoE:

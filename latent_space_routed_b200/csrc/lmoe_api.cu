@@ -531,6 +531,40 @@ lmoe_status lmoe_mx4_dequantize(const void *codes, const void *scales, int64_t r
     return LMOE_OK;
 }
 
+lmoe_status lmoe_mx4_gemm(const void *a_codes, const void *a_scales, int64_t M, const void *w_codes,
+                          const void *w_scales, int64_t N, int64_t K, const int32_t *offsets, int32_t E, int32_t dtype,
+                          void *out, int64_t ldo, void *workspace, size_t ws_bytes, void *stream)
+{
+    g_err.clear();
+    if (M < 0 || N < 0 || K < 0) return fail(LMOE_ERR_INVALID_ARG, "negative size");
+    if (dtype != LMOE_F32 && dtype != LMOE_BF16) return fail(LMOE_ERR_INVALID_ARG, "unknown dtype");
+    if (offsets && E < 1) return fail(LMOE_ERR_INVALID_ARG, "E=%d < 1 with offsets", E);
+    if (ldo < N) return fail(LMOE_ERR_INVALID_ARG, "ldo=%lld < N=%lld", (long long)ldo, (long long)N);
+    if (!workspace || ws_bytes < LMOE_MX4_GEMM_WORKSPACE_BYTES || (uintptr_t)workspace % 256)
+        return fail(LMOE_ERR_WORKSPACE, "needs %zu workspace bytes, 256-byte aligned",
+                    (size_t)LMOE_MX4_GEMM_WORKSPACE_BYTES);
+    if (offsets && E > 1024) return fail(LMOE_ERR_UNSUPPORTED, "E=%d > 1024", E);
+    if (M == 0 || N == 0) return LMOE_OK;
+    if (K == 0 || K % 64) return fail(LMOE_ERR_UNSUPPORTED, "K=%lld is not a positive multiple of 64", (long long)K);
+    const int64_t rows = (offsets ? E : 1) * N, most = 0x7fffffffLL;
+    if (M > most / 2 || K > most || N > most || rows > most || ((M + 127) / 128 + (offsets ? E : 0)) > most / ((N + 63) / 64))
+        return fail(LMOE_ERR_UNSUPPORTED, "sizes exceed 2^31");
+    if (!a_codes || !a_scales || !w_codes || !w_scales || !out) return fail(LMOE_ERR_INVALID_ARG, "NULL pointer");
+    if (((uintptr_t)a_codes | (uintptr_t)w_codes) & 15u)
+        return fail(LMOE_ERR_UNSUPPORTED, "codes must be 16-byte aligned");
+    if ((uintptr_t)out % (dtype == LMOE_BF16 ? 2 : 4)) return fail(LMOE_ERR_UNSUPPORTED, "out is misaligned");
+    const lmoe_status st = tc_check_device();
+    if (st != LMOE_OK) return fail(st, "4-bit products need an sm_100 device");
+    LMOE_CUDA(cudaMemsetAsync(workspace, 0, sizeof(int32_t), (cudaStream_t)stream));
+    Mx4GemmArgs g = {};
+    g.a_codes = (const uint8_t *)a_codes; g.a_scales = (const uint8_t *)a_scales; g.a_pitch = K / 32;
+    g.w_codes = (const uint8_t *)w_codes; g.w_scales = (const uint8_t *)w_scales; g.w_pitch = K / 32;
+    g.M = (int)M; g.N = (int)N; g.K = (int)K; g.E = offsets ? E : 1; g.offsets = offsets;
+    g.out = out; g.out_bf16 = dtype == LMOE_BF16; g.ldo = ldo;
+    LMOE_CUDA(launch_mx4_gemm(g, (int32_t *)workspace, (cudaStream_t)stream));
+    return LMOE_OK;
+}
+
 lmoe_status lmoe_workspace_size(const lmoe_handle *h, int64_t T, size_t *bytes)
 {
     g_err.clear();
@@ -1097,6 +1131,13 @@ lmoe_status lmoe_check_device(lmoe_handle *h, int64_t T, void *workspace, void *
         if (st != LMOE_OK) return st;
     }
     return check_status_word((char *)workspace + plan(h, T).status, (cudaStream_t)stream);
+}
+
+lmoe_status lmoe_mx4_gemm_check(void *workspace, void *stream)
+{
+    g_err.clear();
+    if (!workspace) return fail(LMOE_ERR_INVALID_ARG, "NULL argument");
+    return check_status_word((char *)workspace, (cudaStream_t)stream);
 }
 
 lmoe_status lmoe_check_device_host(lmoe_handle *h, int64_t T, void *workspace, void *stream)

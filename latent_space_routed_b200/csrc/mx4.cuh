@@ -15,4 +15,18 @@ cudaError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, i
 cudaError_t launch_mx4_pack_scales(const uint8_t *G, const uint8_t *U, uint8_t *out, int64_t nE, int F, int blocks,
                                    int64_t pitch, int ib, cudaStream_t s);
 
+// C [M, N] = A W^T of 4-bit matrices (mx4_gemm.cu); grouped when offsets != nullptr
+// (device [E + 1], W of expert e at rows e N).  K a multiple of 64, codes 16-byte
+// aligned; scale rows a_pitch / w_pitch bytes apart.
+struct Mx4GemmArgs {
+    const uint8_t *a_codes, *a_scales, *w_codes, *w_scales;
+    int64_t a_pitch, w_pitch;
+    int M, N, K, E;
+    const int32_t *offsets;
+    void *out;
+    int out_bf16;
+    int64_t ldo;
+};
+cudaError_t launch_mx4_gemm(const Mx4GemmArgs &g, int32_t *status, cudaStream_t s);
+
 }  // namespace lmoe
