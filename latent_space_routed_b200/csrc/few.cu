@@ -7,8 +7,8 @@
 // the order
 //
 //   router       4 rows of W_r                     -> r = sigmoid(W_r x), in 64 bits
-//   down         16 rows of W_down                 -> z
 //   route        (no weights) one token's top-k and p
+//   down         16 rows of W_down                 -> z
 //   shared gu    16 gate and 16 up rows            -> shared hidden
 //   routed gu    16 gate and 16 up rows of expert  -> hidden H of each of its slots
 //   shared down  32 rows of the first shared expert  -> fp32 partial of y
@@ -28,10 +28,10 @@
 //
 // Roles (15 warps, one block per SM):
 //   warps 0-7   consumers: products from shared memory, sums over the warps, epilogues.  Two
-//               teams of four warps, each with half of the ring, take the stages in turn: a stage costs a warp 500 to 700 cycles
-//               of latency (barrier, loads, products, release) against 700 of HBM time, and two
-//               stages at once keep the weight stream the only limit (all eight warps on each
-//               stage: 866 us against 712 without products, 8 tokens, d = 7168)
+//               teams of four warps, each with half of the ring.  An item is a run of sub-items (32
+//               rows, or 16); the teams take them in turn, each with its own barrier, so that one
+//               team's sums and epilogue overlap the other's products.  Where K is long (a
+//               sub-item above SPLIT_BYTES), an item is one sub-item and the teams halve its K
 //   warp 8      producer: one thread keeps a ring of 16 KB stages full, one TMA copy each (measured:
 //               one thread issuing 16 KB boxes streams 7.3 TB/s, as 8 KB boxes 6.4 TB/s).  A box is
 //               four 128-byte k-blocks of two groups of 16 rows (gate and up, or 32 rows), eight
@@ -72,6 +72,7 @@ constexpr int STAGE_BYTES = 16384, KBLK_BYTES = 2048;   // a k-block of 16 rows
 constexpr int SCALE_BYTES = 1024;                // 2 x 16 rows of 32 scales (1024 values)
 constexpr int MAX_STAGES = 12, QUEUE = 32, AHEAD = 3;
 constexpr int MAX_E = 1024;
+constexpr int SPLIT_BYTES = 160 * 1024, ITEM_BYTES = 256 * 1024, MAX_REPS = 8;
 constexpr int SMEM_MAX = 232448;
 
 enum Kind { ROUTER, DOWN, ROUTE, SHARED_GU, ROUTED_GU, SHARED_DOWN, ROUTED_DOWN, COMBINE, UP, END };
@@ -82,11 +83,11 @@ enum Ctl { C_STATUS = 0, C_TICKET = 32, C_ROUTER = 64, C_Z = 96, C_ROUTED = 128,
 
 struct Item {
     int kind;
-    int c1, c2;          // coordinates of the box: row (of its block), and block of rows (two groups)
+    int j0, reps;        // first sub-item of the matrix (of the expert, the half), and how many
+    int block0;          // first block of rows of the matrix (two groups)
     int kb0, nkb;        // first k-block (128 bytes of a row) in the matrix, and their number
     int ncol;            // columns of the product in use
-    int ti;              // touched-expert index, or half of the shared experts
-    int out0;            // first output row
+    int ti;              // touched-expert index, half of the shared experts, or token (route)
 };
 
 // A touched expert: its id, the tokens that selected it (a bit each) and its slots in token order.
@@ -293,7 +294,7 @@ struct RoleBarrier {
 };
 
 struct Shared {
-    uint32_t ring, scales, act, full, empty, act_full, act_empty, cons, load, red_free;   // shared-memory addresses
+    uint32_t ring, scales, act, full, empty, act_full, act_empty, cons, team, load, red_free;   // shared-memory addresses
     float *red;              // [RED_FLOATS]
     Touched *tab;
     uint32_t *mask;          // [MAX_E], the scheduler's
@@ -301,16 +302,13 @@ struct Shared {
     Item *queue;
     float *inv;              // [2 slots][8]: inverse of the activations' scale
     float *lred;             // loaders' sums [4]
-    // [0] abort, [1] items published, [3] sets of x issued, [26, 28) stages issued to each team; items passed: [16, 20) by each
-    // loader, [20] by the producer, [21] by the signaller, [22] by consumer warp 0;
-    // [24] items stored (x 8), [25] touched experts
+    // [0] abort, [1] items published, [3] sets of x issued, [25] touched experts, [26, 28) stages issued to each
+    // team; items passed: [16, 20) by each loader, [20] by the producer, [21] by the signaller; [32, 40) items
+    // finished by each consumer warp
     int *flags;
 };
 
 // ------------------------------------------------------------------ items
-struct Counts {
-    int router, down, shared_gu, routed_gu, shared_down, routed_down, combine, up, touched;
-};
 
 template <int WT> constexpr int k_elems() { return WT == W_F32 ? 32 : 64; }   // values per 128-byte k-block
 
@@ -328,47 +326,88 @@ struct Divisor {
     }
 };
 
+// Sub-items per item: pairs (one for each team) until an item has ITEM_BYTES, but
+// leaving every block about eight items of the phase; 1 where the teams halve K.
+__device__ __forceinline__ int reps_for(int sub_bytes, int subs)
+{
+    if (sub_bytes > SPLIT_BYTES) return 1;
+    const int most = min(MAX_REPS, ITEM_BYTES / sub_bytes) & ~1;
+    return max(2, min(most, subs / (8 * (int)gridDim.x) & ~1));
+}
+
 template <int WT>
 struct Decoder {
     static constexpr int KE = k_elems<WT>();
-    Divisor gu, sd, rd;      // items of one expert: routed gate/up, shared down, routed down
-    __device__ __forceinline__ explicit Decoder(const FewParams &p) : gu(p.f / 16), sd(p.d / 32), rd(p.l / 32) {}
+    int down_r, sgu_r, rgu_r, sd_r, rd_r, up_r;     // sub-items per item
+    int down_n, sgu_n, sd_n, up_n;                  // items of the phase (of a half)
+    Divisor rgu, rd;                                // items of one expert
+    int rgu_total, rd_total;
+    static __device__ __forceinline__ int row_bytes(int K, bool routed)
+    {
+        return WT == W_F32 ? 4 * K : WT == W_MX4 && routed ? K / 2 + K / 32 : 2 * K;
+    }
+    static __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+    __device__ __forceinline__ Decoder(const FewParams &p, int touched) : rgu(1), rd(1)
+    {
+        down_r = reps_for(16 * row_bytes(p.d, false), p.l / 16);
+        sgu_r = reps_for(32 * row_bytes(p.d, false), p.fs / 8);
+        rgu_r = reps_for(32 * row_bytes(p.l, true), touched * (p.f / 16));
+        sd_r = reps_for(32 * row_bytes(p.fs, false), p.d / 16);
+        rd_r = reps_for(32 * row_bytes(p.f, true), touched * (p.l / 32));
+        up_r = reps_for(16 * row_bytes(p.l, false), p.d / 16);
+        down_n = p.standard ? 0 : ceil_div(p.l / 16, down_r);
+        sgu_n = ceil_div(p.fs / 8, sgu_r);
+        sd_n = ceil_div(p.d / 32, sd_r);
+        up_n = p.standard ? 0 : ceil_div(p.d / 16, up_r);
+        rgu = Divisor(ceil_div(p.f / 16, rgu_r));
+        rd = Divisor(ceil_div(p.l / 32, rd_r));
+        rgu_total = touched * rgu.d;
+        rd_total = touched * rd.d;
+    }
+    __device__ __forceinline__ int router_n(const FewParams &p) const { return (p.E + 3) / 4; }
+    __device__ __forceinline__ int combine_n(const FewParams &p) const { return p.l / 32; }
+    // Tickets that need no selection.
+    __device__ __forceinline__ int fixed(const FewParams &p) const { return router_n(p) + p.T + down_n + sgu_n; }
 
     // The item of ticket `tk`; kind END past the last.
-    __device__ __forceinline__ Item operator()(const FewParams &p, const Counts &n, const Touched *tab, unsigned tk) const
+    __device__ __forceinline__ Item operator()(const FewParams &p, const Touched *tab, unsigned tk) const
     {
-        Item it = {END, 0, 0, 0, 0, p.T, 0, 0};
-        int i = (int)tk;
-        if (i < n.router) {
-            it.kind = ROUTER; it.c1 = it.out0 = 4 * i; it.nkb = p.d / 32;
-        } else if ((i -= n.router) < n.down) {
-            it.kind = DOWN; it.c1 = it.out0 = 16 * i; it.nkb = p.d / KE;
-        } else if ((i -= n.down) < p.T) {
-            it.kind = ROUTE; it.ti = i;
-        } else if ((i -= p.T) < n.shared_gu) {      // gate and up rows interleaved in blocks of 64
-            it.kind = SHARED_GU; it.out0 = 16 * i; it.nkb = p.d / KE;
-            it.c1 = 16 * (i & 3); it.c2 = 2 * (i >> 2);
-        } else if ((i -= n.shared_gu) < n.routed_gu) {
-            it.kind = ROUTED_GU; it.ti = gu.div(i);
-            const int j = i - it.ti * gu.d;
-            it.out0 = 16 * j;
-            it.nkb = WT == W_MX4 ? (p.l + 255) / 256 : p.l / KE;
-            it.c1 = 16 * (j & 3); it.c2 = tab[it.ti].expert * (p.f / 32) + 2 * (j >> 2);
-        } else if ((i -= n.routed_gu) < sd.d || (i >= sd.d + n.routed_down && i < 2 * sd.d + n.routed_down)) {
-            it.kind = SHARED_DOWN; it.ti = i >= sd.d;
-            it.out0 = 32 * (it.ti ? i - sd.d - n.routed_down : i); it.c2 = it.out0 / 16;
-            it.nkb = p.fs / KE; it.kb0 = it.ti * it.nkb;
-        } else if ((i -= sd.d) < n.routed_down) {
-            it.kind = ROUTED_DOWN; it.ti = rd.div(i);
-            it.out0 = 32 * (i - it.ti * rd.d);
-            it.c2 = (tab[it.ti].expert * p.l + it.out0) / 16;
-            it.nkb = WT == W_MX4 ? (p.f + 255) / 256 : p.f / KE;
-            it.ncol = __popc((unsigned)tab[it.ti].mask);
-        } else if ((i -= n.routed_down + sd.d) < n.combine) {
-            it.kind = COMBINE; it.out0 = 32 * i;
-        } else if ((i -= n.combine) < n.up) {
-            it.kind = UP; it.c1 = it.out0 = 16 * i; it.nkb = p.l / KE; it.kb0 = 2 * p.fs / KE;
+        Item it = {END, 0, 1, 0, 0, 0, p.T, 0};
+        int i = (int)tk, per = 0;
+        if (i < router_n(p)) {
+            it.kind = ROUTER; it.j0 = i; it.nkb = p.d / 32;
+            return it;
         }
+        if ((i -= router_n(p)) < p.T) {
+            it.kind = ROUTE; it.ti = i;
+            return it;
+        }
+        if ((i -= p.T) < down_n) {
+            it.kind = DOWN; it.reps = down_r; it.nkb = p.d / KE; per = p.l / 16;
+        } else if ((i -= down_n) < sgu_n) {
+            it.kind = SHARED_GU; it.reps = sgu_r; it.nkb = p.d / KE; per = p.fs / 8;
+        } else if ((i -= sgu_n) < rgu_total) {
+            it.kind = ROUTED_GU; it.ti = rgu.div(i); i -= it.ti * rgu.d;
+            it.reps = rgu_r; it.nkb = WT == W_MX4 ? (p.l + 255) / 256 : p.l / KE; per = p.f / 16;
+            it.block0 = tab[it.ti].expert * (p.f / 32);
+        } else if ((i -= rgu_total) < sd_n || (i >= sd_n + rd_total && i < 2 * sd_n + rd_total)) {
+            it.kind = SHARED_DOWN; it.ti = i >= sd_n; i -= it.ti ? sd_n + rd_total : 0;
+            it.reps = sd_r; it.nkb = p.fs / KE; it.kb0 = it.ti * it.nkb; per = p.d / 32;
+        } else if ((i -= sd_n) < rd_total) {
+            it.kind = ROUTED_DOWN; it.ti = rd.div(i); i -= it.ti * rd.d;
+            it.reps = rd_r; it.nkb = WT == W_MX4 ? (p.f + 255) / 256 : p.f / KE; per = p.l / 32;
+            it.block0 = tab[it.ti].expert * (p.l / 16);
+            it.ncol = __popc((unsigned)tab[it.ti].mask);
+        } else if ((i -= rd_total + sd_n) < combine_n(p)) {
+            it.kind = COMBINE; it.j0 = i;
+            return it;
+        } else if ((i -= combine_n(p)) < up_n) {
+            it.kind = UP; it.reps = up_r; it.nkb = p.l / KE; it.kb0 = 2 * p.fs / KE; per = p.d / 16;
+        } else {
+            return it;
+        }
+        it.j0 = i * it.reps;
+        it.reps = min(it.reps, per - it.j0);
         return it;
     }
 };
@@ -380,11 +419,34 @@ __device__ __forceinline__ bool two_groups(int kind)
 }
 // k-blocks per stage: 4, 8 or 32
 __device__ __forceinline__ int stage_kb_log2(int kind) { return kind == ROUTER ? 5 : two_groups(kind) ? 2 : 3; }
-// Team of an item's first stage (its stages alternate): from the item alone, so that
-// the sums are the same in every run; items of a single stage alternate by their place.
-__device__ __forceinline__ int first_team(int kind, int out0)
+// Whether the teams halve the K of the item's one sub-item.
+template <int WT>
+__device__ __forceinline__ bool splits_k(const FewParams &p, const Item &it)
 {
-    return (out0 >> (kind == ROUTER ? 2 : kind == SHARED_DOWN || kind == ROUTED_DOWN ? 5 : 4)) & 1;
+    if (it.kind == ROUTER) return true;
+    const int K = it.kind == DOWN || it.kind == SHARED_GU ? p.d : it.kind == SHARED_DOWN ? p.fs
+                  : it.kind == ROUTED_DOWN ? p.f : p.l;
+    const bool routed = it.kind == ROUTED_GU || it.kind == ROUTED_DOWN;
+    return Decoder<WT>::row_bytes(K, routed) * (it.kind == DOWN || it.kind == UP ? 16 : 32) > SPLIT_BYTES;
+}
+// First output row of a sub-item.
+__device__ __forceinline__ int out_row(int kind, int j)
+{
+    return j * (kind == ROUTER ? 4 : kind == SHARED_DOWN || kind == ROUTED_DOWN ? 32 : 16);
+}
+// Coordinates of a sub-item's boxes: row (of its block), block of rows.
+__device__ __forceinline__ void box_at(const Item &it, int j, int *c1, int *c2)
+{
+    if (it.kind == SHARED_GU || it.kind == ROUTED_GU) {     // gate and up rows in blocks of 64
+        *c1 = 16 * (j & 3);
+        *c2 = it.block0 + 2 * (j >> 2);
+    } else if (it.kind == SHARED_DOWN || it.kind == ROUTED_DOWN) {
+        *c1 = 0;
+        *c2 = it.block0 + 2 * j;
+    } else {
+        *c1 = out_row(it.kind, j);
+        *c2 = 0;
+    }
 }
 __device__ __forceinline__ int chunks(const Item &it)
 {
@@ -396,15 +458,15 @@ __device__ __forceinline__ int chunks(const Item &it)
 // Partial products of an item: per warp two groups of 16 rows x 8 columns, the groups
 // RED_GROUP floats apart (16 more than a group, so that both are read without conflicts).
 constexpr int RED_GROUP = 144, RED_WARP = 2 * RED_GROUP, RED_FLOATS = CONSUMERS * RED_WARP;
-// Sum over the warps of one cell; `packed`: the lo terms' sums are four columns further.
-__device__ __forceinline__ float red_sum(const float *cell, bool packed)
+// Sum over n warps of one cell; `packed`: the lo terms' sums are four columns further.
+__device__ __forceinline__ float red_sum(const float *cell, int n, bool packed)
 {
     float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < CONSUMERS; ++w) v += cell[w * RED_WARP];
+#pragma unroll 4
+    for (int w = 0; w < n; ++w) v += cell[w * RED_WARP];
     if (packed)
-#pragma unroll
-        for (int w = 0; w < CONSUMERS; ++w) v += cell[w * RED_WARP + 4];
+#pragma unroll 4
+        for (int w = 0; w < n; ++w) v += cell[w * RED_WARP + 4];
     return v;
 }
 
@@ -495,10 +557,11 @@ __device__ __forceinline__ void store_token(void *x, int64_t i, float v)
 // keys, four per load; the low words and the index decide only between equal high
 // words (rare).  A place below k selects.  The loops stay rolled: few blocks run this
 // once per call, so its instructions come from L2, and an unrolled top-k (32
-// registers of keys per lane) spent 50 us of its 2 us fetching them.
+// registers of keys per lane) took 50 us, nearly all of it fetching them.  real = false: the same
+// on whatever the scores' memory holds, without writing anything.
 template <int WT>
 __device__ __noinline__ RoleBarrier route_item(const FewParams &p, int t, uint32_t *hi, double *rsel, RoleBarrier bar,
-                                               int warp, int lane)
+                                               int warp, int lane, bool real)
 {
     uint32_t *lo = hi + MAX_E;
     const int tid = warp * 32 + lane;
@@ -522,12 +585,12 @@ __device__ __noinline__ RoleBarrier route_item(const FewParams &p, int t, uint32
             ahead += (h.x > mine) + (h.y > mine) + (h.z > mine) + (h.w > mine);
             same += (h.x == mine) + (h.y == mine) + (h.z == mine) + (h.w == mine);
         }
-        if (same > 1 && ahead < p.k)
+        if (real && same > 1 && ahead < p.k)
 #pragma unroll 1
             for (int q = 0; q < p.E; ++q)
                 ahead += hi[q] == mine && (lo[q] > lo[e] || (lo[q] == lo[e] && q < e));
         if (ahead < p.k) {
-            p.sel[t * p.k + ahead] = e;
+            if (real) p.sel[t * p.k + ahead] = e;
             rsel[ahead] = __ldcg(r + e);
         }
     }
@@ -540,8 +603,10 @@ __device__ __noinline__ RoleBarrier route_item(const FewParams &p, int t, uint32
 #pragma unroll 1
         for (int j = lane; j < p.k; j += 32) {
             const float pv = (float)(rsel[j] / sum);
-            p.p32[t * p.k + j] = pv;
-            store_token<WT>(p.p_out, t * p.k + j, pv);
+            if (real) {
+                p.p32[t * p.k + j] = pv;
+                store_token<WT>(p.p_out, t * p.k + j, pv);
+            }
         }
     } else if (warp == 1 && WT == W_MX4 && p.standard) {   // the routed experts read x itself: its largest magnitude
         float m = 0.f;
@@ -549,20 +614,21 @@ __device__ __noinline__ RoleBarrier route_item(const FewParams &p, int t, uint32
         for (int c = lane; c < p.d; c += 32) m = fmaxf(m, fabsf(token_value<WT>(p.x, (int64_t)t * p.d + c)));
 #pragma unroll 1
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (lane == 0) p.ctl[C_AMAX_X + t] = __float_as_uint(m);
+        if (lane == 0 && real) p.ctl[C_AMAX_X + t] = __float_as_uint(m);
     }
     return bar;
 }
 
 // The touched experts in ascending order with their slots, from the selection of
 // all tokens: every block's scheduler builds its own.  mask [MAX_E]: the tokens that
-// selected an expert; returns the number of touched experts.
+// selected an expert; returns the number of touched experts.  A first run on an unwritten
+// selection (any numbers) stays inside both arrays.
 __device__ __noinline__ int touched_experts(const FewParams &p, uint32_t *mask, Touched *tab, int lane)
 {
     constexpr unsigned FULL = 0xffffffffu;
     const int S = p.T * p.k;
 #pragma unroll 1
-    for (int e = lane; e < p.E; e += 32) mask[e] = 0u;
+    for (int e = lane; e < MAX_E; e += 32) mask[e] = 0u;
     __syncwarp();
 #pragma unroll 4
     for (int i = lane; i < S; i += 32) atomicOr(mask + (__ldcg(p.sel + i) & (MAX_E - 1)), 1u << (i / p.k));
@@ -595,7 +661,7 @@ __device__ __noinline__ int touched_experts(const FewParams &p, uint32_t *mask, 
 template <int WT>
 __device__ __forceinline__ void combine_item(const FewParams &p, const Item &it, int warp, int lane)
 {
-    const int t = warp, c = it.out0 + lane;
+    const int t = warp, c = 32 * it.j0 + lane;
     if (t < p.T) {
         const float *src = p.ysl + (int64_t)t * p.k * p.l + c;
         float u = 0.f;
@@ -617,7 +683,7 @@ __device__ __forceinline__ void combine_item(const FewParams &p, const Item &it,
             float ss = u * u;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (lane == 0) p.ssq[t * (p.l / 32) + it.out0 / 32] = ss;
+            if (lane == 0) p.ssq[t * (p.l / 32) + it.j0] = ss;
         }
     }
 }
@@ -641,7 +707,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
     sh.mask = reinterpret_cast<uint32_t *>(g + o); o += 4 * MAX_E;
     sh.rsel = reinterpret_cast<double *>(g + o); o += 8 * 64;
     sh.queue = reinterpret_cast<Item *>(g + o); o += sizeof(Item) * QUEUE;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(g + o); o += 8 * (2 * MAX_STAGES + 8);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(g + o); o += 8 * (2 * MAX_STAGES + 12);
     sh.inv = reinterpret_cast<float *>(g + o); o += 64;
     sh.lred = reinterpret_cast<float *>(g + o); o += 64;
     sh.flags = reinterpret_cast<int *>(g + o);
@@ -651,7 +717,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
     sh.act_empty = sh.act_full + 16u;
     sh.cons = sh.act_empty + 16u;
     sh.load = sh.cons + 8u;
-    sh.red_free = sh.load + 8u;
+    sh.team = sh.load + 8u;
+    sh.red_free = sh.team + 16u;
     volatile int *abort = sh.flags;
     volatile int *published = sh.flags + 1, *passed = sh.flags + 16;
 
@@ -668,29 +735,19 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
         }
         mbar_init(sh.cons, CONSUMERS);
         mbar_init(sh.load, LOADERS);
-        mbar_init(sh.red_free, CONSUMERS);
-        for (int i = 0; i < 32; ++i) sh.flags[i] = 0;
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(sh.team + 8u * t, CONSUMERS / 2);
+            mbar_init(sh.red_free + 8u * t, CONSUMERS / 2);
+        }
+        for (int i = 0; i < 48; ++i) sh.flags[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     __syncthreads();
 
-    Counts n;
-    n.router = (p.E + 3) / 4;
-    n.down = p.standard ? 0 : p.l / 16;
-    n.shared_gu = 2 * p.fs / 16;
-    n.shared_down = 2 * (p.d / 32);
-    n.combine = p.l / 32;
-    n.up = p.standard ? 0 : p.d / 16;
-    n.touched = n.routed_gu = n.routed_down = 0;
     auto give_up = [&](int code) {
         atomicOr(p.ctl + C_STATUS, (unsigned)code);
         *abort = 1;
-    };
-    auto with_touched = [&](int touched) {
-        n.touched = touched;
-        n.routed_gu = touched * (p.f / 16);
-        n.routed_down = touched * (p.l / 32);
     };
 
     if (warp == CONSUMERS) {
@@ -706,7 +763,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 if (it.kind == END) break;
                 if (weightless(it.kind)) continue;
                 const int nc = chunks(it), kb = 1 << stage_kb_log2(it.kind);
-                const bool two = two_groups(it.kind);
+                const bool two = two_groups(it.kind), split = splits_k<WT>(p, it);
                 const bool mx4 = WT == W_MX4 && (it.kind == ROUTED_GU || it.kind == ROUTED_DOWN);
                 const uint32_t bytes = STAGE_BYTES + (mx4 ? SCALE_BYTES : 0);
                 const CUtensorMap *map = it.kind == ROUTER        ? &maps.router
@@ -717,27 +774,34 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                                          : it.kind == ROUTED_DOWN ? &maps.routed_down
                                                                   : &maps.up;
                 const CUtensorMap *smap = it.kind == ROUTED_GU ? &maps.routed_gu_scales : &maps.routed_down_scales;
-                const int first = first_team(it.kind, it.out0);
-                for (int c = 0; c < nc; ++c) {
-                    const int team = (c ^ first) & 1, s = team ? slot1 : slot0;
-                    const uint32_t fb = sh.full + 8u * s;
-                    if (!(ok = mbar_wait(sh.empty + 8u * s, (team ? ph1 : ph0) ^ 1u, abort))) break;
-                    mbar_expect_tx(fb, bytes);
-                    const uint32_t dst = sh.ring + (uint32_t)s * STAGE_BYTES;
-                    if (two) tma_load_4d(dst, map, fb, it.c1, it.c2, it.kb0 + c * kb);
-                    else tma_load_3d(dst, map, fb, it.c1, it.kb0 + c * kb);
-                    if (mx4) tma_load_3d_at(sh.scales + (uint32_t)s * SCALE_BYTES, smap, fb, 32 * c, it.c1, it.c2);
-                    if (team) {
-                        sh.flags[27] = ++issued1;
-                        if (++slot1 == S) {
-                            slot1 = half;
-                            ph1 ^= 1u;
-                        }
-                    } else {
-                        sh.flags[26] = ++issued0;
-                        if (++slot0 == half) {
-                            slot0 = 0;
-                            ph0 ^= 1u;
+                // stages in the order in which the teams take them: chunk by chunk of a pair of sub-items
+                for (int r = 0; r < it.reps && ok; r += 2) {
+                    int c1[2], c2[2];
+                    box_at(it, it.j0 + r, &c1[0], &c2[0]);
+                    box_at(it, it.j0 + r + 1, &c1[1], &c2[1]);
+                    const bool pair = !split && r + 1 < it.reps;
+                    for (int i = 0; i < (pair ? 2 * nc : nc) && ok; ++i) {
+                        const int team = split || pair ? i & 1 : 0, c = pair ? i >> 1 : i;
+                        const int s = team ? slot1 : slot0, x1 = pair && team ? c1[1] : c1[0], x2 = pair && team ? c2[1] : c2[0];
+                        const uint32_t fb = sh.full + 8u * s;
+                        if (!(ok = mbar_wait(sh.empty + 8u * s, (team ? ph1 : ph0) ^ 1u, abort))) break;
+                        mbar_expect_tx(fb, bytes);
+                        const uint32_t dst = sh.ring + (uint32_t)s * STAGE_BYTES;
+                        if (two) tma_load_4d(dst, map, fb, x1, x2, it.kb0 + c * kb);
+                        else tma_load_3d(dst, map, fb, x1, it.kb0 + c * kb);
+                        if (mx4) tma_load_3d_at(sh.scales + (uint32_t)s * SCALE_BYTES, smap, fb, 32 * c, x1, x2);
+                        if (team) {
+                            sh.flags[27] = ++issued1;
+                            if (++slot1 == S) {
+                                slot1 = half;
+                                ph1 ^= 1u;
+                            }
+                        } else {
+                            sh.flags[26] = ++issued0;
+                            if (++slot0 == half) {
+                                slot0 = 0;
+                                ph0 ^= 1u;
+                            }
                         }
                     }
                 }
@@ -746,34 +810,42 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
         }
     } else if (warp == CONSUMERS + 1) {
         // ------------------------------------------------------------ scheduler
-        const Decoder<WT> item(p);
+        Decoder<WT> item(p, 0);
+        const unsigned fixed = (unsigned)item.fixed(p);        // tickets that need no selection
         unsigned next = 0;
+        int touched = 0;
         if (lane == 0) next = atomicAdd(p.ctl + C_TICKET, 1u);
-        const unsigned fixed = (unsigned)(n.router + n.down + p.T + n.shared_gu);   // tickets that need no selection
         for (int q = 0;; ++q) {
             const unsigned tk = __shfl_sync(0xffffffffu, next, 0);
             int good = 1;
-            if (tk >= fixed && n.touched == 0) {
+            if (tk >= fixed && touched == 0) {
+                // a first run on whatever is there, while the selection is not: its instructions are here then
+                touched_experts(p, sh.mask, sh.tab, lane);
                 if (lane == 0) good = wait_count(p.ctl, C_ROUTED, (unsigned)p.T, abort);
                 good = __shfl_sync(0xffffffffu, good, 0);
                 if (!good) {
                     if (lane == 0) give_up(0x10);
                     break;
                 }
-                with_touched(touched_experts(p, sh.mask, sh.tab, lane));
-                if (lane == 0) sh.flags[25] = n.touched;
+                touched = touched_experts(p, sh.mask, sh.tab, lane);
+                item = Decoder<WT>(p, touched);
+                if (lane == 0) sh.flags[25] = touched;
             }
-            const Item it = item(p, n, sh.tab, tk);
-            if (lane < 2 && (it.kind == ROUTED_GU || it.kind == ROUTED_DOWN)) {
-                const int64_t row = it.kind == ROUTED_GU ? 64 * (int64_t)(it.c2 + lane) + it.c1 : 16 * (int64_t)(it.c2 + lane);
-                prefetch_l2((it.kind == ROUTED_GU ? p.wgu : p.wd) + row * (it.kind == ROUTED_GU ? p.gu_row : p.d_row));
+            const Item it = item(p, sh.tab, tk);
+            if (it.kind == ROUTED_GU || it.kind == ROUTED_DOWN) {
+                int c1, c2;
+                box_at(it, it.j0 + lane, &c1, &c2);
+                if (lane < it.reps)
+                    prefetch_l2((it.kind == ROUTED_GU ? p.wgu + (64 * (int64_t)c2 + c1) * p.gu_row
+                                                      : p.wd + 16 * (int64_t)c2 * p.d_row));
             }
             if (lane == 0) {
-                if (it.kind != END) next = atomicAdd(p.ctl + C_TICKET, 1u);   // used in the next round
                 // not far ahead of the producer, and the entry's previous item behind every reader
                 const long long t0 = clock64();
-                for (int r = 0; r < LOADERS + 3 && good; ++r)
-                    while (q - passed[r] >= (r == LOADERS ? AHEAD : QUEUE - 2) && good) {
+                const volatile int *finished = sh.flags + 32;
+                for (int r = 0; r < LOADERS + 2 + CONSUMERS && good; ++r)
+                    while (q - (r < LOADERS + 2 ? passed[r] : finished[r - LOADERS - 2]) >= (r == LOADERS ? AHEAD : QUEUE) &&
+                           good) {
                         __nanosleep(20);
                         if (*abort || clock64() - t0 > 2 * WAIT_LIMIT_CYCLES) good = 0;
                     }
@@ -781,6 +853,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                     sh.queue[q % QUEUE] = it;
                     __threadfence_block();
                     *published = q + 1;
+                    if (it.kind != END) next = atomicAdd(p.ctl + C_TICKET, 1u);   // used in the next round
                 } else {
                     give_up(0x10);
                 }
@@ -792,6 +865,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
         // ------------------------------------------------------------ loaders
         const int tid = threadIdx.x - 32 * (CONSUMERS + 2), lw = warp - CONSUMERS - 2;
         RoleBarrier bar = {sh.load, 0u, abort, true};
+        const Decoder<WT> item(p, 0);
         int set = 0, cur_key = -1, cur_seg = -1, ready = -1;   // ready: last kind whose inputs are complete
         bool ok = true;
         for (int q = 0; ok; ++q) {
@@ -808,7 +882,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
             if (weightless(it.kind)) continue;
             const ActPlan a = act_plan<WT>(p, it);
             const bool mx4 = WT == W_MX4 && (it.kind == ROUTED_GU || it.kind == ROUTED_DOWN);
-            for (int seg = 0; seg < a.nseg && ok; ++seg) {
+            const int sets = a.nseg == 1 ? 1 : a.nseg * ((it.reps + 1) / 2);     // segments again for every pair
+            for (int i = 0, seg = 0; i < sets && ok; ++i, seg = seg + 1 == a.nseg ? 0 : seg + 1) {
                 if (a.key == cur_key && seg == cur_seg) continue;
                 cur_key = a.key;
                 cur_seg = seg;
@@ -816,15 +891,15 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 if (lane == 0) {
                     good = mbar_wait(sh.act_empty + 8u * slot, (uint32_t)((set >> 1) & 1) ^ 1u, abort);
                     if (good && it.kind != ready) {          // the items that write these values
-                        if (it.kind == ROUTED_GU && !p.standard) good = wait_count(p.ctl, C_Z, n.down, abort);
+                        if (it.kind == ROUTED_GU && !p.standard) good = wait_count(p.ctl, C_Z, (unsigned)item.down_n, abort);
                         // (the failure-detection test waits for one count too many)
                         if (it.kind == SHARED_DOWN)
-                            good = wait_count(p.ctl, C_HS, n.shared_gu + (p.stall_test ? 1u : 0u), abort);
+                            good = wait_count(p.ctl, C_HS, (unsigned)item.sgu_n + (p.stall_test ? 1u : 0u), abort);
                         if (it.kind == ROUTED_DOWN)
-                            good = wait_count(p.ctl, C_H, (unsigned)sh.flags[25] * (p.f / 16), abort);
+                            good = wait_count(p.ctl, C_H, (unsigned)Decoder<WT>(p, sh.flags[25]).rgu_total, abort);
                         if (it.kind == UP)
-                            good = wait_count(p.ctl, C_U, n.combine, abort) &&
-                                   wait_count(p.ctl, C_PART, n.shared_down, abort);
+                            good = wait_count(p.ctl, C_U, (unsigned)item.combine_n(p), abort) &&
+                                   wait_count(p.ctl, C_PART, 2u * item.sd_n, abort);
                     }
                 }
                 ready = it.kind;
@@ -906,14 +981,15 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
         }
     } else if (warp < CONSUMERS) {
         // ------------------------------------------------------------ consumers
-        RoleBarrier bar = {sh.cons, 0u, abort, true};
-        const int team = warp >> 2, sub = warp & 3;      // this team takes every second stage
+        const int team = warp >> 2, sub = warp & 3;
         const int gid = lane >> 2, c4 = lane & 3;
+        RoleBarrier bar = {sh.cons, 0u, abort, true};                     // all eight warps
+        RoleBarrier tbar = {sh.team + 8u * team, 0u, abort, true};        // the team's four
+        const Decoder<WT> item(p, 0);
         int s = team ? half : 0;                         // slot and phase of this team's next stage
         uint32_t ph = 0, red_ph = 1;
         int set = -1, cur_key = -1, cur_seg = -1;
         bool ok = true;
-        // Products with the team's next stage follow; then this warp is done with it.
         auto full = [&]() -> bool { return warp_wait(sh.full + 8u * s, ph, abort); };
         auto release = [&]() {
             __syncwarp();
@@ -923,30 +999,35 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 ph ^= 1u;
             }
         };
-        auto done = [&]() {              // this warp's part of the item is stored
-            __syncwarp();
-            if (lane == 0) red_shared_release(smem_u32(sh.flags + 24), 1u);
-        };
         for (int q = 0;; ++q) {
-            if (threadIdx.x == 0) passed[LOADERS + 2] = q;
             if (!(ok = __all_sync(0xffffffffu, wait_published(published, q, abort)))) break;
+            auto done = [&]() {              // this warp's part of the item is stored
+                __syncwarp();
+                if (lane == 0) sts_release(smem_u32(sh.flags + 32 + warp), (unsigned)(q + 1));
+            };
             const Item it = sh.queue[q % QUEUE];
             const int kind = it.kind;
             if (kind == END) break;
             if (weightless(kind)) {
                 int good = 1;
+                if (kind == ROUTE) {
+                    // a first run on whatever is there, while the scores are not: its instructions are here then
+                    if (!(ok = bar.sync())) break;
+                    bar = route_item<WT>(p, it.ti, reinterpret_cast<uint32_t *>(sh.red), sh.rsel, bar, warp, lane, false);
+                    if (!(ok = bar.ok)) break;
+                }
                 if (lane == 0) {
                     if (kind == ROUTE) {
-                        good = wait_count(p.ctl, C_ROUTER, (unsigned)n.router, abort);
+                        good = wait_count(p.ctl, C_ROUTER, (unsigned)item.router_n(p), abort);
                     } else {
-                        good = wait_count(p.ctl, C_YS, (unsigned)sh.flags[25] * (p.l / 32), abort);
-                        if (good && p.standard) good = wait_count(p.ctl, C_PART, n.shared_down, abort);
+                        good = wait_count(p.ctl, C_YS, (unsigned)Decoder<WT>(p, sh.flags[25]).rd_total, abort);
+                        if (good && p.standard) good = wait_count(p.ctl, C_PART, 2u * item.sd_n, abort);
                     }
                 }
                 ok = __shfl_sync(0xffffffffu, good, 0) != 0 && bar.sync();
                 if (!ok) break;
                 if (kind == ROUTE) {
-                    bar = route_item<WT>(p, it.ti, reinterpret_cast<uint32_t *>(sh.red), sh.rsel, bar, warp, lane);
+                    bar = route_item<WT>(p, it.ti, reinterpret_cast<uint32_t *>(sh.red), sh.rsel, bar, warp, lane, true);
                     if (!(ok = bar.ok)) break;
                 } else {
                     combine_item<WT>(p, it, warp, lane);
@@ -956,7 +1037,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
             }
 
             const ActPlan a = act_plan<WT>(p, it);
-            const bool two = two_groups(kind);
+            const bool two = two_groups(kind), split = splits_k<WT>(p, it);
             const int nc = chunks(it), nkb = it.nkb;
             const uint32_t plane = (uint32_t)(it.ncol * a.stride);
             // Four columns or fewer of two terms: hi in columns 0-3, lo in 4-7 of one product
@@ -981,32 +1062,40 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 act = sh.act + (uint32_t)((set & 1) * p.slot_bytes);
                 return true;
             };
-            // The item's stages: body(c, k0) for this team's ones, k0 the segment's first value.  body
-            // calls release() as soon as its tiles are in registers, before the products.
-            auto stages = [&](auto body) -> bool {
-                int c = first_team(kind, it.out0) ^ team;      // this team's first stage
+            // The stages of this team's sub-item (`mine`: it has one in this pair): body(c, k0), k0 the
+            // segment's first value.  body calls release() as soon as its tiles are in registers, before
+            // the products.
+            auto stages = [&](bool mine, auto body) -> bool {
+                int c = split ? team : 0;
                 for (int seg = 0; seg < a.nseg; ++seg) {
                     if (!take(seg)) return false;
-                    const int end = seg + 1 < a.nseg ? ((seg + 1) * a.kseg) >> kshift : nc;
-                    for (; c < end; c += 2) {
+                    const int end = !mine ? 0 : seg + 1 < a.nseg ? ((seg + 1) * a.kseg) >> kshift : nc;
+                    for (; c < end; c += split ? 2 : 1) {
                         if (!full()) return false;
-                        body(c, seg * a.kseg);       // releases the stage once it has loaded what it needs
+                        body(c, seg * a.kseg);
                     }
                 }
                 return true;
             };
-            float *const mine = sh.red + warp * RED_WARP;
-            auto red_writable = [&]() -> bool {          // everyone has read the last item's sums
-                const bool good = warp_wait(sh.red_free, red_ph, abort);
+            float *const myred = sh.red + warp * RED_WARP;
+            auto red_writable = [&]() -> bool {          // the last sums in this warp's cells have been read
+                const bool good = warp_wait(sh.red_free + 8u * team, red_ph, abort);
                 red_ph ^= 1u;
                 return good;
+            };
+            auto red_read = [&]() {                      // this warp has read its sums
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(sh.red_free + 8u * team);
+                    if (split) mbar_arrive(sh.red_free + 8u * (team ^ 1));
+                }
             };
 
             if (kind == ROUTER) {
                 // ---- 4 rows, 64-bit products: lane (row, 4-value piece)
                 double acc[FEW_MAX_T] = {};
                 const int row = lane >> 3, piece = lane & 7;
-                ok = stages([&](int c, int k0) {
+                ok = stages(true, [&](int c, int k0) {
                     const uint32_t tile = sh.ring + (uint32_t)s * STAGE_BYTES + mytile;
 #pragma unroll 2
                     for (int i = 0; i < 8; ++i) {
@@ -1049,24 +1138,26 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                     }
                 if (!(ok = bar.sync())) break;
                 if (warp == 0) {
-                    const int e = it.out0 + (lane >> 3), t = lane & 7;
+                    const int e = 4 * it.j0 + (lane >> 3), t = lane & 7;
                     if (e < p.E && t < p.T) {
                         double v = 0.0;
                         for (int w = 0; w < CONSUMERS; ++w) v += rd[w * 32 + lane];
                         p.r64[(int64_t)t * p.E + e] = 1.0 / (1.0 + exp(-v));
                     }
-                    __syncwarp();
                 }
-                if (lane == 0) mbar_arrive(sh.red_free);
+                if (team == 0) red_read();
                 done();
                 continue;
             }
 
+            for (int r0 = 0; ok && r0 < it.reps; r0 += 2) {
+            const int rr = split ? 0 : r0 + team;          // this team's sub-item
+            const bool mine = rr < it.reps;
             if (WT == W_F32) {
                 // ---- fp32: lane (4-value piece, rows rq + 4 i); two tiles, of one k-block or of two
                 float acc[2][4][FEW_MAX_T] = {};
                 const int piece = lane & 7, rq = lane >> 3;
-                ok = stages([&](int c, int k0) {
+                ok = stages(mine, [&](int c, int k0) {
                     const uint32_t tile = sh.ring + (uint32_t)s * STAGE_BYTES + mytile;
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
@@ -1097,7 +1188,9 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                     }
                     release();
                 });
-                if (!ok || !(ok = red_writable())) break;
+                if (!ok) break;
+                if (!mine) continue;
+                if (!(ok = red_writable())) break;
 #pragma unroll
                 for (int t = 0; t < FEW_MAX_T; ++t)
                     if (t < it.ncol) {
@@ -1108,7 +1201,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
 #pragma unroll
                                 for (int off = 1; off < 8; off <<= 1)
                                     acc[g][i][t] += __shfl_xor_sync(0xffffffffu, acc[g][i][t], off);
-                                if (piece == 0) mine[g * RED_GROUP + (rq + 4 * i) * 8 + t] = acc[g][i][t];
+                                if (piece == 0) myred[g * RED_GROUP + (rq + 4 * i) * 8 + t] = acc[g][i][t];
                             }
                     }
             } else {
@@ -1123,7 +1216,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                     // them (a word) per lane
                     const int nblk = (kind == ROUTED_GU ? p.l : p.f) / 32;
                     const uint32_t mycol = column(gid) + 16u * c4;
-                    ok = stages([&](int c, int k0) {
+                    ok = stages(mine, [&](int c, int k0) {
                         const int kblk = c * 4 + sub;
                         const int nb = min(nblk - kblk * 8, 8);
                         if (nb > 0) {
@@ -1146,7 +1239,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                         piece[i] = mytile + (uint32_t)(lrow * 128 + (((2 * i + (lane >> 4)) ^ (lrow & 7)) << 4));
                     const bool lo_too = a.planes == 2 && !packed;
                     float acl[2][4] = {};
-                    ok = stages([&](int c, int k0) {
+                    ok = stages(mine, [&](int c, int k0) {
                         const uint32_t tile = sh.ring + (uint32_t)s * STAGE_BYTES;
                         const int kblk = two ? c * 4 + sub : c * 8 + 2 * sub;
                         if (kblk < nkb) {
@@ -1207,25 +1300,27 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                         acc[1][i] += acl[1][i];
                     }
                 }
-                if (!ok || !(ok = red_writable())) break;
+                if (!ok) break;
+                if (!mine) continue;
+                if (!(ok = red_writable())) break;
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
-                    float2 *r = reinterpret_cast<float2 *>(mine + g * RED_GROUP + gid * 8 + 2 * c4);
+                    float2 *r = reinterpret_cast<float2 *>(myred + g * RED_GROUP + gid * 8 + 2 * c4);
                     r[0] = make_float2(acc[g][0], acc[g][1]);
                     r[32] = make_float2(acc[g][2], acc[g][3]);
                 }
             }
 
-            // ---- sums over the warps, and what becomes of them: thread (row, token, group) of
-            // 16 x 8 x 2, the groups in neighbouring lanes.  What the epilogue reads from global
-            // memory is asked for before the barrier.
-            const int grp = threadIdx.x & 1, cell = threadIdx.x >> 1, row = cell >> 3, t = cell & 7;
-            const bool real = t < it.ncol;
-            const int r = it.out0 + (kind == SHARED_DOWN || kind == ROUTED_DOWN ? 16 * grp : 0) + row;
+            // ---- sums over the team's warps (over both teams' where they halved K, by team 0), and
+            // what becomes of them: thread (row, token) of 16 x 8, both groups of rows.  What the
+            // epilogue reads from global memory is asked for before the barrier.
+            const int cell = threadIdx.x & 127, row = cell >> 3, t = cell & 7;
+            const bool real = t < it.ncol && !(split && team);
+            const int r = out_row(kind, it.j0 + rr) + row;
             float add = 0.f;
             int slot = -1;
             if (kind == UP) {
-                if (real && grp == 0) {
+                if (real) {
                     const float *q2 = p.part + (int64_t)t * p.d + r;
                     add = __ldcg(q2) + __ldcg(q2 + (int64_t)p.T * p.d);
                 }
@@ -1236,63 +1331,72 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 }
             } else if (kind == ROUTED_GU) {
                 const unsigned mask = (unsigned)sh.tab[it.ti].mask;
-                if (mask >> t & 1u) slot = sh.tab[it.ti].slot[__popc(mask & ((1u << t) - 1u))];
+                if (real && (mask >> t & 1u)) slot = sh.tab[it.ti].slot[__popc(mask & ((1u << t) - 1u))];
             }
             const float back = mx4 && real ? sh.inv[8 * (set & 1) + t] : 1.f;
-            if (!(ok = bar.sync())) break;
-            const float v = red_sum(sh.red + grp * RED_GROUP + cell, packed && t < 4) * back;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(sh.red_free);
-            const float other = __shfl_xor_sync(0xffffffffu, v, 1);     // the other group's sum
+            if (!(ok = split ? bar.sync() : tbar.sync())) break;
+            if (split && team) break;                      // (its one sub-item)
+            const float *cells = sh.red + (split ? 0 : 4 * team) * RED_WARP + cell;
+            const int nw = split ? CONSUMERS : CONSUMERS / 2;
+            const float v0 = red_sum(cells, nw, packed && t < 4) * back;
+            const float v1 = red_sum(cells + RED_GROUP, nw, packed && t < 4) * back;
+            red_read();
             if (kind == SHARED_GU || kind == ROUTED_GU) {
-                const float h = grp == 0 ? glu_act(p.act, v, other, p.gate_cap, p.up_cap) : 0.f;
+                const float h = glu_act(p.act, v0, v1, p.gate_cap, p.up_cap);
                 if (kind == SHARED_GU) {
-                    if (real && grp == 0) p.hs[(int64_t)t * 2 * p.fs + r] = h;
+                    if (real) p.hs[(int64_t)t * 2 * p.fs + r] = h;
                 } else {
-                    if (slot >= 0 && grp == 0) p.H[(int64_t)slot * p.f + r] = h;
-                    if (WT == W_MX4) {      // rows of a warp: lane bit 4
+                    if (slot >= 0) p.H[(int64_t)slot * p.f + r] = h;
+                    if (WT == W_MX4) {      // rows of a warp: lane bits 3, 4
                         float m = slot >= 0 ? fabsf(h) : 0.f;
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                        if (lane < 16 && grp == 0 && slot >= 0) atomicMax(p.ctl + C_AMAX_H + slot, __float_as_uint(m));
+                        if (lane < 8 && slot >= 0) atomicMax(p.ctl + C_AMAX_H + slot, __float_as_uint(m));
                     }
                 }
             } else if (kind == DOWN) {
-                const float z = v + other;
-                if (real && grp == 0) p.z[(int64_t)t * p.l + r] = z;
+                const float z = v0 + v1;
+                if (real) p.z[(int64_t)t * p.l + r] = z;
                 if (WT == W_MX4) {
                     float m = real ? fabsf(z) : 0.f;
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                    if (lane < 16 && grp == 0 && real) atomicMax(p.ctl + C_AMAX_Z + t, __float_as_uint(m));
+                    if (lane < 8 && real) atomicMax(p.ctl + C_AMAX_Z + t, __float_as_uint(m));
                 }
             } else if (kind == UP) {
-                if (real && grp == 0) store_token<WT>(p.y, (int64_t)t * p.d + r, v + other + add);
+                if (real) store_token<WT>(p.y, (int64_t)t * p.d + r, v0 + v1 + add);
             } else if (kind == SHARED_DOWN) {
-                if (real) p.part[((int64_t)it.ti * p.T + t) * p.d + r] = v;
+                if (real) {
+                    float *q2 = p.part + ((int64_t)it.ti * p.T + t) * p.d + r;
+                    q2[0] = v0;
+                    q2[16] = v1;
+                }
             } else if (real) {
-                p.ysl[(int64_t)slot * p.l + r] = add * v;
+                float *q2 = p.ysl + (int64_t)slot * p.l + r;
+                q2[0] = add * v0;
+                q2[16] = add * v1;
             }
+            }
+            if (!ok) break;
             done();
         }
         if (!ok && lane == 0) give_up(0x8);
     } else {
         // ------------------------------------------------------------ signaller
-        // An item is stored once all eight warps have counted it: no warp counts the
-        // next item before every warp has passed that item's barrier, hence counted this one.
         if (lane == 0) {
-            unsigned counted = 0;
             bool ok = true;
             for (int q = 0; ok; ++q) {
                 passed[LOADERS + 1] = q;
                 if (!(ok = wait_published(published, q, abort))) break;
                 const int kind = sh.queue[q % QUEUE].kind;
                 if (kind == END) break;
-                counted += CONSUMERS;
-                const uint32_t word = smem_u32(sh.flags + 24);
+                const uint32_t word = smem_u32(sh.flags + 32);
                 const long long t1 = clock64();
-                while (lds_acquire(word) < counted && ok) {
-                    __nanosleep(20);
-                    if (*abort || clock64() - t1 > 2 * WAIT_LIMIT_CYCLES) ok = false;
-                }
+                for (int w = 0; w < CONSUMERS; ++w)
+                    while ((int)lds_acquire(word + 4 * w) <= q && ok) {
+                        __nanosleep(20);
+                        if (*abort || clock64() - t1 > 2 * WAIT_LIMIT_CYCLES) ok = false;
+                    }
                 if (!ok) break;
                 const int at = kind == ROUTER        ? C_ROUTER
                                : kind == ROUTE       ? C_ROUTED
@@ -1328,8 +1432,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
 // ------------------------------------------------------------------ host side
 size_t fixed_smem()
 {
-    return 1024 + 4 * RED_FLOATS + sizeof(Touched) * FEW_MAX_SLOTS + 4 * MAX_E + 8 * 64 + sizeof(Item) * QUEUE + 8 * (2 * MAX_STAGES + 8) +
-           64 + 64 + 128;
+    return 1024 + 4 * RED_FLOATS + sizeof(Touched) * FEW_MAX_SLOTS + 4 * MAX_E + 8 * 64 + sizeof(Item) * QUEUE + 8 * (2 * MAX_STAGES + 12) +
+ 64 + 64 + 192;
 }
 
 struct FewLayout {

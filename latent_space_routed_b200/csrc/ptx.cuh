@@ -102,9 +102,9 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 
 // ------------------------------------------------------------------ shared memory
 // Counters between the warps of a block.
-__device__ __forceinline__ void red_shared_release(uint32_t a, unsigned v)
+__device__ __forceinline__ void sts_release(uint32_t a, unsigned v)
 {
-    asm volatile("red.release.cta.shared.add.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+    asm volatile("st.release.cta.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 __device__ __forceinline__ unsigned lds_acquire(uint32_t a)
 {
