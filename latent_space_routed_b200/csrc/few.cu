@@ -7,7 +7,6 @@
 // the order
 //
 //   router       4 rows of W_r                     -> r = sigmoid(W_r x), in 64 bits
-//   route        (no weights) one token's top-k and p
 //   down         16 rows of W_down                 -> z
 //   shared gu    16 gate and 16 up rows            -> shared hidden
 //   routed gu    16 gate and 16 up rows of expert  -> hidden H of each of its slots
@@ -37,7 +36,9 @@
 //               four 128-byte k-blocks of two groups of 16 rows (gate and up, or 32 rows), eight
 //               k-blocks of 16 rows, or 32 of 4 rows (router)
 //   warp 9      scheduler: takes tickets and describes their items in a queue, at most two items
-//               ahead of the producer (its integer work per item would stall the copies)
+//               ahead of the producer (its integer work per item would stall the copies).  Once the
+//               router's rows are done it selects the experts of all tokens itself, in every block:
+//               the same work as reading another block's result would wait for
 //   warps 10-13 loaders: bring an item's activations from global memory into one of two
 //               shared-memory slots, in the form that the product wants, one set ahead
 //   warp 14     signaller: publishes finished items to the other blocks (the fence before the
@@ -75,11 +76,11 @@ constexpr int MAX_E = 1024;
 constexpr int SPLIT_BYTES = 160 * 1024, ITEM_BYTES = 256 * 1024, MAX_REPS = 8;
 constexpr int SMEM_MAX = 232448;
 
-enum Kind { ROUTER, DOWN, ROUTE, SHARED_GU, ROUTED_GU, SHARED_DOWN, ROUTED_DOWN, COMBINE, UP, END };
+enum Kind { ROUTER, DOWN, SHARED_GU, ROUTED_GU, SHARED_DOWN, ROUTED_DOWN, COMBINE, UP, END };
 
 // Words of the control area (zero at launch).
-enum Ctl { C_STATUS = 0, C_TICKET = 32, C_ROUTER = 64, C_Z = 96, C_ROUTED = 128, C_HS = 160, C_H = 192, C_PART = 224,
-           C_YS = 256, C_U = 288, C_AMAX_Z = 320, C_AMAX_X = 328, C_AMAX_H = 352, C_WORDS = C_AMAX_H + FEW_MAX_SLOTS };
+enum Ctl { C_STATUS = 0, C_TICKET = 32, C_ROUTER = 64, C_Z = 96, C_HS = 160, C_H = 192, C_PART = 224,
+           C_YS = 256, C_U = 288, C_AMAX_Z = 320, C_AMAX_H = 352, C_WORDS = C_AMAX_H + FEW_MAX_SLOTS };
 
 struct Item {
     int kind;
@@ -87,7 +88,7 @@ struct Item {
     int block0;          // first block of rows of the matrix (two groups)
     int kb0, nkb;        // first k-block (128 bytes of a row) in the matrix, and their number
     int ncol;            // columns of the product in use
-    int ti;              // touched-expert index, half of the shared experts, or token (route)
+    int ti;              // touched-expert index, or half of the shared experts
 };
 
 // A touched expert: its id, the tokens that selected it (a bit each) and its slots in token order.
@@ -95,7 +96,16 @@ struct Touched {
     int16_t expert, mask, slot[FEW_MAX_T];
 };
 
+// How the phases are cut into items (host side): sub-items per item (_r), items of the
+// phase, of a half or of an expert (_n).
+struct Plan {
+    int router_n, down_r, down_n, sgu_r, sgu_n, rgu_r, rgu_n, sd_r, sd_n, rd_r, rd_n, up_r, up_n, combine_n;
+    float rgu_inv, rd_inv;       // 1 / rgu_n, 1 / rd_n
+    uint32_t split;              // bit of a kind: the teams halve K
+};
+
 struct FewParams {
+    Plan n;
     int T, d, l, f, E, k, fs, act, standard;
     float gate_cap, up_cap, eps;
     const void *x;
@@ -104,7 +114,6 @@ struct FewParams {
     int32_t *sel;
     unsigned *ctl;
     double *r64;             // [T, E] biased scores' raw scores
-    float *p32;              // [T, k]
     float *z, *hs, *H, *part, *ysl, *u, *ssq;   // ssq: [T, l / 32] sums of squares of u
     int stages, slot_bytes, scales;
     const char *wgu, *wd;    // routed weights, and bytes of their rows
@@ -293,12 +302,20 @@ struct RoleBarrier {
     }
 };
 
+// Scratch of the selection, in shared memory (n_touched entries etc. by the call's sizes).
+struct Select {
+    uint32_t *hi, *mask;         // [E rounded up to 128]: score keys' high words; tokens and index of an expert
+    unsigned long long *cand;    // [64] keys of a token's selected
+    uint16_t *cand_e, *sel;      // [64] their experts; [T, k] experts in order
+    float *weight;               // [T, k]
+    Touched *tab;
+};
+
 struct Shared {
     uint32_t ring, scales, act, full, empty, act_full, act_empty, cons, team, load, red_free;   // shared-memory addresses
     float *red;              // [RED_FLOATS]
     Touched *tab;
-    uint32_t *mask;          // [MAX_E], the scheduler's
-    double *rsel;            // [64], of the route items
+    Select select;
     Item *queue;
     float *inv;              // [2 slots][8]: inverse of the activations' scale
     float *lred;             // loaders' sums [4]
@@ -312,123 +329,64 @@ struct Shared {
 
 template <int WT> constexpr int k_elems() { return WT == W_F32 ? 32 : 64; }   // values per 128-byte k-block
 
-// n / d for 0 <= n < 2^24 by a reciprocal (the quotient is off by one at most).
-struct Divisor {
-    int d;
-    float inv;
-    __device__ __forceinline__ explicit Divisor(int v) : d(v), inv(1.0f / (float)v) {}
-    __device__ __forceinline__ int div(int n) const
-    {
-        int q = (int)((float)n * inv);
-        q -= q * d > n;
-        q += (q + 1) * d <= n;
-        return q;
-    }
-};
-
-// Sub-items per item: pairs (one for each team) until an item has ITEM_BYTES, but
-// leaving every block about eight items of the phase; 1 where the teams halve K.
-__device__ __forceinline__ int reps_for(int sub_bytes, int subs)
+// n / d for 0 <= n < 2^24 by a reciprocal (whose quotient is off by one at most).
+__device__ __forceinline__ int divide(int n, int d, float inv)
 {
-    if (sub_bytes > SPLIT_BYTES) return 1;
-    const int most = min(MAX_REPS, ITEM_BYTES / sub_bytes) & ~1;
-    return max(2, min(most, subs / (8 * (int)gridDim.x) & ~1));
+    int q = (int)((float)n * inv);
+    q -= q * d > n;
+    q += (q + 1) * d <= n;
+    return q;
 }
 
+// The item of ticket `tk`; kind END past the last.
 template <int WT>
-struct Decoder {
-    static constexpr int KE = k_elems<WT>();
-    int down_r, sgu_r, rgu_r, sd_r, rd_r, up_r;     // sub-items per item
-    int down_n, sgu_n, sd_n, up_n;                  // items of the phase (of a half)
-    Divisor rgu, rd;                                // items of one expert
-    int rgu_total, rd_total;
-    static __device__ __forceinline__ int row_bytes(int K, bool routed)
-    {
-        return WT == W_F32 ? 4 * K : WT == W_MX4 && routed ? K / 2 + K / 32 : 2 * K;
-    }
-    static __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
-    __device__ __forceinline__ Decoder(const FewParams &p, int touched) : rgu(1), rd(1)
-    {
-        down_r = reps_for(16 * row_bytes(p.d, false), p.l / 16);
-        sgu_r = reps_for(32 * row_bytes(p.d, false), p.fs / 8);
-        rgu_r = reps_for(32 * row_bytes(p.l, true), touched * (p.f / 16));
-        sd_r = reps_for(32 * row_bytes(p.fs, false), p.d / 16);
-        rd_r = reps_for(32 * row_bytes(p.f, true), touched * (p.l / 32));
-        up_r = reps_for(16 * row_bytes(p.l, false), p.d / 16);
-        down_n = p.standard ? 0 : ceil_div(p.l / 16, down_r);
-        sgu_n = ceil_div(p.fs / 8, sgu_r);
-        sd_n = ceil_div(p.d / 32, sd_r);
-        up_n = p.standard ? 0 : ceil_div(p.d / 16, up_r);
-        rgu = Divisor(ceil_div(p.f / 16, rgu_r));
-        rd = Divisor(ceil_div(p.l / 32, rd_r));
-        rgu_total = touched * rgu.d;
-        rd_total = touched * rd.d;
-    }
-    __device__ __forceinline__ int router_n(const FewParams &p) const { return (p.E + 3) / 4; }
-    __device__ __forceinline__ int combine_n(const FewParams &p) const { return p.l / 32; }
-    // Tickets that need no selection.
-    __device__ __forceinline__ int fixed(const FewParams &p) const { return router_n(p) + p.T + down_n + sgu_n; }
-
-    // The item of ticket `tk`; kind END past the last.
-    __device__ __forceinline__ Item operator()(const FewParams &p, const Touched *tab, unsigned tk) const
-    {
-        Item it = {END, 0, 1, 0, 0, 0, p.T, 0};
-        int i = (int)tk, per = 0;
-        if (i < router_n(p)) {
-            it.kind = ROUTER; it.j0 = i; it.nkb = p.d / 32;
-            return it;
-        }
-        if ((i -= router_n(p)) < p.T) {
-            it.kind = ROUTE; it.ti = i;
-            return it;
-        }
-        if ((i -= p.T) < down_n) {
-            it.kind = DOWN; it.reps = down_r; it.nkb = p.d / KE; per = p.l / 16;
-        } else if ((i -= down_n) < sgu_n) {
-            it.kind = SHARED_GU; it.reps = sgu_r; it.nkb = p.d / KE; per = p.fs / 8;
-        } else if ((i -= sgu_n) < rgu_total) {
-            it.kind = ROUTED_GU; it.ti = rgu.div(i); i -= it.ti * rgu.d;
-            it.reps = rgu_r; it.nkb = WT == W_MX4 ? (p.l + 255) / 256 : p.l / KE; per = p.f / 16;
-            it.block0 = tab[it.ti].expert * (p.f / 32);
-        } else if ((i -= rgu_total) < sd_n || (i >= sd_n + rd_total && i < 2 * sd_n + rd_total)) {
-            it.kind = SHARED_DOWN; it.ti = i >= sd_n; i -= it.ti ? sd_n + rd_total : 0;
-            it.reps = sd_r; it.nkb = p.fs / KE; it.kb0 = it.ti * it.nkb; per = p.d / 32;
-        } else if ((i -= sd_n) < rd_total) {
-            it.kind = ROUTED_DOWN; it.ti = rd.div(i); i -= it.ti * rd.d;
-            it.reps = rd_r; it.nkb = WT == W_MX4 ? (p.f + 255) / 256 : p.f / KE; per = p.l / 32;
-            it.block0 = tab[it.ti].expert * (p.l / 16);
-            it.ncol = __popc((unsigned)tab[it.ti].mask);
-        } else if ((i -= rd_total + sd_n) < combine_n(p)) {
-            it.kind = COMBINE; it.j0 = i;
-            return it;
-        } else if ((i -= combine_n(p)) < up_n) {
-            it.kind = UP; it.reps = up_r; it.nkb = p.l / KE; it.kb0 = 2 * p.fs / KE; per = p.d / 16;
-        } else {
-            return it;
-        }
-        it.j0 = i * it.reps;
-        it.reps = min(it.reps, per - it.j0);
+__device__ __forceinline__ Item item_of(const FewParams &p, int touched, const Touched *tab, unsigned tk)
+{
+    constexpr int KE = k_elems<WT>();
+    const Plan &n = p.n;
+    Item it = {END, 0, 1, 0, 0, 0, p.T, 0};
+    const int rgu_total = touched * n.rgu_n, rd_total = touched * n.rd_n;
+    int i = (int)tk, per = 0;
+    if (i < n.router_n) {
+        it.kind = ROUTER; it.j0 = i; it.nkb = p.d / 32;
         return it;
     }
-};
+    if ((i -= n.router_n) < n.down_n) {
+        it.kind = DOWN; it.reps = n.down_r; it.nkb = p.d / KE; per = p.l / 16;
+    } else if ((i -= n.down_n) < n.sgu_n) {
+        it.kind = SHARED_GU; it.reps = n.sgu_r; it.nkb = p.d / KE; per = p.fs / 8;
+    } else if ((i -= n.sgu_n) < rgu_total) {
+        it.kind = ROUTED_GU; it.ti = divide(i, n.rgu_n, n.rgu_inv); i -= it.ti * n.rgu_n;
+        it.reps = n.rgu_r; it.nkb = WT == W_MX4 ? (p.l + 255) / 256 : p.l / KE; per = p.f / 16;
+        it.block0 = tab[it.ti].expert * (p.f / 32);
+    } else if ((i -= rgu_total) < n.sd_n || (i >= n.sd_n + rd_total && i < 2 * n.sd_n + rd_total)) {
+        it.kind = SHARED_DOWN; it.ti = i >= n.sd_n; i -= it.ti ? n.sd_n + rd_total : 0;
+        it.reps = n.sd_r; it.nkb = p.fs / KE; it.kb0 = it.ti * it.nkb; per = p.d / 32;
+    } else if ((i -= n.sd_n) < rd_total) {
+        it.kind = ROUTED_DOWN; it.ti = divide(i, n.rd_n, n.rd_inv); i -= it.ti * n.rd_n;
+        it.reps = n.rd_r; it.nkb = WT == W_MX4 ? (p.f + 255) / 256 : p.f / KE; per = p.l / 32;
+        it.block0 = tab[it.ti].expert * (p.l / 16);
+        it.ncol = __popc((unsigned)tab[it.ti].mask);
+    } else if ((i -= rd_total + n.sd_n) < n.combine_n) {
+        it.kind = COMBINE; it.j0 = i;
+        return it;
+    } else if ((i -= n.combine_n) < n.up_n) {
+        it.kind = UP; it.reps = n.up_r; it.nkb = p.l / KE; it.kb0 = 2 * p.fs / KE; per = p.d / 16;
+    } else {
+        return it;
+    }
+    it.j0 = i * it.reps;
+    it.reps = min(it.reps, per - it.j0);
+    return it;
+}
 
-__device__ __forceinline__ bool weightless(int kind) { return kind == ROUTE || kind == COMBINE || kind == END; }
+__device__ __forceinline__ bool weightless(int kind) { return kind == COMBINE || kind == END; }
 __device__ __forceinline__ bool two_groups(int kind)
 {
     return kind == SHARED_GU || kind == ROUTED_GU || kind == SHARED_DOWN || kind == ROUTED_DOWN;
 }
 // k-blocks per stage: 4, 8 or 32
 __device__ __forceinline__ int stage_kb_log2(int kind) { return kind == ROUTER ? 5 : two_groups(kind) ? 2 : 3; }
-// Whether the teams halve the K of the item's one sub-item.
-template <int WT>
-__device__ __forceinline__ bool splits_k(const FewParams &p, const Item &it)
-{
-    if (it.kind == ROUTER) return true;
-    const int K = it.kind == DOWN || it.kind == SHARED_GU ? p.d : it.kind == SHARED_DOWN ? p.fs
-                  : it.kind == ROUTED_DOWN ? p.f : p.l;
-    const bool routed = it.kind == ROUTED_GU || it.kind == ROUTED_DOWN;
-    return Decoder<WT>::row_bytes(K, routed) * (it.kind == DOWN || it.kind == UP ? 16 : 32) > SPLIT_BYTES;
-}
 // First output row of a sub-item.
 __device__ __forceinline__ int out_row(int kind, int j)
 {
@@ -552,128 +510,184 @@ __device__ __forceinline__ void store_token(void *x, int64_t i, float v)
     else ((bf16 *)x)[i] = __float2bfloat16_rn(v);
 }
 
-// Selection of one token and its weights, by all consumers: an expert's place is
-// the number of experts ahead of it, counted on the high words of the 64-bit score
-// keys, four per load; the low words and the index decide only between equal high
-// words (rare).  A place below k selects.  The loops stay rolled: few blocks run this
-// once per call, so its instructions come from L2, and an unrolled top-k (32
-// registers of keys per lane) took 50 us, nearly all of it fetching them.  real = false: the same
-// on whatever the scores' memory holds, without writing anything.
+// Selection and weights of all tokens, and the touched experts in ascending order with
+// their slots, by one warp; returns the number of touched experts.  Per token: the
+// k-th largest 64-bit score key by bisection on the bits of its high word that the keys
+// do not share; low words and indices decide only where the high words tie (rare);
+// then the k in order of key, equal keys by lower index.  Loops stay rolled: this runs
+// once per call, and unrolled code costs more to fetch than to run (an unrolled top-k
+// took 50 us).  real = false: a run on whatever the scores' memory holds, so that the
+// instructions are here once the scores are; it takes one token, stays inside the arrays and
+// writes no output.  (Inlined: as a function of its own it would read p through generic
+// addresses, and a token's selection takes 6 K cycles instead of .)
 template <int WT>
-__device__ __noinline__ RoleBarrier route_item(const FewParams &p, int t, uint32_t *hi, double *rsel, RoleBarrier bar,
-                                               int warp, int lane, bool real)
-{
-    uint32_t *lo = hi + MAX_E;
-    const int tid = warp * 32 + lane;
-    const double *r = p.r64 + (int64_t)t * p.E;
-    const int E4 = (p.E + 3) & ~3;
-#pragma unroll 1
-    for (int e = tid; e < E4; e += CT) {
-        const unsigned long long key = e < p.E ? key64(__ldcg(r + e) + (double)p.bias[e]) : 0ull;   // real keys > 0
-        hi[e] = (uint32_t)(key >> 32);
-        lo[e] = (uint32_t)key;
-    }
-    if (!bar.sync()) return bar;
-#pragma unroll 1
-    for (int e = tid; e < p.E; e += CT) {
-        const uint32_t mine = hi[e];
-        const uint4 *h4 = reinterpret_cast<const uint4 *>(hi);
-        int ahead = 0, same = 0;
-#pragma unroll 2
-        for (int q = 0; q < E4 / 4; ++q) {
-            const uint4 h = h4[q];
-            ahead += (h.x > mine) + (h.y > mine) + (h.z > mine) + (h.w > mine);
-            same += (h.x == mine) + (h.y == mine) + (h.z == mine) + (h.w == mine);
-        }
-        if (real && same > 1 && ahead < p.k)
-#pragma unroll 1
-            for (int q = 0; q < p.E; ++q)
-                ahead += hi[q] == mine && (lo[q] > lo[e] || (lo[q] == lo[e] && q < e));
-        if (ahead < p.k) {
-            if (real) p.sel[t * p.k + ahead] = e;
-            rsel[ahead] = __ldcg(r + e);
-        }
-    }
-    if (!bar.sync()) return bar;
-    if (warp == 0) {
-        const double r0 = lane < p.k ? rsel[lane] : 0.0, r1 = lane + 32 < p.k ? rsel[lane + 32] : 0.0;
-        double sum = r0 + r1;
-#pragma unroll 1
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-#pragma unroll 1
-        for (int j = lane; j < p.k; j += 32) {
-            const float pv = (float)(rsel[j] / sum);
-            if (real) {
-                p.p32[t * p.k + j] = pv;
-                store_token<WT>(p.p_out, t * p.k + j, pv);
-            }
-        }
-    } else if (warp == 1 && WT == W_MX4 && p.standard) {   // the routed experts read x itself: its largest magnitude
-        float m = 0.f;
-#pragma unroll 1
-        for (int c = lane; c < p.d; c += 32) m = fmaxf(m, fabsf(token_value<WT>(p.x, (int64_t)t * p.d + c)));
-#pragma unroll 1
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (lane == 0 && real) p.ctl[C_AMAX_X + t] = __float_as_uint(m);
-    }
-    return bar;
-}
-
-// The touched experts in ascending order with their slots, from the selection of
-// all tokens: every block's scheduler builds its own.  mask [MAX_E]: the tokens that
-// selected an expert; returns the number of touched experts.  A first run on an unwritten
-// selection (any numbers) stays inside both arrays.
-__device__ __noinline__ int touched_experts(const FewParams &p, uint32_t *mask, Touched *tab, int lane)
+__device__ __forceinline__ int select_experts(const FewParams &p, const Select &q, int lane, bool real)
 {
     constexpr unsigned FULL = 0xffffffffu;
-    const int S = p.T * p.k;
+    const int E = p.E, E4 = (E + 127) / 128 * 32;      // keys in groups of four
+    const unsigned lt = (1u << lane) - 1u;
 #pragma unroll 1
-    for (int e = lane; e < MAX_E; e += 32) mask[e] = 0u;
-    __syncwarp();
+    for (int e = lane; e < 4 * E4; e += 32) q.mask[e] = 0u;
+#pragma unroll 1
+    for (int t = 0; t < (real ? p.T : 1); ++t) {
+        const double *r = p.r64 + (int64_t)t * E;
+        uint32_t all_and = FULL, all_or = 0u;
+        __syncwarp();
 #pragma unroll 4
-    for (int i = lane; i < S; i += 32) atomicOr(mask + (__ldcg(p.sel + i) & (MAX_E - 1)), 1u << (i / p.k));
+        for (int e = lane; e < 4 * E4; e += 32) {
+            uint32_t h = 0u;                           // real keys > 0
+            if (e < E) {
+                h = (uint32_t)(key64(__ldcg(r + e) + (double)__ldg(p.bias + e)) >> 32);
+                all_and &= h;
+                all_or |= h;
+            }
+            q.hi[e] = h;
+        }
+        all_and = __reduce_and_sync(FULL, all_and);
+        const uint32_t diff = all_and ^ __reduce_or_sync(FULL, all_or);
+        __syncwarp();
+        // largest th with at least k keys >= th
+        const int top = 31 - __clz(diff);              // -1: all equal
+        uint32_t th = top == 31 ? 0u : all_and >> (top + 1) << (top + 1);
+        int count = E;
+        const uint4 *h4 = reinterpret_cast<const uint4 *>(q.hi);
+#pragma unroll 1
+        for (int b = top; b >= 0 && count != p.k; --b) {
+            const uint32_t c = th | 1u << b;
+            int mine = 0;
+#pragma unroll 2
+            for (int e = lane; e < E4; e += 32) {
+                const uint4 h = h4[e];
+                mine += (h.x >= c) + (h.y >= c) + (h.z >= c) + (h.w >= c);
+            }
+            const int got = (int)__reduce_add_sync(FULL, (unsigned)mine);
+            if (got >= p.k) {
+                th = c;
+                count = got;
+            }
+        }
+        // compact the selected in index order; where more keys tie on the high word than are
+        // wanted, a tied one is in if fewer than the wanted tied ones are ahead of it
+        int above = 0;
+        if (count != p.k) {
+#pragma unroll 1
+            for (int e = lane; e < E; e += 32) above += q.hi[e] > th;
+            above = (int)__reduce_add_sync(FULL, (unsigned)above);
+        }
+        int pos = 0;
+#pragma unroll 1
+        for (int e0 = 0; e0 < E; e0 += 32) {
+            const int e = e0 + lane;
+            const uint32_t h = e < E ? q.hi[e] : 0u;
+            bool in = e < E && h >= th;
+            if (real && count != p.k && e < E && h == th) {
+                const unsigned long long mine = key64(__ldcg(r + e) + (double)__ldg(p.bias + e));
+                int ahead = above;
+#pragma unroll 1
+                for (int i = 0; i < E; ++i)
+                    if (q.hi[i] == th) {
+                        const unsigned long long other = key64(__ldcg(r + i) + (double)__ldg(p.bias + i));
+                        ahead += other > mine || (other == mine && i < e);
+                    }
+                in = ahead < p.k;
+            }
+            const unsigned b = __ballot_sync(FULL, in);
+            const int at = pos + __popc(b & lt);
+            if (in && at < 64) q.cand_e[at] = (uint16_t)e;
+            pos += __popc(b);
+        }
+        __syncwarp();
+        double rv[2] = {0.0, 0.0};
+        int ex[2] = {0, 0};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (lane + 32 * h < p.k) {
+                ex[h] = min((int)q.cand_e[lane + 32 * h], E - 1);
+                rv[h] = __ldcg(r + ex[h]);
+                q.cand[lane + 32 * h] = key64(rv[h] + (double)__ldg(p.bias + ex[h]));
+            }
+        double sum = rv[0] + rv[1];
+#pragma unroll 1
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+        __syncwarp();
+        const double inv = 1.0 / sum;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = lane + 32 * h;
+            if (i >= p.k) break;
+            const unsigned long long mine = q.cand[i];
+            int place = 0;
+#pragma unroll 2
+            for (int c = 0; c < p.k; ++c) {
+                const unsigned long long other = q.cand[c];
+                place += other > mine || (other == mine && c < i);
+            }
+            const float w = (float)(rv[h] * inv);
+            q.sel[t * p.k + place] = (uint16_t)ex[h];
+            q.weight[t * p.k + place] = w;
+            atomicOr(q.mask + ex[h], 1u << t);
+            if (real && blockIdx.x == 0) {
+                p.sel[t * p.k + place] = ex[h];
+                store_token<WT>(p.p_out, t * p.k + place, w);
+            }
+        }
+    }
     __syncwarp();
     int n = 0;
 #pragma unroll 1
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-        const int e = e0 + lane;
-        const uint32_t m = e < p.E ? mask[e] : 0u;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+        const uint32_t m = q.mask[e0 + lane];
         const unsigned b = __ballot_sync(FULL, m != 0u);
-        const int at = n + __popc(b & ((1u << lane) - 1u));
+        const int at = n + __popc(b & lt);
         if (m) {
-            tab[at].expert = (int16_t)e;
-            tab[at].mask = (int16_t)m;
-            mask[e] = m | (uint32_t)at << 8;
+            q.tab[at].expert = (int16_t)(e0 + lane);
+            q.tab[at].mask = (int16_t)m;
+            q.mask[e0 + lane] = m | (uint32_t)at << 8;
         }
         n += __popc(b);
     }
     __syncwarp();
-#pragma unroll 4
-    for (int i = lane; i < S; i += 32) {
-        const uint32_t m = mask[__ldcg(p.sel + i) & (MAX_E - 1)];
-        const int t = i / p.k;
-        tab[m >> 8].slot[__popc(m & 0xffu & ((1u << t) - 1u))] = (int16_t)i;
-    }
+#pragma unroll 1
+    for (int t = 0; t < (real ? p.T : 1); ++t)
+#pragma unroll 1
+        for (int j = lane; j < p.k; j += 32) {
+            const uint32_t m = q.mask[q.sel[t * p.k + j]];
+            q.tab[m >> 8].slot[__popc(m & 0xffu & ((1u << t) - 1u))] = (int16_t)(t * p.k + j);
+        }
     __syncwarp();
     return n;
 }
 
+// u for 32 latent columns (one per lane) of every token: the token's slots dealt to 8 / T
+// warps (a power of two), their parts summed in order.
 template <int WT>
-__device__ __forceinline__ void combine_item(const FewParams &p, const Item &it, int warp, int lane)
+__device__ __forceinline__ bool combine_item(const FewParams &p, const Item &it, float *red, RoleBarrier &bar, int warp,
+                                             int lane)
 {
-    const int t = warp, c = 32 * it.j0 + lane;
+    const int parts = p.T == 1 ? 8 : p.T == 2 ? 4 : p.T <= 4 ? 2 : 1;
+    const int t = warp / parts, part = warp - t * parts, c = 32 * it.j0 + lane;
+    float u = 0.f;
     if (t < p.T) {
         const float *src = p.ysl + (int64_t)t * p.k * p.l + c;
-        float u = 0.f;
-        int j = 0;
-        for (; j + 8 <= p.k; j += 8) {
-            float v[8];
+        int j = part;
+#pragma unroll 1
+        for (; j + 3 * parts < p.k; j += 4 * parts) {
+            float v[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __ldcg(src + (int64_t)(j + i) * p.l);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) u += v[i];
+            for (int i = 0; i < 4; ++i) v[i] = __ldcg(src + (int64_t)(j + i * parts) * p.l);
+            u += (v[0] + v[1]) + (v[2] + v[3]);
         }
-        for (; j < p.k; ++j) u += __ldcg(src + (int64_t)j * p.l);
+#pragma unroll 1
+        for (; j < p.k; j += parts) u += __ldcg(src + (int64_t)j * p.l);
+    }
+    if (parts > 1) {
+        red[warp * 32 + lane] = u;
+        if (!bar.sync()) return false;
+        if (part == 0)
+#pragma unroll 1
+            for (int i = 1; i < parts; ++i) u += red[(warp + i) * 32 + lane];
+    }
+    if (t < p.T && part == 0) {
         store_token<WT>(p.u_out, (int64_t)t * p.l + c, u);
         if (p.standard) {
             const float *q = p.part + (int64_t)t * p.d + c;
@@ -686,6 +700,7 @@ __device__ __forceinline__ void combine_item(const FewParams &p, const Item &it,
             if (lane == 0) p.ssq[t * (p.l / 32) + it.j0] = ss;
         }
     }
+    return parts == 1 || bar.sync();      // the sums' memory is free again
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -703,9 +718,15 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
     sh.scales = base + o; o += p.scales ? (uint32_t)p.stages * SCALE_BYTES : 0u;
     sh.act = base + o; o += 2u * (uint32_t)p.slot_bytes;
     sh.red = reinterpret_cast<float *>(g + o); o += 4 * RED_FLOATS;
-    sh.tab = reinterpret_cast<Touched *>(g + o); o += sizeof(Touched) * FEW_MAX_SLOTS;
-    sh.mask = reinterpret_cast<uint32_t *>(g + o); o += 4 * MAX_E;
-    sh.rsel = reinterpret_cast<double *>(g + o); o += 8 * 64;
+    const int E128 = (p.E + 127) & ~127, TK = p.T * p.k, TK8 = (TK + 7) & ~7;
+    sh.select.hi = reinterpret_cast<uint32_t *>(g + o); o += 4 * E128;
+    sh.select.mask = reinterpret_cast<uint32_t *>(g + o); o += 4 * E128;
+    sh.select.cand = reinterpret_cast<unsigned long long *>(g + o); o += 8 * 64;
+    sh.select.cand_e = reinterpret_cast<uint16_t *>(g + o); o += 2 * 64;
+    sh.select.weight = reinterpret_cast<float *>(g + o); o += 4 * TK8;
+    sh.select.sel = reinterpret_cast<uint16_t *>(g + o); o += 2 * TK8;
+    sh.tab = sh.select.tab = reinterpret_cast<Touched *>(g + o); o += (uint32_t)sizeof(Touched) * (TK8 < E128 ? TK8 : E128);
+    o = (o + 15u) & ~15u;
     sh.queue = reinterpret_cast<Item *>(g + o); o += sizeof(Item) * QUEUE;
     uint64_t *bars = reinterpret_cast<uint64_t *>(g + o); o += 8 * (2 * MAX_STAGES + 12);
     sh.inv = reinterpret_cast<float *>(g + o); o += 64;
@@ -763,7 +784,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 if (it.kind == END) break;
                 if (weightless(it.kind)) continue;
                 const int nc = chunks(it), kb = 1 << stage_kb_log2(it.kind);
-                const bool two = two_groups(it.kind), split = splits_k<WT>(p, it);
+                const bool two = two_groups(it.kind), split = (p.n.split >> it.kind & 1u) != 0u;
                 const bool mx4 = WT == W_MX4 && (it.kind == ROUTED_GU || it.kind == ROUTED_DOWN);
                 const uint32_t bytes = STAGE_BYTES + (mx4 ? SCALE_BYTES : 0);
                 const CUtensorMap *map = it.kind == ROUTER        ? &maps.router
@@ -810,8 +831,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
         }
     } else if (warp == CONSUMERS + 1) {
         // ------------------------------------------------------------ scheduler
-        Decoder<WT> item(p, 0);
-        const unsigned fixed = (unsigned)item.fixed(p);        // tickets that need no selection
+        const unsigned fixed = (unsigned)(p.n.router_n + p.n.down_n + p.n.sgu_n);     // tickets that need no selection
         unsigned next = 0;
         int touched = 0;
         if (lane == 0) next = atomicAdd(p.ctl + C_TICKET, 1u);
@@ -819,19 +839,21 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
             const unsigned tk = __shfl_sync(0xffffffffu, next, 0);
             int good = 1;
             if (tk >= fixed && touched == 0) {
-                // a first run on whatever is there, while the selection is not: its instructions are here then
-                touched_experts(p, sh.mask, sh.tab, lane);
-                if (lane == 0) good = wait_count(p.ctl, C_ROUTED, (unsigned)p.T, abort);
-                good = __shfl_sync(0xffffffffu, good, 0);
+#pragma unroll 1
+                for (int pass = 0; pass < 2 && good; ++pass) {
+                    if (pass) {
+                        if (lane == 0) good = wait_count(p.ctl, C_ROUTER, (unsigned)p.n.router_n, abort);
+                        good = __shfl_sync(0xffffffffu, good, 0);
+                    }
+                    if (good) touched = select_experts<WT>(p, sh.select, lane, pass != 0);
+                }
                 if (!good) {
                     if (lane == 0) give_up(0x10);
                     break;
                 }
-                touched = touched_experts(p, sh.mask, sh.tab, lane);
-                item = Decoder<WT>(p, touched);
                 if (lane == 0) sh.flags[25] = touched;
             }
-            const Item it = item(p, sh.tab, tk);
+            const Item it = item_of<WT>(p, touched, sh.tab, tk);
             if (it.kind == ROUTED_GU || it.kind == ROUTED_DOWN) {
                 int c1, c2;
                 box_at(it, it.j0 + lane, &c1, &c2);
@@ -865,7 +887,6 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
         // ------------------------------------------------------------ loaders
         const int tid = threadIdx.x - 32 * (CONSUMERS + 2), lw = warp - CONSUMERS - 2;
         RoleBarrier bar = {sh.load, 0u, abort, true};
-        const Decoder<WT> item(p, 0);
         int set = 0, cur_key = -1, cur_seg = -1, ready = -1;   // ready: last kind whose inputs are complete
         bool ok = true;
         for (int q = 0; ok; ++q) {
@@ -891,15 +912,15 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 if (lane == 0) {
                     good = mbar_wait(sh.act_empty + 8u * slot, (uint32_t)((set >> 1) & 1) ^ 1u, abort);
                     if (good && it.kind != ready) {          // the items that write these values
-                        if (it.kind == ROUTED_GU && !p.standard) good = wait_count(p.ctl, C_Z, (unsigned)item.down_n, abort);
+                        if (it.kind == ROUTED_GU && !p.standard) good = wait_count(p.ctl, C_Z, (unsigned)p.n.down_n, abort);
                         // (the failure-detection test waits for one count too many)
                         if (it.kind == SHARED_DOWN)
-                            good = wait_count(p.ctl, C_HS, (unsigned)item.sgu_n + (p.stall_test ? 1u : 0u), abort);
+                            good = wait_count(p.ctl, C_HS, (unsigned)p.n.sgu_n + (p.stall_test ? 1u : 0u), abort);
                         if (it.kind == ROUTED_DOWN)
-                            good = wait_count(p.ctl, C_H, (unsigned)Decoder<WT>(p, sh.flags[25]).rgu_total, abort);
+                            good = wait_count(p.ctl, C_H, (unsigned)(sh.flags[25] * p.n.rgu_n), abort);
                         if (it.kind == UP)
-                            good = wait_count(p.ctl, C_U, (unsigned)item.combine_n(p), abort) &&
-                                   wait_count(p.ctl, C_PART, 2u * item.sd_n, abort);
+                            good = wait_count(p.ctl, C_U, (unsigned)p.n.combine_n, abort) &&
+                                   wait_count(p.ctl, C_PART, 2u * p.n.sd_n, abort);
                     }
                 }
                 ready = it.kind;
@@ -947,14 +968,32 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                         dst, a.stride, plane, it.ncol, kn / 4, tid,
                         [&](int t) { return p.u + (int64_t)t * p.l + k0; }, [&](int t) { return sh.lred[t]; });
                 } else if (mx4) {
-                    const unsigned *amax = p.ctl + (it.kind == ROUTED_DOWN ? C_AMAX_H : x_rows ? C_AMAX_X : C_AMAX_Z);
+                    const unsigned *amax = p.ctl + (it.kind == ROUTED_DOWN ? C_AMAX_H : C_AMAX_Z);
                     const Touched &e = sh.tab[it.ti];
+                    if (x_rows) {       // the experts read x itself: its rows' largest magnitudes first
+                        for (int t = lw; t < it.ncol; t += LOADERS) {
+                            const uint32_t *v = reinterpret_cast<const uint32_t *>((const bf16 *)p.x + (int64_t)t * p.d);
+                            uint32_t m = 0u;
+#pragma unroll 4
+                            for (int c = lane; c < p.d / 2; c += 32) {
+                                const uint32_t w = __ldg(v + c) & 0x7fff7fffu;
+                                m = max(m, max(w << 16, w & 0xffff0000u));
+                            }
+                            m = __reduce_max_sync(0xffffffffu, m);
+                            if (lane == 0) sh.lred[t] = __uint_as_float(m);
+                        }
+                        if (!(ok = bar.sync())) {
+                            if (lane == 0) give_up(0x4);
+                            break;
+                        }
+                    }
                     auto at = [&](int t) { return it.kind == ROUTED_DOWN ? (int)e.slot[t] : t; };
+                    auto largest = [&](int t) { return x_rows ? sh.lred[t] : __uint_as_float(__ldcg(amax + at(t))); };
                     auto mul = [&](int t) {
                         float back;
-                        return f16_scale(__uint_as_float(__ldcg(amax + at(t))), &back);
+                        return f16_scale(largest(t), &back);
                     };
-                    if (tid < it.ncol) f16_scale(__uint_as_float(__ldcg(amax + at(tid))), &inv[tid]);
+                    if (tid < it.ncol) f16_scale(largest(tid), &inv[tid]);
                     if (x_rows) {
                         for (int t = 0; t < it.ncol; ++t)
                             load_row_bf16_scaled(dst + (uint32_t)(t * a.stride), plane,
@@ -985,7 +1024,6 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
         const int gid = lane >> 2, c4 = lane & 3;
         RoleBarrier bar = {sh.cons, 0u, abort, true};                     // all eight warps
         RoleBarrier tbar = {sh.team + 8u * team, 0u, abort, true};        // the team's four
-        const Decoder<WT> item(p, 0);
         int s = team ? half : 0;                         // slot and phase of this team's next stage
         uint32_t ph = 0, red_ph = 1;
         int set = -1, cur_key = -1, cur_seg = -1;
@@ -1010,34 +1048,18 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
             if (kind == END) break;
             if (weightless(kind)) {
                 int good = 1;
-                if (kind == ROUTE) {
-                    // a first run on whatever is there, while the scores are not: its instructions are here then
-                    if (!(ok = bar.sync())) break;
-                    bar = route_item<WT>(p, it.ti, reinterpret_cast<uint32_t *>(sh.red), sh.rsel, bar, warp, lane, false);
-                    if (!(ok = bar.ok)) break;
-                }
                 if (lane == 0) {
-                    if (kind == ROUTE) {
-                        good = wait_count(p.ctl, C_ROUTER, (unsigned)item.router_n(p), abort);
-                    } else {
-                        good = wait_count(p.ctl, C_YS, (unsigned)Decoder<WT>(p, sh.flags[25]).rd_total, abort);
-                        if (good && p.standard) good = wait_count(p.ctl, C_PART, 2u * item.sd_n, abort);
-                    }
+                    good = wait_count(p.ctl, C_YS, (unsigned)(sh.flags[25] * p.n.rd_n), abort);
+                    if (good && p.standard) good = wait_count(p.ctl, C_PART, 2u * p.n.sd_n, abort);
                 }
-                ok = __shfl_sync(0xffffffffu, good, 0) != 0 && bar.sync();
+                ok = __shfl_sync(0xffffffffu, good, 0) != 0 && bar.sync() && combine_item<WT>(p, it, sh.red, bar, warp, lane);
                 if (!ok) break;
-                if (kind == ROUTE) {
-                    bar = route_item<WT>(p, it.ti, reinterpret_cast<uint32_t *>(sh.red), sh.rsel, bar, warp, lane, true);
-                    if (!(ok = bar.ok)) break;
-                } else {
-                    combine_item<WT>(p, it, warp, lane);
-                }
                 done();
                 continue;
             }
 
             const ActPlan a = act_plan<WT>(p, it);
-            const bool two = two_groups(kind), split = splits_k<WT>(p, it);
+            const bool two = two_groups(kind), split = (p.n.split >> it.kind & 1u) != 0u;
             const int nc = chunks(it), nkb = it.nkb;
             const uint32_t plane = (uint32_t)(it.ncol * a.stride);
             // Four columns or fewer of two terms: hi in columns 0-3, lo in 4-7 of one product
@@ -1119,10 +1141,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                                     x0 = __uint_as_float(v.x << 16); x1 = __uint_as_float(v.x & 0xffff0000u);
                                     x2 = __uint_as_float(v.y << 16); x3 = __uint_as_float(v.y & 0xffff0000u);
                                 }
-                                acc[t] = fma(w0, (double)x0, acc[t]);
-                                acc[t] = fma(w1, (double)x1, acc[t]);
-                                acc[t] = fma(w2, (double)x2, acc[t]);
-                                acc[t] = fma(w3, (double)x3, acc[t]);
+                                acc[t] += fma(w0, (double)x0, w1 * (double)x1) + fma(w2, (double)x2, w3 * (double)x3);
                             }
                     }
                     release();
@@ -1327,7 +1346,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
             } else if (kind == ROUTED_DOWN) {
                 if (real) {
                     slot = sh.tab[it.ti].slot[t];
-                    add = __ldcg(p.p32 + slot);
+                    add = sh.select.weight[slot];
                 }
             } else if (kind == ROUTED_GU) {
                 const unsigned mask = (unsigned)sh.tab[it.ti].mask;
@@ -1399,7 +1418,6 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                     }
                 if (!ok) break;
                 const int at = kind == ROUTER        ? C_ROUTER
-                               : kind == ROUTE       ? C_ROUTED
                                : kind == DOWN        ? C_Z
                                : kind == SHARED_GU   ? C_HS
                                : kind == ROUTED_GU   ? C_H
@@ -1430,14 +1448,16 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
 }
 
 // ------------------------------------------------------------------ host side
-size_t fixed_smem()
+size_t fixed_smem(const lmoe_config &c, int T)
 {
-    return 1024 + 4 * RED_FLOATS + sizeof(Touched) * FEW_MAX_SLOTS + 4 * MAX_E + 8 * 64 + sizeof(Item) * QUEUE + 8 * (2 * MAX_STAGES + 12) +
+    const int E128 = (c.E + 127) / 128 * 128, TK8 = (T * c.k + 7) / 8 * 8;
+    return 1024 + 4 * RED_FLOATS + 8 * (size_t)E128 + 8 * 64 + 2 * 64 + 6 * (size_t)TK8 +
+           sizeof(Touched) * (size_t)std::min(TK8, E128) + 16 + sizeof(Item) * QUEUE + 8 * (2 * MAX_STAGES + 12) +
  64 + 64 + 192;
 }
 
 struct FewLayout {
-    size_t ctl, r64, p32, z, hs, H, part, ysl, u, ssq, total;
+    size_t ctl, r64, z, hs, H, part, ysl, u, ssq, total;
 };
 
 FewLayout few_layout(const lmoe_config &c, int64_t T)
@@ -1452,7 +1472,6 @@ FewLayout few_layout(const lmoe_config &c, int64_t T)
     const size_t S = (size_t)T * c.k;
     L.ctl = take(4 * C_WORDS);
     L.r64 = take(8 * (size_t)T * c.E);
-    L.p32 = take(4 * S);
     L.z = take(c.standard ? 0 : 4 * (size_t)T * c.l);
     L.hs = take(4 * (size_t)T * 2 * c.f_shared);
     L.H = take(4 * S * c.f);
@@ -1471,6 +1490,50 @@ cudaError_t launch(const FewMaps &m, const FewParams &p, size_t smem, cudaStream
     if (e != cudaSuccess) return e;
     few_kernel<WT><<<tc_num_sms(), THREADS, smem, s>>>(m, p);
     return cudaGetLastError();
+}
+}  // namespace
+
+namespace {
+// Sub-items per item: pairs (one for each team) until an item has ITEM_BYTES, but leaving every block
+// about eight items of the phase; 1 where the teams halve K.
+int reps_for(int64_t sub_bytes, int64_t subs, int blocks)
+{
+    if (sub_bytes > SPLIT_BYTES) return 1;
+    const int64_t most = std::min<int64_t>(MAX_REPS, ITEM_BYTES / sub_bytes) / 2 * 2;
+    return (int)std::max<int64_t>(2, std::min<int64_t>(most, subs / (8 * (int64_t)blocks) / 2 * 2));
+}
+
+Plan make_plan(const lmoe_config &c, bool mx4, int T, int blocks)
+{
+    const int64_t eb = c.dtype == LMOE_F32 ? 4 : 2;
+    auto row = [&](int64_t K, bool routed) { return mx4 && routed ? K / 2 + K / 32 : K * eb; };
+    auto items = [](int64_t subs, int reps) { return (int)((subs + reps - 1) / reps); };
+    // touched experts, were the selections independent and even
+    double miss = 1.0;
+    for (int t = 0; t < T; ++t) miss *= 1.0 - (double)c.k / c.E;
+    const int64_t touched = std::max<int64_t>(1, (int64_t)(c.E * (1.0 - miss)));
+    Plan n = {};
+    const int64_t down = 16 * row(c.d, false), sgu = 32 * row(c.d, false), rgu = 32 * row(c.l, true),
+                  sd = 32 * row(c.f_shared, false), rd = 32 * row(c.f, true), up = 16 * row(c.l, false);
+    n.router_n = (c.E + 3) / 4;
+    n.combine_n = c.l / 32;
+    n.down_r = reps_for(down, c.l / 16, blocks);
+    n.down_n = c.standard ? 0 : items(c.l / 16, n.down_r);
+    n.sgu_r = reps_for(sgu, c.f_shared / 8, blocks);
+    n.sgu_n = items(c.f_shared / 8, n.sgu_r);
+    n.rgu_r = reps_for(rgu, touched * (c.f / 16), blocks);
+    n.rgu_n = items(c.f / 16, n.rgu_r);
+    n.sd_r = reps_for(sd, c.d / 16, blocks);
+    n.sd_n = items(c.d / 32, n.sd_r);
+    n.rd_r = reps_for(rd, touched * (c.l / 32), blocks);
+    n.rd_n = items(c.l / 32, n.rd_r);
+    n.up_r = reps_for(up, c.d / 16, blocks);
+    n.up_n = c.standard ? 0 : items(c.d / 16, n.up_r);
+    n.rgu_inv = 1.0f / (float)n.rgu_n;
+    n.rd_inv = 1.0f / (float)n.rd_n;
+    const int64_t sub[] = {SPLIT_BYTES + 1, down, sgu, rgu, sd, rd, 0, up};     // by kind
+    for (int k = ROUTER; k <= UP; ++k) n.split |= (uint32_t)(sub[k] > SPLIT_BYTES) << k;
+    return n;
 }
 }  // namespace
 
@@ -1523,10 +1586,11 @@ cudaError_t few_launch(const lmoe_config &c, const FewMaps &m, const FewWeights 
     const FewLayout L = few_layout(c, T);
     char *ws = (char *)workspace;
     FewParams p = {};
+    p.n = make_plan(c, mx4, T, tc_num_sms());
     p.T = T; p.d = c.d; p.l = c.l; p.f = c.f; p.E = c.E; p.k = c.k; p.fs = c.f_shared; p.act = c.act;
     p.standard = c.standard; p.gate_cap = c.gate_cap; p.up_cap = c.up_cap; p.eps = c.eps;
     p.x = x; p.bias = bias; p.y = y; p.p_out = p_out; p.u_out = u_out; p.sel = sel;
-    p.ctl = (unsigned *)(ws + L.ctl); p.r64 = (double *)(ws + L.r64); p.p32 = (float *)(ws + L.p32);
+    p.ctl = (unsigned *)(ws + L.ctl); p.r64 = (double *)(ws + L.r64);
     p.z = (float *)(ws + L.z); p.hs = (float *)(ws + L.hs); p.H = (float *)(ws + L.H);
     p.part = (float *)(ws + L.part); p.ysl = (float *)(ws + L.ysl); p.u = (float *)(ws + L.u);
     p.ssq = (float *)(ws + L.ssq);
@@ -1547,8 +1611,8 @@ cudaError_t few_launch(const lmoe_config &c, const FewMaps &m, const FewWeights 
     slot = (slot + 1023) / 1024 * 1024;
     p.slot_bytes = slot;
     const int stage = STAGE_BYTES + (mx4 ? SCALE_BYTES : 0);
-    p.stages = std::min(MAX_STAGES, (int)((SMEM_MAX - (int)fixed_smem() - 2 * slot) / stage));
-    const size_t smem = fixed_smem() + 2 * (size_t)slot + (size_t)p.stages * stage;
+    p.stages = std::min(MAX_STAGES, (int)((SMEM_MAX - (int)fixed_smem(c, T) - 2 * slot) / stage));
+    const size_t smem = fixed_smem(c, T) + 2 * (size_t)slot + (size_t)p.stages * stage;
     cudaError_t e = cudaMemsetAsync(p.ctl, 0, 4 * C_WORDS, s);
     if (e != cudaSuccess) return e;
     if (f32) return launch<W_F32>(m, p, smem, s);
