@@ -36,11 +36,11 @@
 //               four 128-byte k-blocks of two groups of 16 rows (gate and up, or 32 rows), eight
 //               k-blocks of 16 rows, or 32 of 4 rows (router)
 //   warp 9      scheduler: takes tickets and describes their items in a queue, at most two items
-//               ahead of the producer (its integer work per item would stall the copies).  Once the
-//               router's rows are done it selects the experts of all tokens itself, in every block:
-//               the same work as reading another block's result would wait for
+//               ahead of the producer (its integer work per item would stall the copies)
 //   warps 10-13 loaders: bring an item's activations from global memory into one of two
-//               shared-memory slots, in the form that the product wants, one set ahead
+//               shared-memory slots, in the form that the product wants, one set ahead.  Before the
+//               first routed item they select the experts, a warp per token, in every block: the same
+//               work takes no longer than another block's result would take to arrive
 //   warp 14     signaller: publishes finished items to the other blocks (the fence before the
 //               counter costs 1000 to 2000 cycles, which the consumers would otherwise spend per item)
 //
@@ -68,15 +68,14 @@ using namespace ptx;
 
 constexpr int CONSUMERS = 8, LOADERS = 4;
 constexpr int THREADS = 32 * (CONSUMERS + 2 + LOADERS + 1);
-constexpr int CT = 32 * CONSUMERS, LT = 32 * LOADERS;
+constexpr int LT = 32 * LOADERS;
 constexpr int STAGE_BYTES = 16384, KBLK_BYTES = 2048;   // a k-block of 16 rows
 constexpr int SCALE_BYTES = 1024;                // 2 x 16 rows of 32 scales (1024 values)
 constexpr int MAX_STAGES = 12, QUEUE = 32, AHEAD = 3;
-constexpr int MAX_E = 1024;
 constexpr int SPLIT_BYTES = 160 * 1024, ITEM_BYTES = 256 * 1024, MAX_REPS = 8;
 constexpr int SMEM_MAX = 232448;
 
-enum Kind { ROUTER, DOWN, SHARED_GU, ROUTED_GU, SHARED_DOWN, ROUTED_DOWN, COMBINE, UP, END };
+enum Kind { ROUTER, DOWN, SHARED_GU, ROUTED_GU, SHARED_DOWN, ROUTED_DOWN, COMBINE, UP, END, SELECT };
 
 // Words of the control area (zero at launch).
 enum Ctl { C_STATUS = 0, C_TICKET = 32, C_ROUTER = 64, C_Z = 96, C_HS = 160, C_H = 192, C_PART = 224,
@@ -302,14 +301,16 @@ struct RoleBarrier {
     }
 };
 
-// Scratch of the selection, in shared memory (n_touched entries etc. by the call's sizes).
+// The selection in shared memory.
 struct Select {
-    uint32_t *hi, *mask;         // [E rounded up to 128]: score keys' high words; tokens and index of an expert
-    unsigned long long *cand;    // [64] keys of a token's selected
-    uint16_t *cand_e, *sel;      // [64] their experts; [T, k] experts in order
+    uint32_t *mask;              // [E rounded up to 128]: tokens that selected an expert, then its index as well
+    uint16_t *sel;               // [T, k] experts in order
     float *weight;               // [T, k]
     Touched *tab;
 };
+// Scratch of one warp's token: score keys' high and low words and scores of E rounded up to 128
+// experts; keys and experts of the selected.
+__host__ __device__ constexpr int select_bytes(int E128) { return 12 * E128 + 64 * 8 + 64 * 2; }
 
 struct Shared {
     uint32_t ring, scales, act, full, empty, act_full, act_empty, cons, team, load, red_free;   // shared-memory addresses
@@ -380,7 +381,7 @@ __device__ __forceinline__ Item item_of(const FewParams &p, int touched, const T
     return it;
 }
 
-__device__ __forceinline__ bool weightless(int kind) { return kind == COMBINE || kind == END; }
+__device__ __forceinline__ bool weightless(int kind) { return kind == COMBINE || kind == END || kind == SELECT; }
 __device__ __forceinline__ bool two_groups(int kind)
 {
     return kind == SHARED_GU || kind == ROUTED_GU || kind == SHARED_DOWN || kind == ROUTED_DOWN;
@@ -510,60 +511,76 @@ __device__ __forceinline__ void store_token(void *x, int64_t i, float v)
     else ((bf16 *)x)[i] = __float2bfloat16_rn(v);
 }
 
-// Selection and weights of all tokens, and the touched experts in ascending order with
-// their slots, by one warp; returns the number of touched experts.  Per token: the
-// k-th largest 64-bit score key by bisection on the bits of its high word that the keys
-// do not share; low words and indices decide only where the high words tie (rare);
-// then the k in order of key, equal keys by lower index.  Loops stay rolled: this runs
-// once per call, and unrolled code costs more to fetch than to run (an unrolled top-k
-// took 50 us).  real = false: a run on whatever the scores' memory holds, so that the
-// instructions are here once the scores are; it takes one token, stays inside the arrays and
-// writes no output.  (Inlined: as a function of its own it would read p through generic
-// addresses, and a token's selection takes 6 K cycles instead of .)
+// Selection and weights of token t by one warp: the k-th largest 64-bit score key by
+// bisection on the bits of its high word that the keys do not share; low words and
+// indices decide only where the high words tie (rare); then the k in order of key, equal
+// keys by lower index.  Loops stay rolled: this runs once per call, and unrolled code costs
+// more to fetch than to run (an unrolled top-k took 50 us).
 template <int WT>
-__device__ __forceinline__ int select_experts(const FewParams &p, const Select &q, int lane, bool real)
+__device__ __forceinline__ void select_token(const FewParams &p, const Select &q, uint8_t *scratch, int t, int lane)
 {
     constexpr unsigned FULL = 0xffffffffu;
     const int E = p.E, E4 = (E + 127) / 128 * 32;      // keys in groups of four
     const unsigned lt = (1u << lane) - 1u;
-#pragma unroll 1
-    for (int e = lane; e < 4 * E4; e += 32) q.mask[e] = 0u;
-#pragma unroll 1
-    for (int t = 0; t < (real ? p.T : 1); ++t) {
+    uint32_t *hi = reinterpret_cast<uint32_t *>(scratch), *lo = hi + 4 * E4;
+    float *score = reinterpret_cast<float *>(lo + 4 * E4);
+    unsigned long long *cand = reinterpret_cast<unsigned long long *>(score + 4 * E4);
+    uint16_t *cand_e = reinterpret_cast<uint16_t *>(cand + 64);
+    {
         const double *r = p.r64 + (int64_t)t * E;
         uint32_t all_and = FULL, all_or = 0u;
         __syncwarp();
-#pragma unroll 4
-        for (int e = lane; e < 4 * E4; e += 32) {
-            uint32_t h = 0u;                           // real keys > 0
-            if (e < E) {
-                h = (uint32_t)(key64(__ldcg(r + e) + (double)__ldg(p.bias + e)) >> 32);
-                all_and &= h;
-                all_or |= h;
+#pragma unroll 1
+        for (int e0 = lane; e0 < 4 * E4; e0 += 256) {      // eight loads in flight
+            double v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = e0 + 32 * i < E ? __ldcg(r + e0 + 32 * i) : 0.0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int e = e0 + 32 * i;
+                if (e >= 4 * E4) break;
+                unsigned long long key = 0ull;             // real keys > 0
+                if (e < E) {
+                    key = key64(v[i] + (double)__ldg(p.bias + e));
+                    all_and &= (uint32_t)(key >> 32);
+                    all_or |= (uint32_t)(key >> 32);
+                }
+                hi[e] = (uint32_t)(key >> 32);
+                lo[e] = (uint32_t)key;
+                score[e] = (float)v[i];
             }
-            q.hi[e] = h;
         }
         all_and = __reduce_and_sync(FULL, all_and);
         const uint32_t diff = all_and ^ __reduce_or_sync(FULL, all_or);
         __syncwarp();
-        // largest th with at least k keys >= th
+        // largest th with at least k keys >= th, two bits at a time
         const int top = 31 - __clz(diff);              // -1: all equal
         uint32_t th = top == 31 ? 0u : all_and >> (top + 1) << (top + 1);
         int count = E;
-        const uint4 *h4 = reinterpret_cast<const uint4 *>(q.hi);
+        const uint4 *h4 = reinterpret_cast<const uint4 *>(hi);
 #pragma unroll 1
-        for (int b = top; b >= 0 && count != p.k; --b) {
-            const uint32_t c = th | 1u << b;
-            int mine = 0;
+        for (int b = top | 1; b >= 0 && count != p.k; b -= 2) {     // (b = -1 | 1 = -1: none)
+            const uint32_t step = 1u << (b - 1), c1 = th | step, c2 = th | 2u * step, c3 = c2 | step;
+            unsigned n12 = 0, n3 = 0;                  // counts of c1 and (16 bits further) c2; of c3
 #pragma unroll 2
             for (int e = lane; e < E4; e += 32) {
                 const uint4 h = h4[e];
-                mine += (h.x >= c) + (h.y >= c) + (h.z >= c) + (h.w >= c);
+                n12 += (h.x >= c1) + (h.y >= c1) + (h.z >= c1) + (h.w >= c1);
+                n12 += ((h.x >= c2) + (h.y >= c2) + (h.z >= c2) + (h.w >= c2)) << 16;
+                n3 += (h.x >= c3) + (h.y >= c3) + (h.z >= c3) + (h.w >= c3);
             }
-            const int got = (int)__reduce_add_sync(FULL, (unsigned)mine);
-            if (got >= p.k) {
-                th = c;
-                count = got;
+            n12 = __reduce_add_sync(FULL, n12);
+            n3 = __reduce_add_sync(FULL, n3);
+            const int n1 = (int)(n12 & 0xffffu), n2 = (int)(n12 >> 16);
+            if ((int)n3 >= p.k) {
+                th = c3;
+                count = (int)n3;
+            } else if (n2 >= p.k) {
+                th = c2;
+                count = n2;
+            } else if (n1 >= p.k) {
+                th = c1;
+                count = n1;
             }
         }
         // compact the selected in index order; where more keys tie on the high word than are
@@ -571,71 +588,72 @@ __device__ __forceinline__ int select_experts(const FewParams &p, const Select &
         int above = 0;
         if (count != p.k) {
 #pragma unroll 1
-            for (int e = lane; e < E; e += 32) above += q.hi[e] > th;
+            for (int e = lane; e < E; e += 32) above += hi[e] > th;
             above = (int)__reduce_add_sync(FULL, (unsigned)above);
         }
         int pos = 0;
 #pragma unroll 1
         for (int e0 = 0; e0 < E; e0 += 32) {
             const int e = e0 + lane;
-            const uint32_t h = e < E ? q.hi[e] : 0u;
+            const uint32_t h = e < E ? hi[e] : 0u;
             bool in = e < E && h >= th;
-            if (real && count != p.k && e < E && h == th) {
-                const unsigned long long mine = key64(__ldcg(r + e) + (double)__ldg(p.bias + e));
+            if (count != p.k && e < E && h == th) {
+                const uint32_t mine = lo[e];
                 int ahead = above;
 #pragma unroll 1
-                for (int i = 0; i < E; ++i)
-                    if (q.hi[i] == th) {
-                        const unsigned long long other = key64(__ldcg(r + i) + (double)__ldg(p.bias + i));
-                        ahead += other > mine || (other == mine && i < e);
-                    }
+                for (int i = 0; i < E; ++i) ahead += hi[i] == th && (lo[i] > mine || (lo[i] == mine && i < e));
                 in = ahead < p.k;
             }
             const unsigned b = __ballot_sync(FULL, in);
             const int at = pos + __popc(b & lt);
-            if (in && at < 64) q.cand_e[at] = (uint16_t)e;
+            if (in && at < 64) cand_e[at] = (uint16_t)e;
             pos += __popc(b);
         }
         __syncwarp();
-        double rv[2] = {0.0, 0.0};
+        float rv[2] = {0.f, 0.f};
         int ex[2] = {0, 0};
 #pragma unroll
         for (int h = 0; h < 2; ++h)
             if (lane + 32 * h < p.k) {
-                ex[h] = min((int)q.cand_e[lane + 32 * h], E - 1);
-                rv[h] = __ldcg(r + ex[h]);
-                q.cand[lane + 32 * h] = key64(rv[h] + (double)__ldg(p.bias + ex[h]));
+                ex[h] = min((int)cand_e[lane + 32 * h], E - 1);
+                rv[h] = score[ex[h]];
+                cand[lane + 32 * h] = (unsigned long long)hi[ex[h]] << 32 | lo[ex[h]];
             }
-        double sum = rv[0] + rv[1];
-#pragma unroll 1
+        float sum = rv[0] + rv[1];
+#pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
         __syncwarp();
-        const double inv = 1.0 / sum;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int i = lane + 32 * h;
             if (i >= p.k) break;
-            const unsigned long long mine = q.cand[i];
+            const unsigned long long mine = cand[i];
             int place = 0;
-#pragma unroll 2
+#pragma unroll 4
             for (int c = 0; c < p.k; ++c) {
-                const unsigned long long other = q.cand[c];
+                const unsigned long long other = cand[c];
                 place += other > mine || (other == mine && c < i);
             }
-            const float w = (float)(rv[h] * inv);
+            const float w = rv[h] / sum;
             q.sel[t * p.k + place] = (uint16_t)ex[h];
             q.weight[t * p.k + place] = w;
             atomicOr(q.mask + ex[h], 1u << t);
-            if (real && blockIdx.x == 0) {
+            if (blockIdx.x == 0) {
                 p.sel[t * p.k + place] = ex[h];
                 store_token<WT>(p.p_out, t * p.k + place, w);
             }
         }
     }
-    __syncwarp();
+}
+
+// The touched experts in ascending order with their slots, by one warp; returns their number.
+__device__ __forceinline__ int touched_experts(const FewParams &p, const Select &q, int lane)
+{
+    constexpr unsigned FULL = 0xffffffffu;
+    const unsigned lt = (1u << lane) - 1u;
     int n = 0;
 #pragma unroll 1
-    for (int e0 = 0; e0 < E; e0 += 32) {
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
         const uint32_t m = q.mask[e0 + lane];
         const unsigned b = __ballot_sync(FULL, m != 0u);
         const int at = n + __popc(b & lt);
@@ -648,7 +666,7 @@ __device__ __forceinline__ int select_experts(const FewParams &p, const Select &
     }
     __syncwarp();
 #pragma unroll 1
-    for (int t = 0; t < (real ? p.T : 1); ++t)
+    for (int t = 0; t < p.T; ++t)
 #pragma unroll 1
         for (int j = lane; j < p.k; j += 32) {
             const uint32_t m = q.mask[q.sel[t * p.k + j]];
@@ -719,10 +737,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
     sh.act = base + o; o += 2u * (uint32_t)p.slot_bytes;
     sh.red = reinterpret_cast<float *>(g + o); o += 4 * RED_FLOATS;
     const int E128 = (p.E + 127) & ~127, TK = p.T * p.k, TK8 = (TK + 7) & ~7;
-    sh.select.hi = reinterpret_cast<uint32_t *>(g + o); o += 4 * E128;
     sh.select.mask = reinterpret_cast<uint32_t *>(g + o); o += 4 * E128;
-    sh.select.cand = reinterpret_cast<unsigned long long *>(g + o); o += 8 * 64;
-    sh.select.cand_e = reinterpret_cast<uint16_t *>(g + o); o += 2 * 64;
     sh.select.weight = reinterpret_cast<float *>(g + o); o += 4 * TK8;
     sh.select.sel = reinterpret_cast<uint16_t *>(g + o); o += 2 * TK8;
     sh.tab = sh.select.tab = reinterpret_cast<Touched *>(g + o); o += (uint32_t)sizeof(Touched) * (TK8 < E128 ? TK8 : E128);
@@ -745,6 +760,9 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = p.stages, half = (S + 1) / 2;      // team 0's slots are [0, half), team 1's [half, S)
+    unsigned first_ticket = 0;
+    if (threadIdx.x == 32 * (CONSUMERS + 1)) first_ticket = atomicAdd(p.ctl + C_TICKET, 1u);
+    for (int e = threadIdx.x; e < E128; e += THREADS) sh.select.mask[e] = 0u;
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(sh.full + 8u * s, 1);
@@ -832,28 +850,33 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
     } else if (warp == CONSUMERS + 1) {
         // ------------------------------------------------------------ scheduler
         const unsigned fixed = (unsigned)(p.n.router_n + p.n.down_n + p.n.sgu_n);     // tickets that need no selection
-        unsigned next = 0;
+        unsigned next = first_ticket;
         int touched = 0;
-        if (lane == 0) next = atomicAdd(p.ctl + C_TICKET, 1u);
+        bool selecting = false;
         for (int q = 0;; ++q) {
             const unsigned tk = __shfl_sync(0xffffffffu, next, 0);
             int good = 1;
-            if (tk >= fixed && touched == 0) {
-#pragma unroll 1
-                for (int pass = 0; pass < 2 && good; ++pass) {
-                    if (pass) {
-                        if (lane == 0) good = wait_count(p.ctl, C_ROUTER, (unsigned)p.n.router_n, abort);
-                        good = __shfl_sync(0xffffffffu, good, 0);
+            if (tk >= fixed && selecting && touched == 0) {
+                // the loaders have the selection as their next item
+                if (lane == 0) {
+                    const volatile int *found = sh.flags + 25;
+                    const long long t0 = clock64();
+                    while (*found == 0 && good) {
+                        __nanosleep(20);
+                        if (*abort || clock64() - t0 > 2 * WAIT_LIMIT_CYCLES) good = 0;
                     }
-                    if (good) touched = select_experts<WT>(p, sh.select, lane, pass != 0);
+                    __threadfence_block();
                 }
+                good = __shfl_sync(0xffffffffu, good, 0);
                 if (!good) {
                     if (lane == 0) give_up(0x10);
                     break;
                 }
-                if (lane == 0) sh.flags[25] = touched;
+                touched = sh.flags[25];
             }
-            const Item it = item_of<WT>(p, touched, sh.tab, tk);
+            Item it = {SELECT, 0, 0, 0, 0, 0, 0, 0};      // (no ticket)
+            if (tk < fixed || touched) it = item_of<WT>(p, touched, sh.tab, tk);
+            else selecting = true;
             if (it.kind == ROUTED_GU || it.kind == ROUTED_DOWN) {
                 int c1, c2;
                 box_at(it, it.j0 + lane, &c1, &c2);
@@ -862,20 +885,25 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                                                       : p.wd + 16 * (int64_t)c2 * p.d_row));
             }
             if (lane == 0) {
-                // not far ahead of the producer, and the entry's previous item behind every reader
+                // not far ahead of the producer, and (looked at every eight items) far from every reader's tail
                 const long long t0 = clock64();
                 const volatile int *finished = sh.flags + 32;
-                for (int r = 0; r < LOADERS + 2 + CONSUMERS && good; ++r)
-                    while (q - (r < LOADERS + 2 ? passed[r] : finished[r - LOADERS - 2]) >= (r == LOADERS ? AHEAD : QUEUE) &&
-                           good) {
+                auto behind = [&](const volatile int *reader, int by) {
+                    while (q - *reader >= by && good) {
                         __nanosleep(20);
                         if (*abort || clock64() - t0 > 2 * WAIT_LIMIT_CYCLES) good = 0;
                     }
+                };
+                behind(passed + LOADERS, AHEAD);
+                if ((q & 7) == 0) {
+                    for (int r = 0; r < LOADERS + 2; ++r) behind(passed + r, QUEUE - 8);
+                    for (int r = 0; r < CONSUMERS; ++r) behind(finished + r, QUEUE - 8);
+                }
                 if (good) {
                     sh.queue[q % QUEUE] = it;
                     __threadfence_block();
                     *published = q + 1;
-                    if (it.kind != END) next = atomicAdd(p.ctl + C_TICKET, 1u);   // used in the next round
+                    if (it.kind != END && it.kind != SELECT) next = atomicAdd(p.ctl + C_TICKET, 1u);   // used in the next round
                 } else {
                     give_up(0x10);
                 }
@@ -900,6 +928,30 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
             }
             const Item it = sh.queue[q % QUEUE];
             if (it.kind == END) break;
+            if (it.kind == SELECT) {
+                // the next set's slot is the scratch
+                if (lane == 0) {
+                    good = mbar_wait(sh.act_empty + 8u * (set & 1), (uint32_t)((set >> 1) & 1) ^ 1u, abort) &&
+                           wait_count(p.ctl, C_ROUTER, (unsigned)p.n.router_n, abort);
+                }
+                ok = __shfl_sync(0xffffffffu, good, 0) != 0;
+                if (ok) {
+                    uint8_t *scratch = g + (sh.act - base) + (set & 1) * p.slot_bytes + lw * select_bytes(E128);
+#pragma unroll 1
+                    for (int t = lw; t < p.T; t += LOADERS) select_token<WT>(p, sh.select, scratch, t, lane);
+                    ok = bar.sync();
+                }
+                if (ok && lw == 0) {
+                    const int touched = touched_experts(p, sh.select, lane);
+                    __threadfence_block();
+                    if (lane == 0) *(volatile int *)(sh.flags + 25) = touched;
+                }
+                if (!ok) {
+                    if (lane == 0) give_up(0x4);
+                    break;
+                }
+                continue;
+            }
             if (weightless(it.kind)) continue;
             const ActPlan a = act_plan<WT>(p, it);
             const bool mx4 = WT == W_MX4 && (it.kind == ROUTED_GU || it.kind == ROUTED_DOWN);
@@ -1046,6 +1098,10 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
             const Item it = sh.queue[q % QUEUE];
             const int kind = it.kind;
             if (kind == END) break;
+            if (kind == SELECT) {
+                done();
+                continue;
+            }
             if (weightless(kind)) {
                 int good = 1;
                 if (lane == 0) {
@@ -1451,7 +1507,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
 size_t fixed_smem(const lmoe_config &c, int T)
 {
     const int E128 = (c.E + 127) / 128 * 128, TK8 = (T * c.k + 7) / 8 * 8;
-    return 1024 + 4 * RED_FLOATS + 8 * (size_t)E128 + 8 * 64 + 2 * 64 + 6 * (size_t)TK8 +
+    return 1024 + 4 * RED_FLOATS + 4 * (size_t)E128 + 6 * (size_t)TK8 +
            sizeof(Touched) * (size_t)std::min(TK8, E128) + 16 + sizeof(Item) * QUEUE + 8 * (2 * MAX_STAGES + 12) +
  64 + 64 + 192;
 }
@@ -1608,6 +1664,7 @@ cudaError_t few_launch(const lmoe_config &c, const FewMaps &m, const FewWeights 
     slot = std::max(slot, need(c.f, eb, two, true));
     slot = std::max(slot, need(c.f_shared, eb, two, true));
     slot = std::min(slot, 58 * 1024);
+    slot = std::max(slot, std::min(T, LOADERS) * select_bytes((c.E + 127) / 128 * 128));     // the selection's scratch
     slot = (slot + 1023) / 1024 * 1024;
     p.slot_bytes = slot;
     const int stage = STAGE_BYTES + (mx4 ? SCALE_BYTES : 0);
