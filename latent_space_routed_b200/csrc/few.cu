@@ -271,6 +271,18 @@ __device__ __forceinline__ bool wait_count(const unsigned *ctl, int word, unsign
     }
 }
 
+// fp32 bits (those of a bf16 in the upper half) as a double by integer operations: the conversion
+// instruction takes 8 cycles of a quarter SM, these 3 to 5.  Zeros and subnormals come out as
+// 2^-127 (1 + m), which is nothing beside a score's 2^-53.
+__device__ __forceinline__ double widen(uint32_t f)
+{
+    return __hiloint2double((int)((f & 0x80000000u) | (((f & 0x7fffffffu) >> 3) + 0x38000000u)), (int)(f << 29));
+}
+__device__ __forceinline__ double widen_bf16(uint32_t f)
+{
+    return __hiloint2double((int)((f & 0x80000000u) | (((f & 0x7fff0000u) >> 3) + 0x38000000u)), 0);
+}
+
 // Order-preserving 64-bit key of a double (-0 counts as 0).
 __device__ __forceinline__ unsigned long long key64(double v)
 {
@@ -533,15 +545,19 @@ __device__ __forceinline__ void select_token(const FewParams &p, const Select &q
 #pragma unroll 1
         for (int e0 = lane; e0 < 4 * E4; e0 += 256) {      // eight loads in flight
             double v[8];
+            float b[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = e0 + 32 * i < E ? __ldcg(r + e0 + 32 * i) : 0.0;
+            for (int i = 0; i < 8; ++i) {
+                v[i] = e0 + 32 * i < E ? __ldcg(r + e0 + 32 * i) : 0.0;
+                b[i] = e0 + 32 * i < E ? __ldg(p.bias + e0 + 32 * i) : 0.f;
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int e = e0 + 32 * i;
                 if (e >= 4 * E4) break;
                 unsigned long long key = 0ull;             // real keys > 0
                 if (e < E) {
-                    key = key64(v[i] + (double)__ldg(p.bias + e));
+                    key = key64(v[i] + (double)b[i]);
                     all_and &= (uint32_t)(key >> 32);
                     all_or |= (uint32_t)(key >> 32);
                 }
@@ -1175,30 +1191,43 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 const int row = lane >> 3, piece = lane & 7;
                 ok = stages(true, [&](int c, int k0) {
                     const uint32_t tile = sh.ring + (uint32_t)s * STAGE_BYTES + mytile;
-#pragma unroll 2
-                    for (int i = 0; i < 8; ++i) {
-                        const int kblk = c * 32 + sub * 8 + i;      // 512 bytes each: 4 rows
-                        if (kblk >= nkb) break;
-                        const int R = i * 4 + row;
-                        const uint4 w = lds128(tile + (uint32_t)(R * 128 + ((piece ^ (R & 7)) << 4)));
-                        const double w0 = __uint_as_float(w.x), w1 = __uint_as_float(w.y), w2 = __uint_as_float(w.z),
-                                     w3 = __uint_as_float(w.w);
-                        const int k = kblk * 32 + 4 * piece - k0;
+#pragma unroll 1
+                    for (int i0 = 0; i0 < 8; i0 += 4) {           // four k-blocks (512 bytes each: 4 rows) at a time
+                        const int kblk = c * 32 + sub * 8 + i0, left = nkb - kblk;
+                        if (left <= 0) break;
+                        double w[4][4];
 #pragma unroll
-                        for (int t = 0; t < FEW_MAX_T; ++t)
-                            if (t < p.T) {
-                                float x0, x1, x2, x3;
-                                if (WT == W_F32) {
-                                    const uint4 v = lds128(act + (uint32_t)(t * a.stride + 4 * k));
-                                    x0 = __uint_as_float(v.x); x1 = __uint_as_float(v.y);
-                                    x2 = __uint_as_float(v.z); x3 = __uint_as_float(v.w);
-                                } else {
-                                    const uint2 v = lds64(act + (uint32_t)(t * a.stride + 2 * k));
-                                    x0 = __uint_as_float(v.x << 16); x1 = __uint_as_float(v.x & 0xffff0000u);
-                                    x2 = __uint_as_float(v.y << 16); x3 = __uint_as_float(v.y & 0xffff0000u);
+                        for (int i = 0; i < 4; ++i) {             // zero-filled past K
+                            const int R = (i0 + i) * 4 + row;
+                            const uint4 v = lds128(tile + (uint32_t)(R * 128 + ((piece ^ (R & 7)) << 4)));
+                            w[i][0] = widen(v.x);
+                            w[i][1] = widen(v.y);
+                            w[i][2] = widen(v.z);
+                            w[i][3] = widen(v.w);
+                        }
+                        const uint32_t at = act + (uint32_t)((WT == W_F32 ? 4 : 2) * (kblk * 32 + 4 * piece - k0));
+#pragma unroll
+                        for (int t = 0; t < FEW_MAX_T; ++t) {
+                            if (t >= p.T) break;
+                            double sum[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                sum[i] = 0.0;
+                                if (i < left) {
+                                    double x[4];
+                                    if (WT == W_F32) {
+                                        const uint4 v = lds128(at + (uint32_t)(t * a.stride + 128 * i));
+                                        x[0] = widen(v.x); x[1] = widen(v.y); x[2] = widen(v.z); x[3] = widen(v.w);
+                                    } else {
+                                        const uint2 v = lds64(at + (uint32_t)(t * a.stride + 64 * i));
+                                        x[0] = widen_bf16(v.x << 16); x[1] = widen_bf16(v.x);
+                                        x[2] = widen_bf16(v.y << 16); x[3] = widen_bf16(v.y);
+                                    }
+                                    sum[i] = fma(w[i][0], x[0], w[i][1] * x[1]) + fma(w[i][2], x[2], w[i][3] * x[3]);
                                 }
-                                acc[t] += fma(w0, (double)x0, w1 * (double)x1) + fma(w2, (double)x2, w3 * (double)x3);
                             }
+                            acc[t] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        }
                     }
                     release();
                 });
