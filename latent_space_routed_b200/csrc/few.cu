@@ -443,56 +443,56 @@ __device__ __forceinline__ float red_sum(const float *cell, int n, bool packed)
 
 // A 128-byte k-block (eight blocks of 32 values, nb of them real) of two groups of 16
 // rows of 4-bit weights against eight columns: acc += scale of the row's block *
-// partial sum.  All words and scales come into registers first, then `release` gives
-// the stage back; the blocks' conversions and products overlap, two blocks at a time.
-template <bool PACKED, typename Release>
+// partial sum.  Two blocks per round, rolled: the body stays in the instruction buffers.
+template <bool PACKED>
 __device__ __forceinline__ void mx4_kblock(float (&acc)[2][4], uint32_t tile, uint32_t arow, uint32_t plane,
-                                           uint32_t scales, int gid, int c4, int nb, Release release)
+                                           uint32_t scales, int gid, int c4, int nb)
 {
-    uint32_t w[8][2][2];     // block, group, row gid + 8 h
-    uint2 e[2][2];
-#pragma unroll
-    for (int g = 0; g < 2; ++g)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            e[g][h] = lds64(scales + (uint32_t)(512 * g + 256 * h));
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                w[j][g][h] = lds32(tile + (uint32_t)(KBLK_BYTES * g + 1024 * h + ((j ^ gid) << 4) + 4 * c4));
-        }
-    release();
-#pragma unroll
-    for (int j0 = 0; j0 < 8; j0 += 2) {
-        if (j0 >= nb) break;         // nb is even: K is a multiple of 64
+#pragma unroll 1
+    for (int j0 = 0; j0 < nb; j0 += 2) {             // nb is even: K is a multiple of 64
+        uint32_t w[2][2][2], e[2][2];                // block, group, row gid + 8 h; scales of both blocks
         uint4 x[2], y[2];
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                e[g][h] = lds16(scales + (uint32_t)(512 * g + 256 * h + j0));
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    w[j][g][h] = lds32(tile + (uint32_t)(KBLK_BYTES * g + 1024 * h + (((j0 + j) ^ gid) << 4) + 4 * c4));
+            }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             x[j] = lds128(arow + 64u * (j0 + j));
             if (!PACKED) y[j] = lds128(arow + plane + 64u * (j0 + j));
         }
+        float t[2][2][4] = {};
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
                 uint32_t wa[4], wb[4];
-                e2m1x8_to_f16(wa, w[j0 + j][g][0]);
-                e2m1x8_to_f16(wb, w[j0 + j][g][1]);
-                float t[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_f16(t, wa[0], wb[0], wa[1], wb[1], x[j].x, x[j].y);
-                mma_f16(t, wa[2], wb[2], wa[3], wb[3], x[j].z, x[j].w);
+                e2m1x8_to_f16(wa, w[j][g][0]);
+                e2m1x8_to_f16(wb, w[j][g][1]);
+                mma_f16(t[j][g], wa[0], wb[0], wa[1], wb[1], x[j].x, x[j].y);
+                mma_f16(t[j][g], wa[2], wb[2], wa[3], wb[3], x[j].z, x[j].w);
                 if (!PACKED) {
-                    mma_f16(t, wa[0], wb[0], wa[1], wb[1], y[j].x, y[j].y);
-                    mma_f16(t, wa[2], wb[2], wa[3], wb[3], y[j].z, y[j].w);
+                    mma_f16(t[j][g], wa[0], wb[0], wa[1], wb[1], y[j].x, y[j].y);
+                    mma_f16(t[j][g], wa[2], wb[2], wa[3], wb[3], y[j].z, y[j].w);
                 }
+            }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
                 // 2^(e - 127); e = 0 counts as zero (below fp32's normal range), 255 is NaN
-                const uint32_t ea = j0 < 4 ? e[g][0].x : e[g][0].y, eb = j0 < 4 ? e[g][1].x : e[g][1].y;
-                const uint32_t xa = (ea >> (8 * ((j0 + j) & 3))) & 255u, xb = (eb >> (8 * ((j0 + j) & 3))) & 255u;
+                const uint32_t xa = (e[g][0] >> (8 * j)) & 255u, xb = (e[g][1] >> (8 * j)) & 255u;
                 const float fa = __uint_as_float(xa == 255u ? 0x7fffffffu : xa << 23);
                 const float fb = __uint_as_float(xb == 255u ? 0x7fffffffu : xb << 23);
-                acc[g][0] = fmaf(t[0], fa, acc[g][0]);
-                acc[g][1] = fmaf(t[1], fa, acc[g][1]);
-                acc[g][2] = fmaf(t[2], fb, acc[g][2]);
-                acc[g][3] = fmaf(t[3], fb, acc[g][3]);
+                acc[g][0] = fmaf(t[j][g][0], fa, acc[g][0]);
+                acc[g][1] = fmaf(t[j][g][1], fa, acc[g][1]);
+                acc[g][2] = fmaf(t[j][g][2], fb, acc[g][2]);
+                acc[g][3] = fmaf(t[j][g][3], fb, acc[g][3]);
             }
     }
 }
@@ -1191,13 +1191,15 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 const int row = lane >> 3, piece = lane & 7;
                 ok = stages(true, [&](int c, int k0) {
                     const uint32_t tile = sh.ring + (uint32_t)s * STAGE_BYTES + mytile;
+                    // two k-blocks (512 bytes each: 4 rows) per round: the body stays in the
+                    // instruction buffers (unrolled over a stage it took 3 K cycles, most of them fetches)
 #pragma unroll 1
-                    for (int i0 = 0; i0 < 8; i0 += 4) {           // four k-blocks (512 bytes each: 4 rows) at a time
+                    for (int i0 = 0; i0 < 8; i0 += 2) {
                         const int kblk = c * 32 + sub * 8 + i0, left = nkb - kblk;
                         if (left <= 0) break;
-                        double w[4][4];
+                        double w[2][4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {             // zero-filled past K
+                        for (int i = 0; i < 2; ++i) {             // zero-filled past K
                             const int R = (i0 + i) * 4 + row;
                             const uint4 v = lds128(tile + (uint32_t)(R * 128 + ((piece ^ (R & 7)) << 4)));
                             w[i][0] = widen(v.x);
@@ -1209,9 +1211,9 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
 #pragma unroll
                         for (int t = 0; t < FEW_MAX_T; ++t) {
                             if (t >= p.T) break;
-                            double sum[4];
+                            double sum[2];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
+                            for (int i = 0; i < 2; ++i) {
                                 sum[i] = 0.0;
                                 if (i < left) {
                                     double x[4];
@@ -1226,7 +1228,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                                     sum[i] = fma(w[i][0], x[0], w[i][1] * x[1]) + fma(w[i][2], x[2], w[i][3] * x[3]);
                                 }
                             }
-                            acc[t] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                            acc[t] += sum[0] + sum[1];
                         }
                     }
                     release();
@@ -1327,11 +1329,10 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                             const uint32_t tile = sh.ring + (uint32_t)s * STAGE_BYTES + mytile + 128u * gid;
                             const uint32_t sc = sh.scales + (uint32_t)(s * SCALE_BYTES + 32 * gid + 8 * sub);
                             const uint32_t arow = act + mycol + (uint32_t)(2 * (kblk * 256 - k0));
-                            if (packed) mx4_kblock<true>(acc, tile, arow, 0u, sc, gid, c4, nb, release);
-                            else mx4_kblock<false>(acc, tile, arow, plane, sc, gid, c4, nb, release);
-                        } else {
-                            release();
+                            if (packed) mx4_kblock<true>(acc, tile, arow, 0u, sc, gid, c4, nb);
+                            else mx4_kblock<false>(acc, tile, arow, plane, sc, gid, c4, nb);
                         }
+                        release();
                     });
                 } else {
                     // ---- bf16 rows: 64 values of 16 rows per tile
