@@ -947,10 +947,10 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
             if (it.kind == SELECT) {
                 // the next set's slot is the scratch
                 if (lane == 0) {
-                    good = mbar_wait(sh.act_empty + 8u * (set & 1), (uint32_t)((set >> 1) & 1) ^ 1u, abort) &&
-                           wait_count(p.ctl, C_ROUTER, (unsigned)p.n.router_n, abort);
+                    good = mbar_wait(sh.act_empty + 8u * (set & 1), (uint32_t)((set >> 1) & 1) ^ 1u, abort);
+                    if (good && lw == 0) good = wait_count(p.ctl, C_ROUTER, (unsigned)p.n.router_n, abort);
                 }
-                ok = __shfl_sync(0xffffffffu, good, 0) != 0;
+                ok = __shfl_sync(0xffffffffu, good, 0) != 0 && bar.sync();
                 if (ok) {
                     uint8_t *scratch = g + (sh.act - base) + (set & 1) * p.slot_bytes + lw * select_bytes(E128);
 #pragma unroll 1
@@ -979,7 +979,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 const int slot = set & 1;
                 if (lane == 0) {
                     good = mbar_wait(sh.act_empty + 8u * slot, (uint32_t)((set >> 1) & 1) ^ 1u, abort);
-                    if (good && it.kind != ready) {          // the items that write these values
+                    if (good && lw == 0 && it.kind != ready) {          // the items that write these values
                         if (it.kind == ROUTED_GU && !p.standard) good = wait_count(p.ctl, C_Z, (unsigned)p.n.down_n, abort);
                         // (the failure-detection test waits for one count too many)
                         if (it.kind == SHARED_DOWN)
@@ -991,8 +991,9 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                                    wait_count(p.ctl, C_PART, 2u * p.n.sd_n, abort);
                     }
                 }
+                // one warp of a block polls (all of them on one word kept each other waiting for 3 us)
+                ok = __shfl_sync(0xffffffffu, good, 0) != 0 && (it.kind == ready || bar.sync());
                 ready = it.kind;
-                ok = __shfl_sync(0xffffffffu, good, 0) != 0;
                 if (!ok) {
                     if (lane == 0) give_up(0x4);
                     break;
@@ -1120,7 +1121,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
             }
             if (weightless(kind)) {
                 int good = 1;
-                if (lane == 0) {
+                if (threadIdx.x == 0) {
                     good = wait_count(p.ctl, C_YS, (unsigned)(sh.flags[25] * p.n.rd_n), abort);
                     if (good && p.standard) good = wait_count(p.ctl, C_PART, 2u * p.n.sd_n, abort);
                 }
