@@ -173,8 +173,9 @@ LMOE_API lmoe_status lmoe_mx4_dequantize(const void *codes, const void *scales, 
  *                      values are taken ascending and clamped to [0, M]; rows
  *                      of out that belong to no expert are left as they were
  *  out                 [M, N] dtype, row stride ldo elements
- *  workspace           LMOE_MX4_GEMM_WORKSPACE_BYTES, 256-byte aligned; calls
- *                      that may overlap need one each
+ *  workspace           LMOE_MX4_GEMM_WORKSPACE_BYTES, 256-byte aligned, zero
+ *                      before its first call; calls that may overlap need one
+ *                      each
  * K is a multiple of 64, codes are 16-byte aligned, E <= 1024.  M or N 0 is a
  * no-op.  Runs on the current device, which must be the tensors'.
  * INVALID_ARG: NULL pointer, negative size, unknown dtype, E < 1, ldo < N.
@@ -185,8 +186,8 @@ LMOE_API lmoe_status lmoe_mx4_gemm(const void *a_codes, const void *a_scales, in
                                    int32_t dtype, void *out, int64_t ldo, void *workspace, size_t ws_bytes,
                                    void *stream);
 
-/* Synchronise `stream`, then read and clear the status word of the last
- * lmoe_mx4_gemm on this workspace: LMOE_OK or LMOE_ERR_DEVICE_TIMEOUT. */
+/* Synchronise `stream`, then read and clear the status word of the
+ * lmoe_mx4_gemm calls on this workspace: LMOE_OK or LMOE_ERR_DEVICE_TIMEOUT. */
 LMOE_API lmoe_status lmoe_mx4_gemm_check(void *workspace, void *stream);
 
 /* Routed experts in 4 bits (device pointers, read only during the create call):
@@ -198,7 +199,11 @@ typedef struct {
 
 /* lmoe_create with the routed experts in 4 bits: w->G, w->U and w->D are not
  * read (they may be NULL), and the handle holds only the 4-bit experts.  All
- * other weights, and the tokens, are bf16 on the tensor-core path.
+ * other weights, and the tokens, are bf16 on the tensor-core path.  lmoe_forward
+ * (and its host and noalloc forms) quantises the slot rows of z and the routed
+ * hidden to 4 bits as well and runs both products on 4-bit tensor cores;
+ * lmoe_forward_few keeps both at more than bf16's precision against the 4-bit
+ * weights, so the two differ by that quantisation.
  * Errors as lmoe_create; also UNSUPPORTED for another dtype or gemm = 1, or
  * codes that are not 16-byte aligned. */
 LMOE_API lmoe_status lmoe_create_mx4(const lmoe_config *cfg, const lmoe_weights *w, const lmoe_mx4_experts *experts,
@@ -369,6 +374,8 @@ LMOE_API lmoe_status lmoe_launch_count(const lmoe_handle *h, int64_t T, int32_t 
  * cutoff [T] fp32 (each token's (k+1)-th biased score, -inf when k = E);
  * 12 slot rows [T*k, l] (z of each slot's token, expert-sorted; 0 bytes when
  * the routed GEMVs of a few tokens read z through the slot -> token map).
+ * With 4-bit experts (0 bytes otherwise) 13, 14 codes and scales of the slot
+ * rows, 15, 16 of the routed hidden (then 7 has 0 bytes).
  * INVALID_ARG for an unknown region. */
 LMOE_API lmoe_status lmoe_workspace_region(const lmoe_handle *h, int64_t T, int32_t region, size_t *offset,
                                   size_t *bytes);

@@ -11,6 +11,7 @@ Importing fails loudly (ImportError) when the library has not been built:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Dict, NamedTuple, Optional
@@ -30,7 +31,7 @@ STATUS_NAMES = {0: "LMOE_OK", 1: "LMOE_ERR_INVALID_ARG", 2: "LMOE_ERR_UNSUPPORTE
 
 # lmoe_workspace_region ids
 REGION = {"scores": 0, "p32": 1, "counts": 2, "offsets": 3, "slot_of": 4, "perm_tok": 5, "Z": 6, "H": 7,
-          "Y": 8, "HS": 9, "status": 10, "cutoff": 11, "Zp": 12}
+          "Y": 8, "HS": 9, "status": 10, "cutoff": 11, "Zp": 12, "Zp4": 13, "Zp4_scales": 14, "H4": 15, "H4_scales": 16}
 
 EXPORTS = ("lmoe_config_from_base", "lmoe_create", "lmoe_workspace_size", "lmoe_forward", "lmoe_host_workspace_size",
            "lmoe_forward_host", "lmoe_forward_noalloc", "lmoe_create_mx4", "lmoe_few_workspace_size", "lmoe_forward_few",
@@ -307,9 +308,15 @@ class Mx4(NamedTuple):
         return self
 
 
-def _on(device, stream):
-    """The stream handle to use for tensors of `device`."""
-    return torch.cuda.current_stream(device) if stream is None else stream
+def _with(device, stream):
+    """`device` and `stream`, where they are not the current ones, made current for what is inside: copies and
+    allocations are then ordered with the kernel."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            handle = _stream(stream)
+            stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+        return torch.cuda.stream(stream)
+    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def mx4_quantize(x: torch.Tensor, stream=None) -> Mx4:
@@ -324,17 +331,17 @@ def mx4_quantize(x: torch.Tensor, stream=None) -> Mx4:
     if cols % 32:
         raise ValueError(f"the last dimension {cols} is not a multiple of 32")
     per16 = 16 // x.element_size()
-    # a matrix whose rows are whole and 16-byte aligned is read as it lies; anything else is laid out first
-    x2 = x if x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= cols and x.stride(0) % per16 == 0 \
-        else x.reshape(-1, cols).contiguous() if cols else x.reshape(x.numel() or 0, 0)
-    if x2.data_ptr() % 16:
-        x2 = x2.clone(memory_format=torch.contiguous_format)
-    with torch.cuda.device(x.device):
+    with _with(x.device, stream):
+        # a matrix whose rows are whole and 16-byte aligned is read as it lies; anything else is laid out first
+        x2 = x if x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= cols and x.stride(0) % per16 == 0 \
+            else x.reshape(-1, cols).contiguous() if x.numel() else x
+        if x2.data_ptr() % 16:
+            x2 = x2.clone(memory_format=torch.contiguous_format)
         q = Mx4(torch.empty((*lead, cols // 2), dtype=torch.uint8, device=x.device),
                 torch.empty((*lead, cols // 32), dtype=torch.uint8, device=x.device))
         if x.numel():
             lmoe_mx4_quantize(x2, _LM_DT[x.dtype], x2.shape[0], cols, x2.stride(0) if x2.shape[0] > 1 else cols,
-                              q.codes, q.scales, _on(x.device, stream))
+                              q.codes, q.scales)
     return q
 
 
@@ -344,17 +351,16 @@ def mx4_dequantize(q: Mx4, dtype: torch.dtype = torch.bfloat16, stream=None) -> 
         raise TypeError(f"fp32 or bf16 expected, got {dtype}")
     q.check("q")
     cols = 2 * q.codes.shape[-1]
-    with torch.cuda.device(q.codes.device):
+    with _with(q.codes.device, stream):
         y = torch.empty(q.shape, dtype=dtype, device=q.codes.device)
         if y.numel():
-            lmoe_mx4_dequantize(q.codes, q.scales, y.numel() // cols, cols, _LM_DT[dtype], y, cols,
-                                _on(y.device, stream))
+            lmoe_mx4_dequantize(q.codes, q.scales, y.numel() // cols, cols, _LM_DT[dtype], y, cols)
     return y
 
 
 def mx4_gemm_workspace(device=None) -> torch.Tensor:
     """A workspace for mx4_gemm calls that follow one another on one stream."""
-    return torch.empty(LMOE_MX4_GEMM_WORKSPACE_BYTES, dtype=torch.uint8,
+    return torch.zeros(LMOE_MX4_GEMM_WORKSPACE_BYTES, dtype=torch.uint8,
                        device=torch.device("cuda", torch.cuda.current_device()) if device is None else device)
 
 
@@ -375,19 +381,20 @@ def mx4_gemm(a: Mx4, w: Mx4, offsets: Optional[torch.Tensor] = None, dtype: torc
     if offsets is not None and (offsets.dtype != torch.int32 or offsets.shape != (E + 1,) or offsets.device != dev
                                 or not offsets.is_contiguous()):
         raise ValueError(f"offsets must be a contiguous int32 tensor [{E + 1}] on {dev}")
+    if (dtype if out is None else out.dtype) not in _LM_DT:
+        raise TypeError(f"fp32 or bf16 expected, got {dtype if out is None else out.dtype}")
     if out is None:
         make = torch.empty if offsets is None else torch.zeros
-        out = make(M, N, dtype=dtype, device=dev)
-    if out.dtype not in _LM_DT:
-        raise TypeError(f"fp32 or bf16 expected, got {out.dtype}")
+        with _with(dev, stream):
+            out = make(M, N, dtype=dtype, device=dev)
     if out.shape != (M, N) or (N > 1 and out.stride(1) != 1) or (M > 1 and out.stride(0) < N):
         raise ValueError(f"out must be [{M}, {N}] with whole rows")
     if w.codes.device != dev or out.device != dev or (workspace is not None and workspace.device != dev):
         raise ValueError(f"all tensors must be on {dev}")
-    with torch.cuda.device(dev):
+    with _with(dev, stream):
         ws = mx4_gemm_workspace(dev) if workspace is None else workspace
         lmoe_mx4_gemm(a.codes, a.scales, M, w.codes, w.scales, N, K, offsets, E, _LM_DT[out.dtype], out,
-                      out.stride(0) if M > 1 else N, ws, ws.numel() * ws.element_size(), _on(dev, stream))
+                      out.stride(0) if M > 1 else N, ws, ws.numel() * ws.element_size())
     return out
 
 
@@ -493,8 +500,9 @@ class LatentMoE:
         if x.shape[-1] != c.d:
             raise ValueError(f"last dim {x.shape[-1]} != d={c.d}")
         lead = x.shape[:-1]
-        x2 = x.reshape(-1, c.d).to(device=self.device, dtype=self.dtype).contiguous()
-        out = forward_into(x2, self.empty_outputs(x2.shape[0]), stream=stream)
+        with contextlib.nullcontext() if stream is None else _with(self.device, stream):
+            x2 = x.reshape(-1, c.d).to(device=self.device, dtype=self.dtype).contiguous()
+            out = forward_into(x2, self.empty_outputs(x2.shape[0]), stream=stream)
         return {"output": out["output"].reshape(*lead, c.d),
                 "selected_experts": out["selected_experts"].reshape(*lead, c.k),
                 "mixture_weights": out["mixture_weights"].reshape(*lead, c.k),

@@ -371,7 +371,7 @@ __device__ __forceinline__ Item item_of(const FewParams &p, int touched, const T
     } else if ((i -= n.sgu_n) < rgu_total) {
         it.kind = ROUTED_GU; it.ti = divide(i, n.rgu_n, n.rgu_inv); i -= it.ti * n.rgu_n;
         it.reps = n.rgu_r; it.nkb = WT == W_MX4 ? (p.l + 255) / 256 : p.l / KE; per = p.f / 16;
-        it.block0 = tab[it.ti].expert * (p.f / 32);
+        it.block0 = tab[it.ti].expert * (p.f / (WT == W_MX4 ? 16 : 32));
     } else if ((i -= rgu_total) < n.sd_n || (i >= n.sd_n + rd_total && i < 2 * n.sd_n + rd_total)) {
         it.kind = SHARED_DOWN; it.ti = i >= n.sd_n; i -= it.ti ? n.sd_n + rd_total : 0;
         it.reps = n.sd_r; it.nkb = p.fs / KE; it.kb0 = it.ti * it.nkb; per = p.d / 32;
@@ -406,11 +406,13 @@ __device__ __forceinline__ int out_row(int kind, int j)
     return j * (kind == ROUTER ? 4 : kind == SHARED_DOWN || kind == ROUTED_DOWN ? 32 : 16);
 }
 // Coordinates of a sub-item's boxes: row (of its block), block of rows.
+template <int WT>
 __device__ __forceinline__ void box_at(const Item &it, int j, int *c1, int *c2)
 {
-    if (it.kind == SHARED_GU || it.kind == ROUTED_GU) {     // gate and up rows in blocks of 64
-        *c1 = 16 * (j & 3);
-        *c2 = it.block0 + 2 * (j >> 2);
+    if (it.kind == SHARED_GU || it.kind == ROUTED_GU) {     // gate and up rows in blocks of 64 (4 bits: 32)
+        const int sh = WT == W_MX4 && it.kind == ROUTED_GU ? 1 : 2;
+        *c1 = 16 * (j & ((1 << sh) - 1));
+        *c2 = it.block0 + 2 * (j >> sh);
     } else if (it.kind == SHARED_DOWN || it.kind == ROUTED_DOWN) {
         *c1 = 0;
         *c2 = it.block0 + 2 * j;
@@ -832,8 +834,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 // stages in the order in which the teams take them: chunk by chunk of a pair of sub-items
                 for (int r = 0; r < it.reps && ok; r += 2) {
                     int c1[2], c2[2];
-                    box_at(it, it.j0 + r, &c1[0], &c2[0]);
-                    box_at(it, it.j0 + r + 1, &c1[1], &c2[1]);
+                    box_at<WT>(it, it.j0 + r, &c1[0], &c2[0]);
+                    box_at<WT>(it, it.j0 + r + 1, &c1[1], &c2[1]);
                     const bool pair = !split && r + 1 < it.reps;
                     for (int i = 0; i < (pair ? 2 * nc : nc) && ok; ++i) {
                         const int team = split || pair ? i & 1 : 0, c = pair ? i >> 1 : i;
@@ -895,9 +897,9 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
             else selecting = true;
             if (it.kind == ROUTED_GU || it.kind == ROUTED_DOWN) {
                 int c1, c2;
-                box_at(it, it.j0 + lane, &c1, &c2);
+                box_at<WT>(it, it.j0 + lane, &c1, &c2);
                 if (lane < it.reps)
-                    prefetch_l2((it.kind == ROUTED_GU ? p.wgu + (64 * (int64_t)c2 + c1) * p.gu_row
+                    prefetch_l2((it.kind == ROUTED_GU ? p.wgu + ((WT == W_MX4 ? 32 : 64) * (int64_t)c2 + c1) * p.gu_row
                                                       : p.wd + 16 * (int64_t)c2 * p.d_row));
             }
             if (lane == 0) {
@@ -1633,8 +1635,8 @@ bool few_make_maps(const lmoe_config &c, const FewWeights &w, FewMaps *m)
     const uint32_t ke = f32 ? 32 : 64;
     const uint64_t eb = f32 ? 4 : 2;
     // Rows of K values as 128-byte k-blocks.  One group: a box is eight k-blocks of
-    // 16 rows.  Two groups: rows in blocks of `block` (64: gate and up alternate;
-    // 16: consecutive rows), a box is four k-blocks of 16 rows of two blocks.
+    // 16 rows.  Two groups: rows in blocks of `block` (64, for 4 bits 32: gate
+    // and up alternate; 16: consecutive rows), a box is four k-blocks of 16 rows of two blocks.
     auto one = [&](CUtensorMap *t, const void *base, uint64_t K, uint64_t nrows) {
         return tc_encode_map(t, ty, base, 3, {ke, nrows, K / ke}, {K * eb, 128}, {ke, 16, 8}, true);
     };
@@ -1659,8 +1661,8 @@ bool few_make_maps(const lmoe_config &c, const FewWeights &w, FewMaps *m)
                     (c.standard || (one(&m->down, w.Wdown, d, l) && one(&m->up, w.Wcat, cat, d))) &&
                     two(&m->shared_gu, w.Wgu_s, d, 4 * fs, 64) && two(&m->shared_down, w.Wcat, cat, d, 16);
     if (w.mx4)
-        return ok && codes(&m->routed_gu, w.Wgu, l, E * 2 * f, 64) && codes(&m->routed_down, w.D, f, E * l, 16) &&
-               scales(&m->routed_gu_scales, w.Wgu_scales, l, E * 2 * f, 64) &&
+        return ok && codes(&m->routed_gu, w.Wgu, l, E * 2 * f, 32) && codes(&m->routed_down, w.D, f, E * l, 16) &&
+               scales(&m->routed_gu_scales, w.Wgu_scales, l, E * 2 * f, 32) &&
                scales(&m->routed_down_scales, w.D_scales, f, E * l, 16);
     return ok && two(&m->routed_gu, w.Wgu, l, E * 2 * f, 64) && two(&m->routed_down, w.D, f, E * l, 16);
 }

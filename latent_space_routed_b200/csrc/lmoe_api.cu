@@ -2,7 +2,7 @@
 // handle-owned repacked weights, the workspace plan, and the launch sequence
 // of one layer forward on one stream.
 //
-// Forward sequence for T tokens (S = T k slot rows):
+// (lmoe_forward_few: few.cu.)  Forward sequence for T tokens (S = T k slot rows):
 //   1 router GEMM      r = sigmoid(x W_r^T)                     [T, E] fp32
 //   2 top-k            sel, p (fp32 and token dtype), per-block expert counts
 //   3 scan             counts, offsets, per-block bases, m-tile prefix
@@ -14,6 +14,8 @@
 //   9 combine+norm     u = sum_j Y[slot_of[t, j]], n = RMSNorm(u)
 //  10 shared gate/up   h_s = act([G_1; G_2] x, [U_1; U_2] x)    [T, 2 f_s]
 //  11 final GEMM       y = [h_s | n] [D_s1 | D_s2 | W_up]^T     [T, d]
+// 4-bit experts: 6 is followed by the quantisation of Zp, 7 and 8 are 4-bit products, the gate's outputs
+// quantised in 7's epilogue.
 // The standard-MoE form (config.standard) skips 5, permutes x, skips the norm
 // in 9 and computes y = h_s [D_s1 | D_s2]^T + u in 11.
 //
@@ -74,7 +76,7 @@ int64_t hs_cols(const lmoe_config &c) { return 2 * (int64_t)c.f_shared + (c.stan
 
 struct Layout {
     size_t r32, p32, blockhist, base, counts, offsets, tile_off, slot_of, perm_tok, perm_w, z, Zp, H, Yp, HS, partial,
-        partial_side, cutoff, status, touched, final32;
+        partial_side, cutoff, status, touched, final32, Zp4, Zp4s, H4, H4s;
     size_t total;
 };
 
@@ -139,7 +141,7 @@ constexpr int SPLIT_MAX = 16;
 
 // Few-token plans of the tensor-core path.
 bool small_route(const lmoe_handle *h, int64_t T) { return h->tc && T <= ROUTE_SMALL_MAX_T; }
-bool gemv_experts(const lmoe_handle *h, int64_t T) { return h->tc && T <= GEMV_MAX_T; }
+bool gemv_experts(const lmoe_handle *h, int64_t T) { return h->tc && !h->mx4 && T <= GEMV_MAX_T; }
 // Few tokens, latent form: the final GEMV's shared-expert columns (K = 2 f_s of
 // 2 f_s + l) run as their own GEMV into an fp32 partial on the side stream,
 // beside the routed GEMVs; the final GEMV after the combine + RMSNorm then
@@ -236,7 +238,7 @@ Layout plan(const lmoe_handle *h, int64_t T)
     L.perm_w = take(sizeof(float) * S);
     L.z = take(c.standard ? 0 : h->tb * T * c.l);   // the standard form permutes x itself
     L.Zp = take(h->tb * S * c.l);
-    L.H = take(h->tb * S * c.f);
+    L.H = take(h->mx4 ? 0 : h->tb * S * c.f);
     L.Yp = take(h->tb * S * c.l);
     L.HS = take(h->tb * T * (2 * (int64_t)c.f_shared + c.l));
     const SplitPlan sp = plan_splits(h, T);
@@ -245,6 +247,11 @@ Layout plan(const lmoe_handle *h, int64_t T)
     L.cutoff = take(sizeof(float) * T);
     L.touched = take(sizeof(int32_t) * c.E);
     L.final32 = take(split_final(h, T) ? sizeof(float) * T * c.d : 0);
+    // 4-bit experts: slot rows and hidden as codes and scales
+    L.Zp4 = take(h->mx4 ? S * (c.l / 2) : 0);
+    L.Zp4s = take(h->mx4 ? S * (c.l / 32) : 0);
+    L.H4 = take(h->mx4 ? S * (c.f / 2) : 0);
+    L.H4s = take(h->mx4 ? S * (c.f / 32) : 0);
     L.total = o;
     return L;
 }
@@ -399,11 +406,11 @@ static lmoe_status create_handle(const lmoe_config *cfg, const lmoe_weights *w, 
     if (!c.standard) STEP(cudaMemcpyAsync(h->Wdown, w->W_down, tb * c.l * c.d, cudaMemcpyDeviceToDevice, s));
     if (x4) {
         STEP(cudaMemcpyAsync(h->D, x4->D, (size_t)c.E * c.l * (c.f / 2), cudaMemcpyDeviceToDevice, s));
-        STEP(launch_pack_glu(x4->G, x4->U, h->Wgu, c.E, c.f, c.l / 32, h->ib, 16, s));
+        STEP(launch_pack_glu(x4->G, x4->U, h->Wgu, c.E, c.f, c.l / 32, MX4_GLU_BLOCK, 16, s));
         STEP(launch_mx4_pack_scales((const uint8_t *)x4->G_scales, (const uint8_t *)x4->U_scales, h->Wgu_scales, c.E,
-                                    c.f, c.l / 32, pitch_l, h->ib, s));
+                                    c.f, c.l / 32, pitch_l, MX4_GLU_BLOCK, s));
         STEP(launch_mx4_pack_scales((const uint8_t *)x4->D_scales, nullptr, h->D_scales, c.E, c.l, c.f / 32, pitch_f,
-                                    h->ib, s));
+                                    MX4_GLU_BLOCK, s));
     } else {
         STEP(cudaMemcpyAsync(h->D, w->D, tb * (size_t)c.E * c.l * c.f, cudaMemcpyDeviceToDevice, s));
         STEP(launch_pack_glu(w->G, w->U, h->Wgu, c.E, c.f, c.l, h->ib, (int)tb, s));
@@ -531,6 +538,18 @@ lmoe_status lmoe_mx4_dequantize(const void *codes, const void *scales, int64_t r
     return LMOE_OK;
 }
 
+// tc_check_device, once per device (of the first 64).
+static lmoe_status tc_device_once()
+{
+    static std::atomic<uint64_t> good{0};
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) return LMOE_ERR_CUDA;
+    if (dev < 64 && (good.load() >> dev & 1u)) return LMOE_OK;
+    const lmoe_status st = tc_check_device();
+    if (st == LMOE_OK && dev < 64) good.fetch_or((uint64_t)1 << dev);
+    return st;
+}
+
 lmoe_status lmoe_mx4_gemm(const void *a_codes, const void *a_scales, int64_t M, const void *w_codes,
                           const void *w_scales, int64_t N, int64_t K, const int32_t *offsets, int32_t E, int32_t dtype,
                           void *out, int64_t ldo, void *workspace, size_t ws_bytes, void *stream)
@@ -553,9 +572,8 @@ lmoe_status lmoe_mx4_gemm(const void *a_codes, const void *a_scales, int64_t M, 
     if (((uintptr_t)a_codes | (uintptr_t)w_codes) & 15u)
         return fail(LMOE_ERR_UNSUPPORTED, "codes must be 16-byte aligned");
     if ((uintptr_t)out % (dtype == LMOE_BF16 ? 2 : 4)) return fail(LMOE_ERR_UNSUPPORTED, "out is misaligned");
-    const lmoe_status st = tc_check_device();
+    const lmoe_status st = tc_device_once();
     if (st != LMOE_OK) return fail(st, "4-bit products need an sm_100 device");
-    LMOE_CUDA(cudaMemsetAsync(workspace, 0, sizeof(int32_t), (cudaStream_t)stream));
     Mx4GemmArgs g = {};
     g.a_codes = (const uint8_t *)a_codes; g.a_scales = (const uint8_t *)a_scales; g.a_pitch = K / 32;
     g.w_codes = (const uint8_t *)w_codes; g.w_scales = (const uint8_t *)w_scales; g.w_pitch = K / 32;
@@ -590,12 +608,16 @@ lmoe_status lmoe_workspace_region(const lmoe_handle *h, int64_t T, int32_t regio
     case 4: *offset = L.slot_of; *bytes = sizeof(int32_t) * S; break;
     case 5: *offset = L.perm_tok; *bytes = sizeof(int32_t) * S; break;
     case 6: *offset = L.z; *bytes = c.standard ? 0 : h->tb * T * c.l; break;
-    case 7: *offset = L.H; *bytes = h->tb * S * c.f; break;
+    case 7: *offset = L.H; *bytes = h->mx4 ? 0 : h->tb * S * c.f; break;
     case 8: *offset = L.Yp; *bytes = h->tb * S * c.l; break;
     case 9: *offset = L.HS; *bytes = h->tb * T * (2 * (int64_t)c.f_shared + c.l); break;
     case 10: *offset = L.status; *bytes = sizeof(int32_t); break;
     case 11: *offset = L.cutoff; *bytes = sizeof(float) * T; break;
     case 12: *offset = L.Zp; *bytes = gemv_experts(h, T) ? 0 : h->tb * S * c.l; break;
+    case 13: *offset = L.Zp4; *bytes = h->mx4 ? S * (c.l / 2) : 0; break;
+    case 14: *offset = L.Zp4s; *bytes = h->mx4 ? S * (c.l / 32) : 0; break;
+    case 15: *offset = L.H4; *bytes = h->mx4 ? S * (c.f / 2) : 0; break;
+    case 16: *offset = L.H4s; *bytes = h->mx4 ? S * (c.f / 32) : 0; break;
     default: return fail(LMOE_ERR_INVALID_ARG, "unknown region %d", region);
     }
     return LMOE_OK;
@@ -646,7 +668,7 @@ lmoe_status lmoe_launch_count(const lmoe_handle *h, int64_t T, int32_t *launches
     const SplitPlan sp = plan_splits(h, T);
     *launches = 11 - (c.standard ? 1 : 0) + (sp.down > 1) + (sp.shared > 1) + (sp.final_ > 1) -
                 (small_route(h, T) ? 3 : 0) - (gemv_experts(h, T) ? 1 : 0) - (sp.fused_router ? 1 : 0) +
-                (split_final(h, T) ? 1 : 0);
+                (split_final(h, T) ? 1 : 0) + (h->mx4 ? 1 : 0);   // 4-bit experts: quantised slot rows
     return LMOE_OK;
 }
 
@@ -703,7 +725,6 @@ static lmoe_status forward_body(lmoe_handle *h, const void *x, int64_t T, void *
     if (!h) return fail(LMOE_ERR_INVALID_ARG, "handle is NULL");
     if (T < 0) return fail(LMOE_ERR_INVALID_ARG, "T < 0");
     if (T == 0) return LMOE_OK;
-    if (h->mx4) return fail(LMOE_ERR_UNSUPPORTED, "4-bit experts: not built yet");
     if (!x || !output || !selected_experts || !mixture_weights || !latent_routed_aggregate || !workspace)
         return fail(LMOE_ERR_INVALID_ARG, "NULL tensor pointer");
     if (T * h->cfg.k > 0x7fffffffLL) return fail(LMOE_ERR_UNSUPPORTED, "T * k exceeds 2^31 - 1");
@@ -865,8 +886,20 @@ static lmoe_status forward_body(lmoe_handle *h, const void *x, int64_t T, void *
         LMOE_CUDA(launch_permute_tokens(c.standard ? x : z, slot_of, Zp, T, c.k, c.l, (int)h->tb, q));
         return LMOE_OK;
     };
+    // 4-bit experts: the slot rows quantised, H = act(G z, U z) quantised in the product's epilogue, and the
+    // weighted rows of the down-projection
+    Mx4GemmArgs m4 = {};
+    m4.M = (int)S; m4.E = c.E; m4.offsets = offsets; m4.act = c.act; m4.gate_cap = c.gate_cap; m4.up_cap = c.up_cap;
     auto st_gate_up = [&](cudaStream_t q) -> lmoe_status {
-        if (gemv_routed) {
+        if (h->mx4) {
+            uint8_t *zc = (uint8_t *)ws + L.Zp4, *zs = (uint8_t *)ws + L.Zp4s;
+            LMOE_CUDA(launch_mx4_quantize(Zp, 1, S, c.l, c.l, zc, zs, q));
+            Mx4GemmArgs g = m4;
+            g.mode = MX4_GLU; g.a_codes = zc; g.a_scales = zs; g.a_pitch = c.l / 32;
+            g.w_codes = (const uint8_t *)h->Wgu; g.w_scales = h->Wgu_scales; g.w_pitch = mx4_scale_pitch(c.l);
+            g.N = 2 * c.f; g.K = c.l; g.out = ws + L.H4; g.out_scales = (uint8_t *)ws + L.H4s;
+            LMOE_CUDA(launch_mx4_gemm(g, status, q));
+        } else if (gemv_routed) {
             GemmArgs g = gu;
             g.A = c.standard ? x : z;
             g.lda = c.l;
@@ -877,7 +910,13 @@ static lmoe_status forward_body(lmoe_handle *h, const void *x, int64_t T, void *
         return LMOE_OK;
     };
     auto st_down_combine = [&](cudaStream_t q) -> lmoe_status {
-        if (gemv_routed)
+        if (h->mx4) {
+            Mx4GemmArgs g = m4;
+            g.mode = MX4_WEIGHTED; g.a_codes = (const uint8_t *)ws + L.H4; g.a_scales = (const uint8_t *)ws + L.H4s;
+            g.a_pitch = c.f / 32; g.w_codes = (const uint8_t *)h->D; g.w_scales = h->D_scales;
+            g.w_pitch = mx4_scale_pitch(c.f); g.N = c.l; g.K = c.f; g.out = Yp; g.out_bf16 = 1; g.ldo = c.l; g.row_w = perm_w;
+            LMOE_CUDA(launch_mx4_gemm(g, status, q));
+        } else if (gemv_routed)
             LMOE_CUDA(launch_gemv_grouped(EPI_COMBINE, gc, touched, status + CTL_NTOUCHED,
                                           (int)std::min<int64_t>(c.E, S), nullptr, (int)T, q));
         else if (h->tc) LMOE_CUDA(tc_gemm(EPI_COMBINE, gc, max_mtiles, cg_grouped, status, q));

@@ -15,12 +15,19 @@
 // a byte per value, the outputs 2 or 4 bytes each (prompt slot rows: outputs are 55 %
 // of the bytes), and with few rows per expert the weights are nearly all of them.
 //
+// Epilogues: plain (bf16 or fp32 rows); rows times a weight each (the routed down-projection);
+// and the gate of the routed experts with requantisation: columns alternate between 32
+// gates and their 32 ups, so that a lane holds one row's gates and ups of a whole block of 32
+// outputs, applies the gate to the fp32 sums and stores 16 bytes of codes and the scale.
+//
 // Warps: 0 TMA producer; 1 TMEM owner and MMA issuer; 2-5 scales: rows of K / 32 bytes
 // are read with plain loads one stage ahead (any row start, so that a group may begin
 // anywhere) and written as the 32 x 16-byte matrices that tcgen05.cp spreads over the
 // lanes; 6-13 epilogue, two per TMEM lane quarter.
 //
 // Every wait is bounded; one that gives up sets the status word and ends its role.
+#include <atomic>
+
 #include "gemm_tc.cuh"
 #include "mx4.cuh"
 #include "ptx.cuh"
@@ -52,8 +59,12 @@ struct Params {
     int64_t a_pitch, w_pitch;     // bytes between scale rows
     int M, N, K, E, grouped;
     const int32_t *offsets;
-    void *out;
+    void *out;                    // GLU: codes [M, N / 4]
     int64_t ldo;
+    uint8_t *out_scales;          // GLU: [M, N / 64]
+    const float *row_w;           // WEIGHTED: weight of each row
+    int act;
+    float gate_cap, up_cap;
     int32_t *status;
 };
 
@@ -199,7 +210,24 @@ __device__ __forceinline__ void store_row<float>(float *dst, const float (&v)[32
     }
 }
 
-template <typename TO>
+// A block of 32 values as 16 bytes of codes and its scale byte (see mx4.cu).
+__device__ __forceinline__ uint4 quantize_block(const float (&v)[32], uint32_t *scale)
+{
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    const uint32_t e = m >> 23, sc = e > 2u ? e - 2u : 0u;
+    *scale = e < 255u ? sc : 255u;
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    if (e < 255u) {
+        const float inv = __uint_as_float((254u - sc) << 23);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i >> 2] |= f32_to_e2m1x2(v[2 * i] * inv, v[2 * i + 1] * inv) << (8 * (i & 3));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <typename TO, int MODE>
 __global__ void __launch_bounds__(THREADS, 1)
 mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW, const __grid_constant__ Params p)
 {
@@ -418,13 +446,36 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             TO *dst = (TO *)p.out + (int64_t)row * p.ldo + t.n0;
             const uint32_t src = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * BN);
             if (t.row0 + 32 * q < t.row_end) {                  // uniform: some row of this quarter is real
+                if (MODE == MX4_GLU) {
 #pragma unroll 1
-                for (int c = 96 * hset; c < 96 * hset + 96; c += 32) {
-                    const int left = p.N - t.n0 - c;
-                    if (left <= 0) break;
-                    float v[32];
-                    tmem_ld32(src + c, v);
-                    if (row < t.row_end) store_row<TO>(dst + c, v, left, vec);
+                    for (int c = 64 * hset; c < BN && t.n0 + c < p.N; c += 128) {     // N is a multiple of 64
+                        float v[32], u[32];
+                        tmem_ld32(src + c, v);
+                        tmem_ld32(src + c + 32, u);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = glu_act(p.act, v[i], u[i], p.gate_cap, p.up_cap);
+                        uint32_t scale;
+                        const uint4 w = quantize_block(v, &scale);
+                        if (row < t.row_end) {
+                            const int64_t block = (int64_t)row * (p.N / 64) + (t.n0 + c) / 64;
+                            reinterpret_cast<uint4 *>(p.out)[block] = w;
+                            p.out_scales[block] = (uint8_t)scale;
+                        }
+                    }
+                } else {
+                    const float weight = MODE == MX4_WEIGHTED && row < t.row_end ? p.row_w[row] : 1.f;
+#pragma unroll 1
+                    for (int c = 96 * hset; c < 96 * hset + 96; c += 32) {
+                        const int left = p.N - t.n0 - c;
+                        if (left <= 0) break;
+                        float v[32];
+                        tmem_ld32(src + c, v);
+                        if (MODE == MX4_WEIGHTED) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] *= weight;
+                        }
+                        if (row < t.row_end) store_row<TO>(dst + c, v, left, vec);
+                    }
                 }
             }
             fence_before();
@@ -449,12 +500,19 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-template <typename TO>
+template <typename TO, int MODE>
 cudaError_t launch(const CUtensorMap &a, const CUtensorMap &w, const Params &p, int grid, cudaStream_t s)
 {
-    cudaError_t e = cudaFuncSetAttribute(mx4_gemm_kernel<TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
+    static std::atomic<uint64_t> ready{0};       // devices (the first 64) whose shared-memory limit is set
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    mx4_gemm_kernel<TO><<<grid, THREADS, SMEM, s>>>(a, w, p);
+    if (dev >= 64 || !(ready.load() >> dev & 1u)) {
+        e = cudaFuncSetAttribute(mx4_gemm_kernel<TO, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready.fetch_or((uint64_t)1 << dev);
+    }
+    mx4_gemm_kernel<TO, MODE><<<grid, THREADS, SMEM, s>>>(a, w, p);
     return cudaGetLastError();
 }
 }  // namespace
@@ -474,7 +532,10 @@ cudaError_t launch_mx4_gemm(const Mx4GemmArgs &g, int32_t *status, cudaStream_t 
     const int64_t tiles = ((g.M + BM - 1) / BM + (g.offsets ? g.E : 0)) * ntn;     // at most
     const int sms = tc_num_sms() > 0 ? tc_num_sms() : 148;
     const int grid = (int)(tiles < sms ? tiles : sms);
-    return g.out_bf16 ? launch<bf16>(a, w, p, grid, s) : launch<float>(a, w, p, grid, s);
+    p.out_scales = g.out_scales; p.row_w = g.row_w; p.act = g.act; p.gate_cap = g.gate_cap; p.up_cap = g.up_cap;
+    if (g.mode == MX4_GLU) return launch<bf16, MX4_GLU>(a, w, p, grid, s);
+    if (g.mode == MX4_WEIGHTED) return launch<bf16, MX4_WEIGHTED>(a, w, p, grid, s);
+    return g.out_bf16 ? launch<bf16, MX4_STORE>(a, w, p, grid, s) : launch<float, MX4_STORE>(a, w, p, grid, s);
 }
 
 }  // namespace lmoe
