@@ -86,7 +86,7 @@ struct Item {
     int j0, reps;        // first sub-item of the matrix (of the expert, the half), and how many
     int block0;          // first block of rows of the matrix (two groups)
     int kb0, nkb;        // first k-block (128 bytes of a row) in the matrix, and their number
-    int ncol;            // columns of the product in use
+    int ncol;            // rows of activations in the slot
     int ti;              // touched-expert index, or half of the shared experts
 };
 
@@ -446,19 +446,26 @@ __device__ __forceinline__ float red_sum(const float *cell, int n, bool packed)
 // A 128-byte k-block (eight blocks of 32 values, nb of them real) of two groups of 16
 // rows of 4-bit weights against eight columns: acc += scale of the row's block *
 // partial sum.  Two blocks per round, rolled: the body stays in the instruction buffers.
+// A scale byte becomes fp32's exponent field: 2^(e - 127), but 0 for e = 0 (2^-127, below
+// fp32's normal range) and infinity for 255, whose blocks the handle's codes hold as zeros:
+// 0 x infinity is the NaN that they stand for.
 template <bool PACKED>
 __device__ __forceinline__ void mx4_kblock(float (&acc)[2][4], uint32_t tile, uint32_t arow, uint32_t plane,
                                            uint32_t scales, int gid, int c4, int nb)
 {
+    uint2 e[2][2];                                   // a row's eight scales; two move out per round
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) e[g][h] = lds64(scales + (uint32_t)(512 * g + 256 * h));
 #pragma unroll 1
     for (int j0 = 0; j0 < nb; j0 += 2) {             // nb is even: K is a multiple of 64
-        uint32_t w[2][2][2], e[2][2];                // block, group, row gid + 8 h; scales of both blocks
+        uint32_t w[2][2][2];                         // block, group, row gid + 8 h
         uint4 x[2], y[2];
 #pragma unroll
         for (int g = 0; g < 2; ++g)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                e[g][h] = lds16(scales + (uint32_t)(512 * g + 256 * h + j0));
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
                     w[j][g][h] = lds32(tile + (uint32_t)(KBLK_BYTES * g + 1024 * h + (((j0 + j) ^ gid) << 4) + 4 * c4));
@@ -487,14 +494,19 @@ __device__ __forceinline__ void mx4_kblock(float (&acc)[2][4], uint32_t tile, ui
         for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-                // 2^(e - 127); e = 0 counts as zero (below fp32's normal range), 255 is NaN
-                const uint32_t xa = (e[g][0] >> (8 * j)) & 255u, xb = (e[g][1] >> (8 * j)) & 255u;
-                const float fa = __uint_as_float(xa == 255u ? 0x7fffffffu : xa << 23);
-                const float fb = __uint_as_float(xb == 255u ? 0x7fffffffu : xb << 23);
+                const float fa = __uint_as_float(e[g][0].x << (23 - 8 * j) & 0x7f800000u);
+                const float fb = __uint_as_float(e[g][1].x << (23 - 8 * j) & 0x7f800000u);
                 acc[g][0] = fmaf(t[j][g][0], fa, acc[g][0]);
                 acc[g][1] = fmaf(t[j][g][1], fa, acc[g][1]);
                 acc[g][2] = fmaf(t[j][g][2], fb, acc[g][2]);
                 acc[g][3] = fmaf(t[j][g][3], fb, acc[g][3]);
+            }
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                e[g][h].x = __funnelshift_r(e[g][h].x, e[g][h].y, 16);
+                e[g][h].y >>= 16;
             }
     }
 }
@@ -1137,8 +1149,19 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
             const bool two = two_groups(kind), split = (p.n.split >> it.kind & 1u) != 0u;
             const int nc = chunks(it), nkb = it.nkb;
             const uint32_t plane = (uint32_t)(it.ncol * a.stride);
+            // Columns of the product: the slot's rows, but of the routed gate/up (whose slot holds
+            // every token) only the expert's tokens.  `tok`: the row of column lane % 8 (past the
+            // last column: the last one's)
+            const unsigned mask = kind == ROUTED_GU ? (unsigned)sh.tab[it.ti].mask : 0u;
+            const int ncol = kind == ROUTED_GU ? __popc(mask) : it.ncol;
+            int tok = min(lane & 7, ncol - 1);
+            if (kind == ROUTED_GU) {
+                unsigned m = mask;
+                for (; tok > 0; --tok) m &= m - 1u;
+                tok = __ffs(m) - 1;
+            }
             // Four columns or fewer of two terms: hi in columns 0-3, lo in 4-7 of one product
-            const bool packed = a.planes == 2 && it.ncol <= 4;
+            const bool packed = a.planes == 2 && ncol <= 4;
             const bool mx4 = WT == W_MX4 && (kind == ROUTED_GU || kind == ROUTED_DOWN);
             // values of K per stage
             const int kshift = kind == ROUTER ? 10 : mx4 ? 10 : (WT == W_F32 ? 5 : 6) + (two ? 2 : 3);
@@ -1283,8 +1306,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                             }
 #pragma unroll
                             for (int t = 0; t < FEW_MAX_T; ++t)
-                                if (t < it.ncol) {
-                                    const uint4 v = lds128(act + (uint32_t)(t * a.stride + 4 * k));
+                                if (t < ncol) {
+                                    const uint4 v = lds128(act + (uint32_t)(__shfl_sync(0xffffffffu, tok, t) * a.stride + 4 * k));
 #pragma unroll
                                     for (int i = 0; i < 4; ++i) {
                                         acc[g][i][t] = fmaf(w[i].x, __uint_as_float(v.x), acc[g][i][t]);
@@ -1302,7 +1325,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 if (!(ok = red_writable())) break;
 #pragma unroll
                 for (int t = 0; t < FEW_MAX_T; ++t)
-                    if (t < it.ncol) {
+                    if (t < ncol) {
 #pragma unroll
                         for (int g = 0; g < 2; ++g)
 #pragma unroll
@@ -1315,10 +1338,10 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                     }
             } else {
                 float acc[2][4] = {};
-                // the activation row of one of the eight columns (columns past the tokens repeat the last)
+                // where column r's activations are
                 auto column = [&](int r) -> uint32_t {
-                    const int t = packed ? (r & 3) : r;
-                    return (uint32_t)((t < it.ncol ? t : it.ncol - 1) * a.stride) + (packed && r >= 4 ? plane : 0u);
+                    return (uint32_t)(__shfl_sync(0xffffffffu, tok, packed ? (r & 3) : r) * a.stride) +
+                           (packed && r >= 4 ? plane : 0u);
                 };
                 if (mx4) {
                     // ---- 4-bit rows: a 16-byte piece of a row is one block of 32 values, eight of
@@ -1423,7 +1446,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
             // what becomes of them: thread (row, token) of 16 x 8, both groups of rows.  What the
             // epilogue reads from global memory is asked for before the barrier.
             const int cell = threadIdx.x & 127, row = cell >> 3, t = cell & 7;
-            const bool real = t < it.ncol && !(split && team);
+            const bool real = t < ncol && !(split && team);
             const int r = out_row(kind, it.j0 + rr) + row;
             float add = 0.f;
             int slot = -1;
@@ -1438,10 +1461,9 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                     add = sh.select.weight[slot];
                 }
             } else if (kind == ROUTED_GU) {
-                const unsigned mask = (unsigned)sh.tab[it.ti].mask;
-                if (real && (mask >> t & 1u)) slot = sh.tab[it.ti].slot[__popc(mask & ((1u << t) - 1u))];
+                if (real) slot = sh.tab[it.ti].slot[t];
             }
-            const float back = mx4 && real ? sh.inv[8 * (set & 1) + t] : 1.f;
+            const float back = mx4 && real ? sh.inv[8 * (set & 1) + tok] : 1.f;
             if (!(ok = split ? bar.sync() : tbar.sync())) break;
             if (split && team) break;                      // (its one sub-item)
             const float *cells = sh.red + (split ? 0 : 4 * team) * RED_WARP + cell;

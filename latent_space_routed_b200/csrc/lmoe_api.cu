@@ -407,10 +407,10 @@ static lmoe_status create_handle(const lmoe_config *cfg, const lmoe_weights *w, 
     if (x4) {
         STEP(cudaMemcpyAsync(h->D, x4->D, (size_t)c.E * c.l * (c.f / 2), cudaMemcpyDeviceToDevice, s));
         STEP(launch_pack_glu(x4->G, x4->U, h->Wgu, c.E, c.f, c.l / 32, MX4_GLU_BLOCK, 16, s));
-        STEP(launch_mx4_pack_scales((const uint8_t *)x4->G_scales, (const uint8_t *)x4->U_scales, h->Wgu_scales, c.E,
-                                    c.f, c.l / 32, pitch_l, MX4_GLU_BLOCK, s));
-        STEP(launch_mx4_pack_scales((const uint8_t *)x4->D_scales, nullptr, h->D_scales, c.E, c.l, c.f / 32, pitch_f,
-                                    MX4_GLU_BLOCK, s));
+        STEP(launch_mx4_pack_scales((const uint8_t *)x4->G_scales, (const uint8_t *)x4->U_scales, h->Wgu_scales, h->Wgu,
+                                    c.E, c.f, c.l / 32, pitch_l, MX4_GLU_BLOCK, s));
+        STEP(launch_mx4_pack_scales((const uint8_t *)x4->D_scales, nullptr, h->D_scales, h->D, c.E, c.l, c.f / 32,
+                                    pitch_f, MX4_GLU_BLOCK, s));
     } else {
         STEP(cudaMemcpyAsync(h->D, w->D, tb * (size_t)c.E * c.l * c.f, cudaMemcpyDeviceToDevice, s));
         STEP(launch_pack_glu(w->G, w->U, h->Wgu, c.E, c.f, c.l, h->ib, (int)tb, s));

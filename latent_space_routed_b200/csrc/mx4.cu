@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(THREADS) dequantize_kernel(const uint32_t *__r
 }
 
 __global__ void pack_scales_kernel(const uint8_t *__restrict__ G, const uint8_t *__restrict__ U,
-                                   uint8_t *__restrict__ out, int64_t rows, int F, int blocks, int64_t pitch, int ib)
+                                   uint8_t *__restrict__ out, uint4 *__restrict__ codes, int64_t rows, int F, int blocks,
+                                   int64_t pitch, int ib)
 {
     const int64_t total = rows * pitch;
     for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
@@ -133,6 +134,7 @@ __global__ void pack_scales_kernel(const uint8_t *__restrict__ G, const uint8_t 
             }
         }
         out[i] = v;
+        if (v == 255u) codes[r * blocks + c] = make_uint4(0u, 0u, 0u, 0u);
     }
 }
 
@@ -177,10 +179,10 @@ cudaError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, i
     return cudaGetLastError();
 }
 
-cudaError_t launch_mx4_pack_scales(const uint8_t *G, const uint8_t *U, uint8_t *out, int64_t nE, int F, int blocks,
-                                   int64_t pitch, int ib, cudaStream_t s)
+cudaError_t launch_mx4_pack_scales(const uint8_t *G, const uint8_t *U, uint8_t *out, void *codes, int64_t nE, int F,
+                                   int blocks, int64_t pitch, int ib, cudaStream_t s)
 {
-    pack_scales_kernel<<<2048, 256, 0, s>>>(G, U, out, nE * F * (U ? 2 : 1), F, blocks, pitch, ib);
+    pack_scales_kernel<<<2048, 256, 0, s>>>(G, U, out, (uint4 *)codes, nE * F * (U ? 2 : 1), F, blocks, pitch, ib);
     return cudaGetLastError();
 }
 

@@ -11,9 +11,11 @@ cudaError_t launch_mx4_quantize(const void *x, int bf16_in, int64_t rows, int64_
 cudaError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols, void *y,
                                   int bf16_out, int64_t ld, cudaStream_t s);
 // Scale rows of `blocks` bytes to rows `pitch` bytes apart, zero behind them.  With U != nullptr the rows
-// of G and U [nE, F] are interleaved in blocks of ib, as launch_pack_glu does with the codes.
-cudaError_t launch_mx4_pack_scales(const uint8_t *G, const uint8_t *U, uint8_t *out, int64_t nE, int F, int blocks,
-                                   int64_t pitch, int ib, cudaStream_t s);
+// of G and U [nE, F] are interleaved in blocks of ib, as launch_pack_glu does with the codes.  `codes`: the
+// codes in the new order, where blocks of scale 255 (NaN) become zeros (the few-token kernel multiplies
+// them by infinity).
+cudaError_t launch_mx4_pack_scales(const uint8_t *G, const uint8_t *U, uint8_t *out, void *codes, int64_t nE, int F,
+                                   int blocks, int64_t pitch, int ib, cudaStream_t s);
 
 // C [M, N] = A W^T of 4-bit matrices (mx4_gemm.cu); grouped when offsets != nullptr
 // (device [E + 1], W of expert e at rows e N).  K a multiple of 64, codes 16-byte

@@ -300,6 +300,21 @@ def test_layer_stages(T, d, l, f, E, k, act, standard):
     assert all(torch.equal(again[n], out[n]) for n in out)
 
 
+def test_nan_blocks_of_the_experts_reach_their_tokens_only():
+    """A block of scale 255 stands for NaN whatever its codes: in the few-token form and in the other."""
+    w = li.custom("mx4", 40, 256, 128, 256, 16, 4, 128, seed=3)
+    W = li.weights(w)
+    x = li.tokens(w).cuda()
+    for name, at in (("G", (5, 17, 3)), ("U", (5, 0, 0)), ("D", (5, 127, 7))):
+        Q = {n: lm.mx4_quantize(W[n].cuda()) for n in ("G", "U", "D")}
+        Q[name].scales[at] = 255
+        layer = lm.LatentMoE(lm.config_for(w), {**{n: v.cuda() for n, v in W.items() if n not in Q}, **Q})
+        for out in (layer(x), layer.forward_few(x[:8]), layer.forward_few(x[3:4])):
+            has = (out["selected_experts"] == 5).any(1)
+            assert torch.equal(torch.isnan(out["latent_routed_aggregate"]).any(1), has)
+            assert torch.equal(torch.isnan(out["output"]).any(1), has)
+
+
 def test_layer_host_and_noalloc_forms():
     w = li.custom("mx4", 40, 256, 128, 256, 16, 4, 128, seed=2)
     layer, _, _ = mx4_layer(w)
