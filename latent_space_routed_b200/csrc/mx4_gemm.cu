@@ -245,7 +245,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(full + 8 * s, 1 + SF_WARPS);
+            mbar_init(full + 8 * s, 2);                        // the copies, the scales
             mbar_init(empty + 8 * s, 1);
         }
         for (int a = 0; a < 2; ++a) {
@@ -368,7 +368,8 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         }
     } else if (warp < 2 + SF_WARPS) {
         // ---------------------------------------------------------- scales
-        const int tid = threadIdx.x - 64;                      // rows tid of A; tid and tid + 128 of W
+        // Warp w brings every fourth stage, all 320 rows of it (lane: rows lane + 32 i), and asks for
+        // its next one before it waits for the slot: four stages of small loads are in flight
         const int n = p.K / 32;
         auto align_of = [](const uint8_t *b, int64_t pitch) {
             const uint64_t v = (uint64_t)b | (uint64_t)pitch;
@@ -376,56 +377,53 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         };
         const int al_a = align_of(p.a_scales, p.a_pitch), al_w = align_of(p.w_scales, p.w_pitch);
         const int64_t wrows = (int64_t)(p.grouped ? p.E : 1) * p.N;
-        int s = 0;
-        uint32_t ph = 0;
-        bool ok = true;
-        int item = blockIdx.x, kb = 0;
-        uint2 ra, rw0, rw1;
-        const uint8_t *pa = nullptr, *pw0 = nullptr, *pw1 = nullptr;
-        bool va = false, vw0 = false, vw1 = false;
-        auto point = [&]() {
-            const Tile t = decode(p, tile_off, row_off, item, ntn);
-            va = t.row0 + tid < t.row_end;
-            pa = p.a_scales + (int64_t)(t.row0 + tid) * p.a_pitch;
-            const int64_t w = t.wrow + tid;
-            vw0 = w < wrows;
-            vw1 = w + 128 < wrows && tid < BN - 128;
-            pw0 = p.w_scales + w * p.w_pitch;
-            pw1 = pw0 + 128 * p.w_pitch;
+        const int first = warp - 2;
+        int item = blockIdx.x, kb = 0, at = -1;
+        Tile t;
+        uint2 r[10];                                           // rows of A, then of W
+        auto advance = [&](int by) {                           // `by` stages on; the tile where it changes
+            for (kb += by; kb >= nkb; kb -= nkb) item += gridDim.x;
+            if (item < total && item != at) t = decode(p, tile_off, row_off, item, ntn);
+            at = item;
         };
         auto fetch = [&]() {
-            ra = load_scales(pa, kb * 8, n, va, al_a);
-            rw0 = load_scales(pw0, kb * 8, n, vw0, al_w);
-            rw1 = load_scales(pw1, kb * 8, n, vw1, al_w);
+            const uint8_t *pa = p.a_scales + (int64_t)(t.row0 + lane) * p.a_pitch;
+            const uint8_t *pw = p.w_scales + (int64_t)(t.wrow + lane) * p.w_pitch;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                r[i] = load_scales(pa + 32 * i * p.a_pitch, kb * 8, n, t.row0 + 32 * i + lane < t.row_end, al_a);
+#pragma unroll
+            for (int i = 0; i < 6; ++i)
+                r[4 + i] = load_scales(pw + 32 * i * p.w_pitch, kb * 8, n, t.wrow + 32 * i + lane < wrows, al_w);
         };
-        if (item < total) {
-            point();
-            fetch();
-        }
+        bool ok = true;
+        int s = first % STAGES;
+        uint32_t ph = 0;
+        advance(first);
+        if (item < total) fetch();
         while (item < total) {
-            const uint2 a = ra, w0 = rw0, w1 = rw1;
-            if (++kb == nkb) {
-                kb = 0;
-                item += gridDim.x;
-                if (item < total) point();
-            }
-            if (item < total) fetch();                         // the next stage's, while this one's slot is awaited
+            uint2 v[10];
+#pragma unroll
+            for (int i = 0; i < 10; ++i) v[i] = r[i];
+            advance(SF_WARPS);
+            if (item < total) fetch();                         // while this stage's slot is awaited
             ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * s, ph ^ 1u, abort));
             if (!ok) break;
             // row r of a 128-row chunk: 4 bytes at (r % 32) * 16 + (r / 32) * 4
-            const uint32_t sf = base + (uint32_t)(s * STAGE_BYTES + A_BYTES + B_BYTES) + (uint32_t)((tid & 31) * 16 + (tid >> 5) * 4);
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(sf), "r"(a.x) : "memory");
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(sf + 512), "r"(a.y) : "memory");
+            const uint32_t sf = base + (uint32_t)(s * STAGE_BYTES + A_BYTES + B_BYTES) + (uint32_t)(lane * 16);
             const uint32_t sw = sf + SFA_BYTES;
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(sw), "r"(w0.x) : "memory");
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(sw + 512), "r"(w1.x) : "memory");
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(sw + 1024), "r"(w0.y) : "memory");
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(sw + 1536), "r"(w1.y) : "memory");
+            sts128(sf, v[0].x, v[1].x, v[2].x, v[3].x);
+            sts128(sf + 512, v[0].y, v[1].y, v[2].y, v[3].y);
+            sts128(sw, v[4].x, v[5].x, v[6].x, v[7].x);
+            sts64(sw + 512, v[8].x, v[9].x);
+            sts128(sw + 1024, v[4].y, v[5].y, v[6].y, v[7].y);
+            sts64(sw + 1536, v[8].y, v[9].y);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(full + 8 * s);
-            if (++s == STAGES) {
-                s = 0;
+            s += SF_WARPS;
+            if (s >= STAGES) {
+                s -= STAGES;
                 ph ^= 1u;
             }
         }
