@@ -889,13 +889,13 @@ static lmoe_status forward_body(lmoe_handle *h, const void *x, int64_t T, void *
     // 4-bit experts: the slot rows quantised, H = act(G z, U z) quantised in the product's epilogue, and the
     // weighted rows of the down-projection
     Mx4GemmArgs m4 = {};
-    m4.M = (int)S; m4.E = c.E; m4.offsets = offsets; m4.act = c.act; m4.gate_cap = c.gate_cap; m4.up_cap = c.up_cap;
+    m4.M = (int)S; m4.E = c.E; m4.offsets = offsets; m4.gate_cap = c.gate_cap; m4.up_cap = c.up_cap;
     auto st_gate_up = [&](cudaStream_t q) -> lmoe_status {
         if (h->mx4) {
             uint8_t *zc = (uint8_t *)ws + L.Zp4, *zs = (uint8_t *)ws + L.Zp4s;
             LMOE_CUDA(launch_mx4_quantize(Zp, 1, S, c.l, c.l, zc, zs, q));
             Mx4GemmArgs g = m4;
-            g.mode = MX4_GLU; g.a_codes = zc; g.a_scales = zs; g.a_pitch = c.l / 32;
+            g.mode = c.act == LMOE_ACT_SITU ? MX4_GLU_SITU : MX4_GLU; g.a_codes = zc; g.a_scales = zs; g.a_pitch = c.l / 32;
             g.w_codes = (const uint8_t *)h->Wgu; g.w_scales = h->Wgu_scales; g.w_pitch = mx4_scale_pitch(c.l);
             g.N = 2 * c.f; g.K = c.l; g.out = ws + L.H4; g.out_scales = (uint8_t *)ws + L.H4s;
             LMOE_CUDA(launch_mx4_gemm(g, status, q));

@@ -23,14 +23,14 @@ cudaError_t launch_mx4_pack_scales(const uint8_t *G, const uint8_t *U, uint8_t *
 enum Mx4Mode {
     MX4_STORE = 0,       // out [M, N], bf16 or fp32
     MX4_WEIGHTED = 1,    // bf16 out, row m times row_w[m]
-    MX4_GLU = 2          // columns alternate 32 gates, 32 ups: act(gate, up) requantised to out (codes) and out_scales
+    MX4_GLU = 2,         // columns alternate 32 gates, 32 ups: SwiGLU requantised to out (codes) and out_scales
+    MX4_GLU_SITU = 3     // the same with the SiTU gate
 };
 constexpr int MX4_GLU_BLOCK = 32;
 struct Mx4GemmArgs {
     int mode;
     uint8_t *out_scales;
     const float *row_w;
-    int act;
     float gate_cap, up_cap;
     const uint8_t *a_codes, *a_scales, *w_codes, *w_scales;
     int64_t a_pitch, w_pitch;

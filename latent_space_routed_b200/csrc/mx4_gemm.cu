@@ -7,8 +7,8 @@
 // tcgen05.mma kind::mxf4 (block_scale, scale_vec::2X) takes the codes from shared memory
 // (128-byte-swizzled tiles, 256 values per row) and the scales from tensor memory.
 // One tile is 128 x 192: two fp32 accumulators take 384 of the 512 TMEM columns, so
-// that the epilogue of a tile overlaps the next one's main loop, and the scales of five
-// ring stages take 120 more (24 each: 4 per 128 rows and 128 values).  With 256
+// that the epilogue of a tile overlaps the next one's main loop, and the scales of four
+// ring stages take 96 more (24 each: 4 per 128 rows and 128 values).  With 256
 // columns per tile there would be room for one accumulator only.
 //
 // What bounds it is memory wherever the layer uses it: codes and scales are 17/32 of
@@ -40,7 +40,7 @@ constexpr int BM = 128, BN = 192, KB = 256;              // tile; K values per s
 constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
 constexpr int SFA_BYTES = 2 * 512, SFB_BYTES = 2 * 1024;  // two 128-value chunks; 128 and 256 rows each
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
-constexpr int STAGES = 5;
+constexpr int STAGES = 4;                                 // five: prompt rows 2 % slower, the rest the same
 constexpr int SF_WARPS = 4, EPI_WARPS = 8;
 constexpr int THREADS = 32 * (2 + SF_WARPS + EPI_WARPS);
 constexpr int MAX_E = 1024;
@@ -63,7 +63,6 @@ struct Params {
     int64_t ldo;
     uint8_t *out_scales;          // GLU: [M, N / 64]
     const float *row_w;           // WEIGHTED: weight of each row
-    int act;
     float gate_cap, up_cap;
     int32_t *status;
 };
@@ -174,39 +173,82 @@ __device__ __forceinline__ uint2 load_scales(const uint8_t *row, int at, int n, 
     return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
 }
 
-template <typename TO>
-__device__ __forceinline__ void store_row(TO *dst, const float (&v)[32], int n, bool vec);
-template <>
-__device__ __forceinline__ void store_row<bf16>(bf16 *dst, const float (&v)[32], int n, bool vec)
+// 16-byte pieces: piece j of the lane's row -> piece lane % 4 of the row of lane (lane & ~3) + j.
+__device__ __forceinline__ void transpose4(uint4 (&c)[4], int lane)
 {
+    auto exchange = [&](uint32_t &lo, uint32_t &hi, int bit) {
+        const bool upper = (lane & bit) != 0;
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? lo : hi, bit);
+        if (upper) lo = got; else hi = got;
+    };
+    auto pieces = [&](uint4 &lo, uint4 &hi, int bit) {
+        exchange(lo.x, hi.x, bit);
+        exchange(lo.y, hi.y, bit);
+        exchange(lo.z, hi.z, bit);
+        exchange(lo.w, hi.w, bit);
+    };
+    pieces(c[0], c[1], 1);
+    pieces(c[2], c[3], 1);
+    pieces(c[0], c[2], 2);
+    pieces(c[1], c[3], 2);
+}
+
+// 32 columns of 32 rows (a row per lane, `rows` of them real) to dst = the first row's, ldo apart.  Four lanes
+// first exchange pieces, so that a store writes 64-byte parts of eight rows: a lane that stores its own row
+// 16 bytes at a time makes every store touch 32 lines (prompt rows: 1488 us against 1086).
+template <typename TO>
+__device__ __forceinline__ void store_block(TO *dst, int64_t ldo, const float (&v)[32], int rows, int n, bool vec, int lane)
+{
+    constexpr int PER = 16 / (int)sizeof(TO);        // values per piece
     if (vec && n >= 32) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            uint32_t w[4];
+        for (int part = 0; part < 32 / (4 * PER); ++part) {
+            uint4 c[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * q + 2 * i], v[8 * q + 2 * i + 1]);
-                w[i] = *reinterpret_cast<const uint32_t *>(&b);
+            for (int j = 0; j < 4; ++j) {
+                const float *x = v + 4 * PER * part + PER * j;
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if constexpr (sizeof(TO) == 2) {
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+                        w[i] = *reinterpret_cast<const uint32_t *>(&b);
+                    } else {
+                        w[i] = __float_as_uint(x[i]);
+                    }
+                c[j] = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            reinterpret_cast<uint4 *>(dst)[q] = make_uint4(w[0], w[1], w[2], w[3]);
+            transpose4(c, lane);
+            TO *at = dst + 4 * PER * part + PER * (lane & 3);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int row = (lane & ~3) + j;
+                if (row < rows) *reinterpret_cast<uint4 *>(at + row * ldo) = c[j];
+            }
         }
-    } else {
+    } else if (lane < rows) {
+        dst += lane * ldo;
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-            if (i < n) dst[i] = __float2bfloat16_rn(v[i]);
+            if (i < n) {
+                if constexpr (sizeof(TO) == 2) dst[i] = __float2bfloat16_rn(v[i]);
+                else dst[i] = v[i];
+            }
     }
 }
-template <>
-__device__ __forceinline__ void store_row<float>(float *dst, const float (&v)[32], int n, bool vec)
+
+// The gate of 32 outputs.  SwiGLU with the hardware's exponential and reciprocal: 2^-21 of the value, where
+// what follows rounds to 4 bits.  SiTU is its own instantiation: both in one unrolled body (with
+// full-precision functions) made the kernel wait for instructions (98304 slot rows x 2816 x 512: 783 us, now 195).
+template <bool SITU>
+__device__ __forceinline__ void gate(float (&g)[32], const float (&u)[32], float cg, float cu)
 {
-    if (vec && n >= 32) {
+    if (SITU) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-            reinterpret_cast<float4 *>(dst)[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        for (int i = 0; i < 32; ++i) g[i] = glu_act(LMOE_ACT_SITU, g[i], u[i], cg, cu);
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < n) dst[i] = v[i];
+        for (int i = 0; i < 32; ++i) g[i] = g[i] * __fdividef(1.f, 1.f + __expf(-g[i])) * u[i];
     }
 }
 
@@ -430,6 +472,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         if (!ok && lane == 0) give_up(0x4);
     } else {
         // ---------------------------------------------------------- epilogue
+        constexpr bool GLU = MODE == MX4_GLU || MODE == MX4_GLU_SITU;
         const int q = warp & 3, hset = (warp - 2 - SF_WARPS) >> 2;     // lane quarter; half of the columns
         const bool vec = ((uintptr_t)p.out & 15u) == 0 && (p.ldo * (int)sizeof(TO)) % 16 == 0;
         int local = 0;
@@ -441,17 +484,16 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             if (!ok) break;
             fence_after();
             const int row = t.row0 + 32 * q + lane;
-            TO *dst = (TO *)p.out + (int64_t)row * p.ldo + t.n0;
+            TO *dst = (TO *)p.out + (int64_t)(t.row0 + 32 * q) * p.ldo + t.n0;
             const uint32_t src = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * BN);
             if (t.row0 + 32 * q < t.row_end) {                  // uniform: some row of this quarter is real
-                if (MODE == MX4_GLU) {
+                if (GLU) {
 #pragma unroll 1
-                    for (int c = 64 * hset; c < BN && t.n0 + c < p.N; c += 128) {     // N is a multiple of 64
+                    for (int c = 64 * (hset ^ (local & 1)); c < BN && t.n0 + c < p.N; c += 128) {  // N: a multiple of 64
                         float v[32], u[32];
                         tmem_ld32(src + c, v);
                         tmem_ld32(src + c + 32, u);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = glu_act(p.act, v[i], u[i], p.gate_cap, p.up_cap);
+                        gate<MODE == MX4_GLU_SITU>(v, u, p.gate_cap, p.up_cap);
                         uint32_t scale;
                         const uint4 w = quantize_block(v, &scale);
                         if (row < t.row_end) {
@@ -472,7 +514,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 #pragma unroll
                             for (int i = 0; i < 32; ++i) v[i] *= weight;
                         }
-                        if (row < t.row_end) store_row<TO>(dst + c, v, left, vec);
+                        store_block<TO>(dst + c, p.ldo, v, t.row_end - t.row0 - 32 * q, left, vec, lane);
                     }
                 }
             }
@@ -530,8 +572,9 @@ cudaError_t launch_mx4_gemm(const Mx4GemmArgs &g, int32_t *status, cudaStream_t 
     const int64_t tiles = ((g.M + BM - 1) / BM + (g.offsets ? g.E : 0)) * ntn;     // at most
     const int sms = tc_num_sms() > 0 ? tc_num_sms() : 148;
     const int grid = (int)(tiles < sms ? tiles : sms);
-    p.out_scales = g.out_scales; p.row_w = g.row_w; p.act = g.act; p.gate_cap = g.gate_cap; p.up_cap = g.up_cap;
+    p.out_scales = g.out_scales; p.row_w = g.row_w; p.gate_cap = g.gate_cap; p.up_cap = g.up_cap;
     if (g.mode == MX4_GLU) return launch<bf16, MX4_GLU>(a, w, p, grid, s);
+    if (g.mode == MX4_GLU_SITU) return launch<bf16, MX4_GLU_SITU>(a, w, p, grid, s);
     if (g.mode == MX4_WEIGHTED) return launch<bf16, MX4_WEIGHTED>(a, w, p, grid, s);
     return g.out_bf16 ? launch<bf16, MX4_STORE>(a, w, p, grid, s) : launch<float, MX4_STORE>(a, w, p, grid, s);
 }
