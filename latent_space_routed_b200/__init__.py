@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from typing import Dict, NamedTuple, Optional
 
@@ -109,9 +110,12 @@ def _check(status: int):
         raise LmoeError(status, _lib.lmoe_last_error().decode())
 
 
+_cuda_available = functools.lru_cache(maxsize=None)(torch.cuda.is_available)
+
+
 def _stream(stream) -> Optional[int]:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+    if stream is None:      # (the raw handle: a Stream object costs microseconds per call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if _cuda_available() else None
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
