@@ -453,19 +453,15 @@ template <bool PACKED>
 __device__ __forceinline__ void mx4_kblock(float (&acc)[2][4], uint32_t tile, uint32_t arow, uint32_t plane,
                                            uint32_t scales, int gid, int c4, int nb)
 {
-    uint2 e[2][2];                                   // a row's eight scales; two move out per round
-#pragma unroll
-    for (int g = 0; g < 2; ++g)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) e[g][h] = lds64(scales + (uint32_t)(512 * g + 256 * h));
 #pragma unroll 1
     for (int j0 = 0; j0 < nb; j0 += 2) {             // nb is even: K is a multiple of 64
-        uint32_t w[2][2][2];                         // block, group, row gid + 8 h
+        uint32_t w[2][2][2], e[2][2];                // block, group, row gid + 8 h; scales of both blocks
         uint4 x[2], y[2];
 #pragma unroll
         for (int g = 0; g < 2; ++g)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+                e[g][h] = lds16(scales + (uint32_t)(512 * g + 256 * h + j0));
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
                     w[j][g][h] = lds32(tile + (uint32_t)(KBLK_BYTES * g + 1024 * h + (((j0 + j) ^ gid) << 4) + 4 * c4));
@@ -494,19 +490,12 @@ __device__ __forceinline__ void mx4_kblock(float (&acc)[2][4], uint32_t tile, ui
         for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-                const float fa = __uint_as_float(e[g][0].x << (23 - 8 * j) & 0x7f800000u);
-                const float fb = __uint_as_float(e[g][1].x << (23 - 8 * j) & 0x7f800000u);
+                const float fa = __uint_as_float(e[g][0] << (23 - 8 * j) & 0x7f800000u);
+                const float fb = __uint_as_float(e[g][1] << (23 - 8 * j) & 0x7f800000u);
                 acc[g][0] = fmaf(t[j][g][0], fa, acc[g][0]);
                 acc[g][1] = fmaf(t[j][g][1], fa, acc[g][1]);
                 acc[g][2] = fmaf(t[j][g][2], fb, acc[g][2]);
                 acc[g][3] = fmaf(t[j][g][3], fb, acc[g][3]);
-            }
-#pragma unroll
-        for (int g = 0; g < 2; ++g)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                e[g][h].x = __funnelshift_r(e[g][h].x, e[g][h].y, 16);
-                e[g][h].y >>= 16;
             }
     }
 }
