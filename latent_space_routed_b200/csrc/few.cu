@@ -66,8 +66,8 @@ namespace lmoe {
 namespace {
 using namespace ptx;
 
-constexpr int CONSUMERS = 8, LOADERS = 4;
-constexpr int THREADS = 32 * (CONSUMERS + 2 + LOADERS + 1);
+constexpr int CONSUMERS = 8, LOADERS = 3, FINISHERS = 2;
+constexpr int THREADS = 32 * (CONSUMERS + 2 + LOADERS + 1 + FINISHERS);
 constexpr int LT = 32 * LOADERS;
 constexpr int STAGE_BYTES = 16384, KBLK_BYTES = 2048;   // a k-block of 16 rows
 constexpr int SCALE_BYTES = 1024;                // 2 x 16 rows of 32 scales (1024 values)
@@ -325,16 +325,17 @@ struct Select {
 __host__ __device__ constexpr int select_bytes(int E128) { return 12 * E128 + 64 * 8 + 64 * 2; }
 
 struct Shared {
-    uint32_t ring, scales, act, full, empty, act_full, act_empty, cons, team, load, red_free;   // shared-memory addresses
-    float *red;              // [RED_FLOATS]
+    uint32_t ring, scales, act, full, empty, act_full, act_empty, cons, load, cells, free;   // shared-memory addresses
+    float *red;              // [2 buffers][2 teams][4 warps][RED_WARP]
+    float *sums;             // [SUM_BYTES / 4]
     Touched *tab;
     Select select;
     Item *queue;
     float *inv;              // [2 slots][8]: inverse of the activations' scale
     float *lred;             // loaders' sums [4]
     // [0] abort, [1] items published, [3] sets of x issued, [25] touched experts, [26, 28) stages issued to each
-    // team; items passed: [16, 20) by each loader, [20] by the producer, [21] by the signaller; [32, 40) items
-    // finished by each consumer warp
+    // team; items passed: [16, 19) by each loader, [19] by the producer, [20] by the signaller; [32, 42) items
+    // finished by each consumer and finisher warp
     int *flags;
 };
 
@@ -430,16 +431,17 @@ __device__ __forceinline__ int chunks(const Item &it)
 // ------------------------------------------------------------------ consumers
 // Partial products of an item: per warp two groups of 16 rows x 8 columns, the groups
 // RED_GROUP floats apart (16 more than a group, so that both are read without conflicts).
-constexpr int RED_GROUP = 144, RED_WARP = 2 * RED_GROUP, RED_FLOATS = CONSUMERS * RED_WARP;
-// Sum over n warps of one cell; `packed`: the lo terms' sums are four columns further.
-__device__ __forceinline__ float red_sum(const float *cell, int n, bool packed)
+constexpr int RED_GROUP = 144, RED_WARP = 2 * RED_GROUP, RED_FLOATS = 2 * CONSUMERS * RED_WARP;
+constexpr int SUM_BYTES = 2048;          // sums of the router's and the combine items' warps
+// Sum over a team's warps of one cell; `packed`: the lo terms' sums are four columns further.
+__device__ __forceinline__ float red_sum(const float *cell, bool packed)
 {
     float v = 0.f;
-#pragma unroll 4
-    for (int w = 0; w < n; ++w) v += cell[w * RED_WARP];
+#pragma unroll
+    for (int w = 0; w < CONSUMERS / 2; ++w) v += cell[w * RED_WARP];
     if (packed)
-#pragma unroll 4
-        for (int w = 0; w < n; ++w) v += cell[w * RED_WARP + 4];
+#pragma unroll
+        for (int w = 0; w < CONSUMERS / 2; ++w) v += cell[w * RED_WARP + 4];
     return v;
 }
 
@@ -498,6 +500,15 @@ __device__ __forceinline__ void mx4_kblock(float (&acc)[2][4], uint32_t tile, ui
                 acc[g][3] = fmaf(t[j][g][3], fb, acc[g][3]);
             }
     }
+}
+
+// The largest magnitude of a warp's eight rows of one column (four columns side by side), into *word.
+__device__ __forceinline__ void largest_of_rows(unsigned *word, float v, bool real, int lane)
+{
+    float m = real ? fabsf(v) : 0.f;
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    if (lane < 4 && real) atomicMax(word, __float_as_uint(m));
 }
 
 // Wait until item q is in the queue.
@@ -755,6 +766,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
     sh.scales = base + o; o += p.scales ? (uint32_t)p.stages * SCALE_BYTES : 0u;
     sh.act = base + o; o += 2u * (uint32_t)p.slot_bytes;
     sh.red = reinterpret_cast<float *>(g + o); o += 4 * RED_FLOATS;
+    sh.sums = reinterpret_cast<float *>(g + o); o += SUM_BYTES;
     const int E128 = (p.E + 127) & ~127, TK = p.T * p.k, TK8 = (TK + 7) & ~7;
     sh.select.mask = reinterpret_cast<uint32_t *>(g + o); o += 4 * E128;
     sh.select.weight = reinterpret_cast<float *>(g + o); o += 4 * TK8;
@@ -762,7 +774,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
     sh.tab = sh.select.tab = reinterpret_cast<Touched *>(g + o); o += (uint32_t)sizeof(Touched) * (TK8 < E128 ? TK8 : E128);
     o = (o + 15u) & ~15u;
     sh.queue = reinterpret_cast<Item *>(g + o); o += sizeof(Item) * QUEUE;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(g + o); o += 8 * (2 * MAX_STAGES + 12);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(g + o); o += 8 * (2 * MAX_STAGES + 14);
     sh.inv = reinterpret_cast<float *>(g + o); o += 64;
     sh.lred = reinterpret_cast<float *>(g + o); o += 64;
     sh.flags = reinterpret_cast<int *>(g + o);
@@ -772,8 +784,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
     sh.act_empty = sh.act_full + 16u;
     sh.cons = sh.act_empty + 16u;
     sh.load = sh.cons + 8u;
-    sh.team = sh.load + 8u;
-    sh.red_free = sh.team + 16u;
+    sh.cells = sh.load + 8u;         // [team][buffer]: partial sums written
+    sh.free = sh.cells + 32u;        // [team][buffer]: and read
     volatile int *abort = sh.flags;
     volatile int *published = sh.flags + 1, *passed = sh.flags + 16;
 
@@ -793,9 +805,9 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
         }
         mbar_init(sh.cons, CONSUMERS);
         mbar_init(sh.load, LOADERS);
-        for (int t = 0; t < 2; ++t) {
-            mbar_init(sh.team + 8u * t, CONSUMERS / 2);
-            mbar_init(sh.red_free + 8u * t, CONSUMERS / 2);
+        for (int t = 0; t < 4; ++t) {
+            mbar_init(sh.cells + 8u * t, CONSUMERS / 2);
+            mbar_init(sh.free + 8u * t, FINISHERS);
         }
         for (int i = 0; i < 48; ++i) sh.flags[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -916,7 +928,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 behind(passed + LOADERS, AHEAD);
                 if ((q & 7) == 0) {
                     for (int r = 0; r < LOADERS + 2; ++r) behind(passed + r, QUEUE - 8);
-                    for (int r = 0; r < CONSUMERS; ++r) behind(finished + r, QUEUE - 8);
+                    for (int r = 0; r < CONSUMERS + FINISHERS; ++r) behind(finished + r, QUEUE - 8);
                 }
                 if (good) {
                     sh.queue[q % QUEUE] = it;
@@ -1095,9 +1107,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
         const int team = warp >> 2, sub = warp & 3;
         const int gid = lane >> 2, c4 = lane & 3;
         RoleBarrier bar = {sh.cons, 0u, abort, true};                     // all eight warps
-        RoleBarrier tbar = {sh.team + 8u * team, 0u, abort, true};        // the team's four
         int s = team ? half : 0;                         // slot and phase of this team's next stage
-        uint32_t ph = 0, red_ph = 1;
+        uint32_t ph = 0, cell_n = 0;                     // sub-items of this team so far
         int set = -1, cur_key = -1, cur_seg = -1;
         bool ok = true;
         auto full = [&]() -> bool { return warp_wait(sh.full + 8u * s, ph, abort); };
@@ -1128,7 +1139,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                     good = wait_count(p.ctl, C_YS, (unsigned)(sh.flags[25] * p.n.rd_n), abort);
                     if (good && p.standard) good = wait_count(p.ctl, C_PART, 2u * p.n.sd_n, abort);
                 }
-                ok = __shfl_sync(0xffffffffu, good, 0) != 0 && bar.sync() && combine_item<WT>(p, it, sh.red, bar, warp, lane);
+                ok = __shfl_sync(0xffffffffu, good, 0) != 0 && bar.sync() && combine_item<WT>(p, it, sh.sums, bar, warp, lane);
                 if (!ok) break;
                 done();
                 continue;
@@ -1186,18 +1197,17 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 }
                 return true;
             };
-            float *const myred = sh.red + warp * RED_WARP;
-            auto red_writable = [&]() -> bool {          // the last sums in this warp's cells have been read
-                const bool good = warp_wait(sh.red_free + 8u * team, red_ph, abort);
-                red_ph ^= 1u;
-                return good;
+            // The cells for this sub-item's partial sums, once their last use has been read, and their hand-over
+            // to the finishers: two buffers a team, so that the next products do not wait for the epilogue.
+            float *myred = nullptr;
+            auto cells_free = [&]() -> bool {
+                myred = sh.red + (8 * (cell_n & 1u) + warp) * RED_WARP;
+                return warp_wait(sh.free + 16u * team + 8u * (cell_n & 1u), (cell_n >> 1 & 1u) ^ 1u, abort);
             };
-            auto red_read = [&]() {                      // this warp has read its sums
+            auto cells_written = [&]() {
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(sh.red_free + 8u * team);
-                    if (split) mbar_arrive(sh.red_free + 8u * (team ^ 1));
-                }
+                if (lane == 0) mbar_arrive(sh.cells + 16u * team + 8u * (cell_n & 1u));
+                ++cell_n;
             };
 
             if (kind == ROUTER) {
@@ -1248,8 +1258,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                     }
                     release();
                 });
-                if (!ok || !(ok = red_writable())) break;
-                double *rd = reinterpret_cast<double *>(sh.red);      // [8 warps][4 rows][8 tokens]
+                if (!ok) break;
+                double *rd = reinterpret_cast<double *>(sh.sums);     // [8 warps][4 rows][8 tokens]
 #pragma unroll
                 for (int t = 0; t < FEW_MAX_T; ++t)
                     if (t < p.T) {
@@ -1266,7 +1276,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                         p.r64[(int64_t)t * p.E + e] = 1.0 / (1.0 + exp(-v));
                     }
                 }
-                if (team == 0) red_read();
+                if (!(ok = bar.sync())) break;                // the sums' memory is free again
                 done();
                 continue;
             }
@@ -1311,7 +1321,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 });
                 if (!ok) break;
                 if (!mine) continue;
-                if (!(ok = red_writable())) break;
+                if (!(ok = cells_free())) break;
 #pragma unroll
                 for (int t = 0; t < FEW_MAX_T; ++t)
                     if (t < ncol) {
@@ -1422,84 +1432,117 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 }
                 if (!ok) break;
                 if (!mine) continue;
-                if (!(ok = red_writable())) break;
+                if (!(ok = cells_free())) break;
+                // 4-bit experts: the activations' scale comes out here, while their slot is held
+                float back[2] = {1.f, 1.f};
+                if (mx4) {
+                    const float *inv = sh.inv + 8 * (set & 1);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int col = 2 * c4 + i;
+                        back[i] = inv[__shfl_sync(0xffffffffu, tok, packed ? (col & 3) : col)];
+                    }
+                }
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     float2 *r = reinterpret_cast<float2 *>(myred + g * RED_GROUP + gid * 8 + 2 * c4);
-                    r[0] = make_float2(acc[g][0], acc[g][1]);
-                    r[32] = make_float2(acc[g][2], acc[g][3]);
+                    r[0] = make_float2(acc[g][0] * back[0], acc[g][1] * back[1]);
+                    r[32] = make_float2(acc[g][2] * back[0], acc[g][3] * back[1]);
                 }
             }
-
-            // ---- sums over the team's warps (over both teams' where they halved K, by team 0), and
-            // what becomes of them: thread (row, token) of 16 x 8, both groups of rows.  What the
-            // epilogue reads from global memory is asked for before the barrier.
-            const int cell = threadIdx.x & 127, row = cell >> 3, t = cell & 7;
-            const bool real = t < ncol && !(split && team);
-            const int r = out_row(kind, it.j0 + rr) + row;
-            float add = 0.f;
-            int slot = -1;
-            if (kind == UP) {
-                if (real) {
-                    const float *q2 = p.part + (int64_t)t * p.d + r;
-                    add = __ldcg(q2) + __ldcg(q2 + (int64_t)p.T * p.d);
-                }
-            } else if (kind == ROUTED_DOWN) {
-                if (real) {
-                    slot = sh.tab[it.ti].slot[t];
-                    add = sh.select.weight[slot];
-                }
-            } else if (kind == ROUTED_GU) {
-                if (real) slot = sh.tab[it.ti].slot[t];
-            }
-            const float back = mx4 && real ? sh.inv[8 * (set & 1) + tok] : 1.f;
-            if (!(ok = split ? bar.sync() : tbar.sync())) break;
-            if (split && team) break;                      // (its one sub-item)
-            const float *cells = sh.red + (split ? 0 : 4 * team) * RED_WARP + cell;
-            const int nw = split ? CONSUMERS : CONSUMERS / 2;
-            const float v0 = red_sum(cells, nw, packed && t < 4) * back;
-            const float v1 = red_sum(cells + RED_GROUP, nw, packed && t < 4) * back;
-            red_read();
-            if (kind == SHARED_GU || kind == ROUTED_GU) {
-                const float h = glu_act(p.act, v0, v1, p.gate_cap, p.up_cap);
-                if (kind == SHARED_GU) {
-                    if (real) p.hs[(int64_t)t * 2 * p.fs + r] = h;
-                } else {
-                    if (slot >= 0) p.H[(int64_t)slot * p.f + r] = h;
-                    if (WT == W_MX4) {      // rows of a warp: lane bits 3, 4
-                        float m = slot >= 0 ? fabsf(h) : 0.f;
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                        if (lane < 8 && slot >= 0) atomicMax(p.ctl + C_AMAX_H + slot, __float_as_uint(m));
-                    }
-                }
-            } else if (kind == DOWN) {
-                const float z = v0 + v1;
-                if (real) p.z[(int64_t)t * p.l + r] = z;
-                if (WT == W_MX4) {
-                    float m = real ? fabsf(z) : 0.f;
-                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                    if (lane < 8 && real) atomicMax(p.ctl + C_AMAX_Z + t, __float_as_uint(m));
-                }
-            } else if (kind == UP) {
-                if (real) store_token<WT>(p.y, (int64_t)t * p.d + r, v0 + v1 + add);
-            } else if (kind == SHARED_DOWN) {
-                if (real) {
-                    float *q2 = p.part + ((int64_t)it.ti * p.T + t) * p.d + r;
-                    q2[0] = v0;
-                    q2[16] = v1;
-                }
-            } else if (real) {
-                float *q2 = p.ysl + (int64_t)slot * p.l + r;
-                q2[0] = add * v0;
-                q2[16] = add * v1;
-            }
+            cells_written();
             }
             if (!ok) break;
             done();
         }
         if (!ok && lane == 0) give_up(0x8);
+    } else if (warp >= THREADS / 32 - FINISHERS) {
+        // ------------------------------------------------------------ finishers
+        // Sums over the team's warps (over both teams' where they halved K) and what becomes of them:
+        // thread (row, column) of 16 x 4, both groups of rows, the other four columns after them
+        const int fw = warp - (THREADS / 32 - FINISHERS), row = 8 * fw + (lane >> 2);
+        uint32_t n0 = 0, n1 = 0;                          // sub-items of each team so far
+        bool ok = true;
+        for (int q = 0; ok; ++q) {
+            if (!(ok = __all_sync(0xffffffffu, wait_published(published, q, abort)))) break;
+            const Item it = sh.queue[q % QUEUE];
+            const int kind = it.kind;
+            if (kind == END) break;
+            const bool cells = kind != ROUTER && !weightless(kind);
+            const bool split = (p.n.split >> kind & 1u) != 0u;
+            const bool routed = kind == ROUTED_GU || kind == ROUTED_DOWN;
+            const int ncol = kind == ROUTED_GU ? __popc((unsigned)sh.tab[it.ti].mask) : it.ncol;
+            const bool packed = cells && ncol <= 4 && act_plan<WT>(p, it).planes == 2;
+            for (int rr = 0; cells && rr < it.reps; ++rr) {
+                const int team = split ? 0 : rr & 1;
+                const uint32_t n = team ? n1 : n0;
+                const int r = out_row(kind, it.j0 + rr) + row;
+                const float *cell0 = sh.red + (8 * (n & 1u) + 4 * team) * RED_WARP + row * 8 + (lane & 3);
+                const float *cell1 = sh.red + (8 * (n1 & 1u) + 4) * RED_WARP + row * 8 + (lane & 3);   // (split)
+#pragma unroll 1
+                for (int t0 = 0; t0 < ncol; t0 += 4) {
+                    const int t = t0 + (lane & 3);
+                    const bool real = t < ncol;
+                    if (t0 == 0) {
+                        ok = warp_wait(sh.cells + 16u * team + 8u * (n & 1u), n >> 1 & 1u, abort);
+                        if (ok && split) ok = warp_wait(sh.cells + 16u + 8u * (n1 & 1u), n1 >> 1 & 1u, abort);
+                        if (!ok) break;
+                    }
+                    float add = 0.f;
+                    int slot = -1;
+                    if (kind == UP) {        // (complete only now: the products' activations waited for the shared experts)
+                        if (real) {
+                            const float *q2 = p.part + (int64_t)t * p.d + r;
+                            add = __ldcg(q2) + __ldcg(q2 + (int64_t)p.T * p.d);
+                        }
+                    } else if (routed && real) {
+                        slot = sh.tab[it.ti].slot[t];
+                        if (kind == ROUTED_DOWN) add = sh.select.weight[slot];
+                    }
+                    float v0 = red_sum(cell0 + t0, packed), v1 = red_sum(cell0 + t0 + RED_GROUP, packed);
+                    if (split) {
+                        v0 += red_sum(cell1 + t0, packed);
+                        v1 += red_sum(cell1 + t0 + RED_GROUP, packed);
+                    }
+                    if (kind == SHARED_GU || kind == ROUTED_GU) {
+                        const float h = glu_act(p.act, v0, v1, p.gate_cap, p.up_cap);
+                        if (kind == SHARED_GU) {
+                            if (real) p.hs[(int64_t)t * 2 * p.fs + r] = h;
+                        } else {
+                            if (real) p.H[(int64_t)slot * p.f + r] = h;
+                            if (WT == W_MX4) largest_of_rows(p.ctl + C_AMAX_H + slot, h, real, lane);
+                        }
+                    } else if (kind == DOWN) {
+                        const float z = v0 + v1;
+                        if (real) p.z[(int64_t)t * p.l + r] = z;
+                        if (WT == W_MX4) largest_of_rows(p.ctl + C_AMAX_Z + t, z, real, lane);
+                    } else if (kind == UP) {
+                        if (real) store_token<WT>(p.y, (int64_t)t * p.d + r, v0 + v1 + add);
+                    } else if (kind == SHARED_DOWN) {
+                        if (real) {
+                            float *q2 = p.part + ((int64_t)it.ti * p.T + t) * p.d + r;
+                            q2[0] = v0;
+                            q2[16] = v1;
+                        }
+                    } else if (real) {
+                        float *q2 = p.ysl + (int64_t)slot * p.l + r;
+                        q2[0] = add * v0;
+                        q2[16] = add * v1;
+                    }
+                }
+                if (!ok) break;
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(sh.free + 16u * team + 8u * (n & 1u));
+                    if (split) mbar_arrive(sh.free + 16u + 8u * (n1 & 1u));
+                }
+                if (team) ++n1; else ++n0;
+                if (split) ++n1;
+            }
+            __syncwarp();
+            if (ok && lane == 0) sts_release(smem_u32(sh.flags + 32 + CONSUMERS + fw), (unsigned)(q + 1));
+        }
+        if (!ok && lane == 0) give_up(0x40);
     } else {
         // ------------------------------------------------------------ signaller
         if (lane == 0) {
@@ -1511,7 +1554,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 if (kind == END) break;
                 const uint32_t word = smem_u32(sh.flags + 32);
                 const long long t1 = clock64();
-                for (int w = 0; w < CONSUMERS; ++w)
+                for (int w = 0; w < CONSUMERS + FINISHERS; ++w)
                     while ((int)lds_acquire(word + 4 * w) <= q && ok) {
                         __nanosleep(20);
                         if (*abort || clock64() - t1 > 2 * WAIT_LIMIT_CYCLES) ok = false;
@@ -1551,8 +1594,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
 size_t fixed_smem(const lmoe_config &c, int T)
 {
     const int E128 = (c.E + 127) / 128 * 128, TK8 = (T * c.k + 7) / 8 * 8;
-    return 1024 + 4 * RED_FLOATS + 4 * (size_t)E128 + 6 * (size_t)TK8 +
-           sizeof(Touched) * (size_t)std::min(TK8, E128) + 16 + sizeof(Item) * QUEUE + 8 * (2 * MAX_STAGES + 12) +
+    return 1024 + 4 * RED_FLOATS + SUM_BYTES + 4 * (size_t)E128 + 6 * (size_t)TK8 +
+           sizeof(Touched) * (size_t)std::min(TK8, E128) + 16 + sizeof(Item) * QUEUE + 8 * (2 * MAX_STAGES + 14) +
  64 + 64 + 192;
 }
 
