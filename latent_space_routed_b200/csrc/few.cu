@@ -502,13 +502,13 @@ __device__ __forceinline__ void mx4_kblock(float (&acc)[2][4], uint32_t tile, ui
     }
 }
 
-// The largest magnitude of a warp's eight rows of one column (four columns side by side), into *word.
+// The largest magnitude of a warp's 16 rows of one column (two columns side by side), into *word.
 __device__ __forceinline__ void largest_of_rows(unsigned *word, float v, bool real, int lane)
 {
     float m = real ? fabsf(v) : 0.f;
 #pragma unroll
-    for (int off = 4; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    if (lane < 4 && real) atomicMax(word, __float_as_uint(m));
+    for (int off = 2; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    if (lane < 2 && real) atomicMax(word, __float_as_uint(m));
 }
 
 // Wait until item q is in the queue.
@@ -1458,9 +1458,10 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
         if (!ok && lane == 0) give_up(0x8);
     } else if (warp >= THREADS / 32 - FINISHERS) {
         // ------------------------------------------------------------ finishers
-        // Sums over the team's warps (over both teams' where they halved K) and what becomes of them:
-        // thread (row, column) of 16 x 4, both groups of rows, the other four columns after them
-        const int fw = warp - (THREADS / 32 - FINISHERS), row = 8 * fw + (lane >> 2);
+        // A warp for each team: sums over the team's warps (over both teams' by the first where they
+        // halved K) and what becomes of them; lane (row, column) of 16 x 2, both groups of rows, then
+        // the next two columns
+        const int fw = warp - (THREADS / 32 - FINISHERS), row = lane >> 1;
         uint32_t n0 = 0, n1 = 0;                          // sub-items of each team so far
         bool ok = true;
         for (int q = 0; ok; ++q) {
@@ -1475,17 +1476,38 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
             const bool packed = cells && ncol <= 4 && act_plan<WT>(p, it).planes == 2;
             for (int rr = 0; cells && rr < it.reps; ++rr) {
                 const int team = split ? 0 : rr & 1;
-                const uint32_t n = team ? n1 : n0;
+                const uint32_t n = team ? n1 : n0, m1 = n1;
+                if (team) ++n1; else ++n0;
+                if (split) ++n1;
+                // Where the first warp reads both teams' sums it must not be ahead of the second one, nor this one
+                // behind: a wait knows a barrier's phases only modulo two.  So the second warp waits for its team's
+                // sums as well, its arrival counts towards their release, and the first waits for its earlier items.
+                if (split && fw) {
+                    if (!(ok = warp_wait(sh.cells + 16u + 8u * (m1 & 1u), m1 >> 1 & 1u, abort))) break;
+                    if (lane == 0) mbar_arrive(sh.free + 16u + 8u * (m1 & 1u));
+                    continue;
+                }
+                if (split) {
+                    int good = 1;
+                    if (lane == 0) {
+                        const uint32_t other = smem_u32(sh.flags + 32 + CONSUMERS + 1);
+                        const long long t1 = clock64();
+                        while ((int)lds_acquire(other) < q && good)
+                            if (*abort || clock64() - t1 > 2 * WAIT_LIMIT_CYCLES) good = 0;
+                    }
+                    if (!(ok = __shfl_sync(0xffffffffu, good, 0) != 0)) break;
+                }
+                if (team != fw) continue;
                 const int r = out_row(kind, it.j0 + rr) + row;
-                const float *cell0 = sh.red + (8 * (n & 1u) + 4 * team) * RED_WARP + row * 8 + (lane & 3);
-                const float *cell1 = sh.red + (8 * (n1 & 1u) + 4) * RED_WARP + row * 8 + (lane & 3);   // (split)
+                const float *cell0 = sh.red + (8 * (n & 1u) + 4 * team) * RED_WARP + row * 8 + (lane & 1);
+                const float *cell1 = sh.red + (8 * (m1 & 1u) + 4) * RED_WARP + row * 8 + (lane & 1);   // (split)
 #pragma unroll 1
-                for (int t0 = 0; t0 < ncol; t0 += 4) {
-                    const int t = t0 + (lane & 3);
+                for (int t0 = 0; t0 < ncol; t0 += 2) {
+                    const int t = t0 + (lane & 1);
                     const bool real = t < ncol;
                     if (t0 == 0) {
                         ok = warp_wait(sh.cells + 16u * team + 8u * (n & 1u), n >> 1 & 1u, abort);
-                        if (ok && split) ok = warp_wait(sh.cells + 16u + 8u * (n1 & 1u), n1 >> 1 & 1u, abort);
+                        if (ok && split) ok = warp_wait(sh.cells + 16u + 8u * (m1 & 1u), m1 >> 1 & 1u, abort);
                         if (!ok) break;
                     }
                     float add = 0.f;
@@ -1533,11 +1555,9 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 if (!ok) break;
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(sh.free + 16u * team + 8u * (n & 1u));
-                    if (split) mbar_arrive(sh.free + 16u + 8u * (n1 & 1u));
+                    for (int i = 0; i < FINISHERS; ++i) mbar_arrive(sh.free + 16u * team + 8u * (n & 1u));
+                    if (split) mbar_arrive(sh.free + 16u + 8u * (m1 & 1u));
                 }
-                if (team) ++n1; else ++n0;
-                if (split) ++n1;
             }
             __syncwarp();
             if (ok && lane == 0) sts_release(smem_u32(sh.flags + 32 + CONSUMERS + fw), (unsigned)(q + 1));
