@@ -490,6 +490,8 @@ class LatentMoE:
         Calls that may overlap on the GPU, and graphs that may replay beside other
         calls, need a ``workspace`` of their own (``lmoe_few_workspace_size`` bytes)."""
         T = x.shape[0]
+        if x.dim() != 2 or x.shape[1] != self.cfg.d or x.dtype != self.dtype or not x.is_contiguous():
+            raise ValueError(f"x must be a contiguous {self.dtype} tensor [T, {self.cfg.d}]")
         ws = self.few_workspace(T) if workspace is None else workspace
         lmoe_forward_few(self.handle, x, T, out["output"], out["selected_experts"], out["mixture_weights"],
                          out["latent_routed_aggregate"], ws, ws.numel(), stream)

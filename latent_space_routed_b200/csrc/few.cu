@@ -25,24 +25,34 @@
 // producer warps keep the next items' tiles in flight while its other warps
 // still wait for the activations: HBM does not idle between the stages.
 //
-// Roles (15 warps, one block per SM):
-//   warps 0-7   consumers: products from shared memory, sums over the warps, epilogues.  Two
-//               teams of four warps, each with half of the ring.  An item is a run of sub-items (32
-//               rows, or 16); the teams take them in turn, each with its own barrier, so that one
-//               team's sums and epilogue overlap the other's products.  Where K is long (a
-//               sub-item above SPLIT_BYTES), an item is one sub-item and the teams halve its K
+// Roles (16 warps, one block per SM):
+//   warps 0-7   consumers: products from shared memory.  Two teams of four warps, each with half
+//               of the ring.  An item is a run of sub-items (32 rows, or 16); the teams take them in
+//               turn and leave their warps' partial sums in one of two buffers a team.  Where K is
+//               long (a sub-item above SPLIT_BYTES), an item is one sub-item and the teams halve its K
 //   warp 8      producer: one thread keeps a ring of 16 KB stages full, one TMA copy each (measured:
 //               one thread issuing 16 KB boxes streams 7.3 TB/s, as 8 KB boxes 6.4 TB/s).  A box is
 //               four 128-byte k-blocks of two groups of 16 rows (gate and up, or 32 rows), eight
 //               k-blocks of 16 rows, or 32 of 4 rows (router)
-//   warp 9      scheduler: takes tickets and describes their items in a queue, at most two items
+//   warp 9      scheduler: takes tickets and describes their items in a queue, at most three items
 //               ahead of the producer (its integer work per item would stall the copies)
-//   warps 10-13 loaders: bring an item's activations from global memory into one of two
+//   warps 10-12 loaders: bring an item's activations from global memory into one of two
 //               shared-memory slots, in the form that the product wants, one set ahead.  Before the
 //               first routed item they select the experts, a warp per token, in every block: the same
 //               work takes no longer than another block's result would take to arrive
-//   warp 14     signaller: publishes finished items to the other blocks (the fence before the
-//               counter costs 1000 to 2000 cycles, which the consumers would otherwise spend per item)
+//   warp 13     signaller: publishes finished items to the other blocks (the fence before the
+//               counter costs 1000 to 2000 cycles, which others would otherwise spend per item)
+//   warps 14-15 finishers, one a team: sums over the team's warps, gates, weights and stores.  By the
+//               consumers themselves these cost 67 us of 439 with 6 tokens and 4-bit experts
+//
+// What it takes (d 7168, l 1792, f 2048, 384 experts, 32 a token; bytes at the copy rate of 6.46 TB/s):
+//   1 token            158 us, 92 % of the rate
+//   8 tokens           726 us, 96 %
+//   1 token, 4 bits    139 us, 47 %; 6 tokens 372 us, 48 %: the consumers' instructions bound the 4-bit
+//                      stages (products skipped: 112 of then 151 us, 277 of 500).  Eight warps a team
+//                      or deeper unrolling were slower, the instruction buffers being what they compete for
+// and at d 2048, l 512, f 1408, 256 experts, 24 a token, 1 token: 62 us, 36 %: the seven dependent
+// stages have latencies (selection 5 us, the last three stages 13 us) that a stream of 22 us cannot hide.
 //
 // Arithmetic: bf16 weights are the A operand of m16n8k16 (16 weight rows), the tokens its
 // eight columns, fp32 sums.  tcgen05 would need 128 rows per tile and gains nothing here: the

@@ -29,9 +29,8 @@ inline int64_t mx4_scale_pitch(int64_t K) { return (K / 32 + 15) / 16 * 16; }
 
 bool few_make_maps(const lmoe_config &c, const FewWeights &w, FewMaps *m);
 
-// Workspace of one call: bytes, and the offset of its status word.
+// Bytes of one call's workspace, which begins with the status word.
 size_t few_workspace_bytes(const lmoe_config &c, int64_t T);
-constexpr size_t FEW_STATUS_OFFSET = 0;
 
 cudaError_t few_launch(const lmoe_config &c, const FewMaps &m, const FewWeights &w, const float *bias, const void *x, int T,
                        void *y, int32_t *sel, void *p_out, void *u_out, void *workspace, bool stall_test,

@@ -9,7 +9,9 @@
 // Both directions move bytes and little else (6 to 9 bytes per pair of bf16
 // values, 10 to 17 per pair of fp32).  Four lanes share a block: each loads 8
 // values with 16-byte loads and stores one word of codes, so that a warp's loads and
-// stores are whole lines; the block's maximum is two shuffles.
+// stores are whole lines; the block's maximum is two shuffles.  360448 x 512 fp32 values
+// to 4 bits and back (1.67 GB): 275 us, 94 % of the copy rate.  More groups in flight per
+// thread (2, 4) or other grids were no faster.
 #include "mx4.cuh"
 #include "ptx.cuh"
 
@@ -37,7 +39,7 @@ __device__ __forceinline__ void load8(float (&v)[8], const float *p)
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
-__device__ __forceinline__ void store8(bf16 *p, const float (&v)[8])
+__device__ __forceinline__ void store8(bf16 *p, const float (&v)[8], bool)
 {
     uint32_t u[4];
 #pragma unroll
@@ -47,8 +49,16 @@ __device__ __forceinline__ void store8(bf16 *p, const float (&v)[8])
     }
     *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
-__device__ __forceinline__ void store8(float *p, const float (&v)[8])
+// `whole`: 32-byte aligned, one store.  Two 16-byte stores of a lane leave every store of the warp with half
+// sectors (360448 x 512 values to 4 bits and back: 323 us against 275).
+__device__ __forceinline__ void store8(float *p, const float (&v)[8], bool whole)
 {
+    if (whole) {
+        asm volatile("st.global.v8.f32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"f"(v[0]), "f"(v[1]), "f"(v[2]),
+                     "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "l"(p)
+                     : "memory");
+        return;
+    }
     reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
     reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
@@ -95,7 +105,7 @@ __global__ void __launch_bounds__(THREADS) quantize_kernel(const T *__restrict__
 template <typename T, typename Idx>
 __global__ void __launch_bounds__(THREADS) dequantize_kernel(const uint32_t *__restrict__ codes,
                                                              const uint8_t *__restrict__ scales, Idx n, Idx c8,
-                                                             int64_t ld, T *__restrict__ y)
+                                                             int64_t ld, T *__restrict__ y, bool whole)
 {
     const bool dense = ld == (int64_t)c8 * 8;
     const Idx step = (Idx)gridDim.x * THREADS;
@@ -111,7 +121,7 @@ __global__ void __launch_bounds__(THREADS) dequantize_kernel(const uint32_t *__r
             v[2 * j] = __low2float(p) * s;
             v[2 * j + 1] = __high2float(p) * s;
         }
-        store8(y + place<Idx>(i, c8, ld, dense), v);
+        store8(y + place<Idx>(i, c8, ld, dense), v, whole);
     }
 }
 
@@ -169,12 +179,13 @@ cudaError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, i
     const int64_t n = rows * (cols / 8), c8 = cols / 8;
     const unsigned g = grid_for(n);
     const uint32_t *w = (const uint32_t *)codes;
+    const bool whole = (uintptr_t)y % 32 == 0 && (rows == 1 || ld % 8 == 0);
     if (n < IDX32) {
-        if (bf16_out) dequantize_kernel<bf16, uint32_t><<<g, THREADS, 0, s>>>(w, scales, (uint32_t)n, (uint32_t)c8, ld, (bf16 *)y);
-        else dequantize_kernel<float, uint32_t><<<g, THREADS, 0, s>>>(w, scales, (uint32_t)n, (uint32_t)c8, ld, (float *)y);
+        if (bf16_out) dequantize_kernel<bf16, uint32_t><<<g, THREADS, 0, s>>>(w, scales, (uint32_t)n, (uint32_t)c8, ld, (bf16 *)y, whole);
+        else dequantize_kernel<float, uint32_t><<<g, THREADS, 0, s>>>(w, scales, (uint32_t)n, (uint32_t)c8, ld, (float *)y, whole);
     } else {
-        if (bf16_out) dequantize_kernel<bf16, uint64_t><<<g, THREADS, 0, s>>>(w, scales, (uint64_t)n, (uint64_t)c8, ld, (bf16 *)y);
-        else dequantize_kernel<float, uint64_t><<<g, THREADS, 0, s>>>(w, scales, (uint64_t)n, (uint64_t)c8, ld, (float *)y);
+        if (bf16_out) dequantize_kernel<bf16, uint64_t><<<g, THREADS, 0, s>>>(w, scales, (uint64_t)n, (uint64_t)c8, ld, (bf16 *)y, whole);
+        else dequantize_kernel<float, uint64_t><<<g, THREADS, 0, s>>>(w, scales, (uint64_t)n, (uint64_t)c8, ld, (float *)y, whole);
     }
     return cudaGetLastError();
 }

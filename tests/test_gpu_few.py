@@ -122,6 +122,26 @@ def test_zero_and_large_tokens():
             assert ((y - r).abs() <= 2.0 ** -8 * r.abs() + 2.0 ** -9 * top + 1e-30).all(), n
 
 
+@pytest.mark.parametrize("mx4", [False, True])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_a_token_that_is_not_finite_stays_alone(mx4, bad):
+    w, W, layer = make(5, 256, 128, 256, 40, 6, mx4=mx4)
+    x = li.tokens(w).cuda()
+    x[2, 17] = bad
+    out = layer.forward_few(x)
+    lm.lmoe_check_device(layer.handle, 5, layer.few_workspace(5))
+    sel = out["selected_experts"]
+    assert ((sel >= 0) & (sel < 40)).all() and all(len(set(r)) == 6 for r in sel.tolist())
+    rows = [0, 1, 3, 4]
+    assert not torch.isfinite(out["output"][2]).any()
+    for n in ("output", "mixture_weights", "latent_routed_aggregate"):
+        assert torch.isfinite(out[n][rows]).all()
+    ref = oracle.forward(x[rows].cpu(), W, w.k)
+    assert torch.equal(sel[rows].cpu().long(), torch.from_numpy(ref["selected_experts"].astype("int64")))
+    y, r = out["output"][rows].double().cpu(), torch.from_numpy(ref["output"])
+    assert ((y - r).abs() <= 2.0 ** -8 * r.abs() + 2.0 ** -9 * r.abs().amax(1, keepdim=True)).all()
+
+
 def test_streams_graphs_and_two_calls_at_once():
     w, W, layer = make(6, 512, 128, 256, 32, 6)
     xs = [li.tokens(w, seed=i).cuda() for i in range(4)]
@@ -206,6 +226,9 @@ def test_shapes_refusals_and_empty():
     with pytest.raises(lm.LmoeError):
         lm.lmoe_few_workspace_size(h, 9)
     assert lm.lmoe_few_workspace_size(h, 0) == 0
+    for bad in (x.float(), x.t().contiguous().t(), x[:, :128], x[0]):
+        with pytest.raises(ValueError, match="contiguous"):
+            layer.forward_few_into(bad, flat)
     with pytest.raises(TypeError, match="all be Mx4"):
         lm.LatentMoE(layer.cfg, {**{n: v.cuda() for n, v in W.items()}, "G": lm.mx4_quantize(W["G"].cuda())})
 

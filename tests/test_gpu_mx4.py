@@ -81,6 +81,21 @@ def test_quantize_strided_misaligned_and_empty():
         assert q.shape == shape and lm.mx4_dequantize(q).shape == shape
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_dequantize_into_rows_of_any_alignment(dtype):
+    """Row strides and starts of 16 bytes, and of 32, through the C name."""
+    q = lm.mx4_quantize(rand((37, 96), 6).cuda())
+    want = mx4ref.values(*q)
+    per16 = 4 if dtype == "f32" else 8
+    for ld, at in ((96, 0), (96, per16), (96 + per16, 0), (96 + 2 * per16, 2 * per16), (96 + 2 * per16, per16)):
+        y = torch.full((37 * ld + at + 64,), 5.0, dtype=DT[dtype], device="cuda")
+        lm.lmoe_mx4_dequantize(q.codes, q.scales, 37, 96, lm.LMOE_F32 if dtype == "f32" else lm.LMOE_BF16,
+                               y.data_ptr() + at * y.element_size(), ld)
+        rows = y[at:at + 37 * ld].view(37, ld)
+        assert torch.equal(rows[:, :96].double().cpu(), want)
+        assert (rows[:, 96:] == 5.0).all() and (y[:at] == 5.0).all() and (y[at + 37 * ld:] == 5.0).all()
+
+
 def test_quantize_on_another_stream_and_in_a_graph():
     x = rand((65, 128), 4, torch.bfloat16).cuda()
     want = lm.mx4_quantize(x)
