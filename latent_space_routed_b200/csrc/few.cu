@@ -28,8 +28,8 @@
 // Roles (16 warps, one block per SM):
 //   warps 0-7   consumers: products from shared memory.  Two teams of four warps, each with half
 //               of the ring.  An item is a run of sub-items (32 rows, or 16); the teams take them in
-//               turn and leave their warps' partial sums in one of two buffers a team.  Where K is
-//               long (a sub-item above SPLIT_BYTES), an item is one sub-item and the teams halve its K
+//               turn and leave their warps' partial sums in one of two buffers a team.  (Router
+//               items are one sub-item, whose K the teams halve.)
 //   warp 8      producer: one thread keeps a ring of 16 KB stages full, one TMA copy each (measured:
 //               one thread issuing 16 KB boxes streams 7.3 TB/s, as 8 KB boxes 6.4 TB/s).  A box is
 //               four 128-byte k-blocks of two groups of 16 rows (gate and up, or 32 rows), eight
@@ -82,7 +82,7 @@ constexpr int LT = 32 * LOADERS;
 constexpr int STAGE_BYTES = 16384, KBLK_BYTES = 2048;   // a k-block of 16 rows
 constexpr int SCALE_BYTES = 1024;                // 2 x 16 rows of 32 scales (1024 values)
 constexpr int MAX_STAGES = 12, QUEUE = 32, AHEAD = 3;
-constexpr int SPLIT_BYTES = 160 * 1024, ITEM_BYTES = 256 * 1024, MAX_REPS = 8;
+constexpr int ITEM_BYTES = 512 * 1024, MAX_REPS = 8;
 constexpr int SMEM_MAX = 232448;
 
 enum Kind { ROUTER, DOWN, SHARED_GU, ROUTED_GU, SHARED_DOWN, ROUTED_DOWN, COMBINE, UP, END, SELECT };
@@ -110,7 +110,6 @@ struct Touched {
 struct Plan {
     int router_n, down_r, down_n, sgu_r, sgu_n, rgu_r, rgu_n, sd_r, sd_n, rd_r, rd_n, up_r, up_n, combine_n;
     float rgu_inv, rd_inv;       // 1 / rgu_n, 1 / rd_n
-    uint32_t split;              // bit of a kind: the teams halve K
 };
 
 struct FewParams {
@@ -817,7 +816,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
         mbar_init(sh.load, LOADERS);
         for (int t = 0; t < 4; ++t) {
             mbar_init(sh.cells + 8u * t, CONSUMERS / 2);
-            mbar_init(sh.free + 8u * t, FINISHERS);
+            mbar_init(sh.free + 8u * t, 1);
         }
         for (int i = 0; i < 48; ++i) sh.flags[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -843,7 +842,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 if (it.kind == END) break;
                 if (weightless(it.kind)) continue;
                 const int nc = chunks(it), kb = 1 << stage_kb_log2(it.kind);
-                const bool two = two_groups(it.kind), split = (p.n.split >> it.kind & 1u) != 0u;
+                const bool two = two_groups(it.kind), split = it.kind == ROUTER;
                 const bool mx4 = WT == W_MX4 && (it.kind == ROUTED_GU || it.kind == ROUTED_DOWN);
                 const uint32_t bytes = STAGE_BYTES + (mx4 ? SCALE_BYTES : 0);
                 const CUtensorMap *map = it.kind == ROUTER        ? &maps.router
@@ -1156,7 +1155,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
             }
 
             const ActPlan a = act_plan<WT>(p, it);
-            const bool two = two_groups(kind), split = (p.n.split >> it.kind & 1u) != 0u;
+            const bool two = two_groups(kind), split = kind == ROUTER;
             const int nc = chunks(it), nkb = it.nkb;
             const uint32_t plane = (uint32_t)(it.ncol * a.stride);
             // Columns of the product: the slot's rows, but of the routed gate/up (whose slot holds
@@ -1292,7 +1291,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
             }
 
             for (int r0 = 0; ok && r0 < it.reps; r0 += 2) {
-            const int rr = split ? 0 : r0 + team;          // this team's sub-item
+            const int rr = r0 + team;                      // this team's sub-item
             const bool mine = rr < it.reps;
             if (WT == W_F32) {
                 // ---- fp32: lane (4-value piece, rows rq + 4 i); two tiles, of one k-block or of two
@@ -1468,11 +1467,10 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
         if (!ok && lane == 0) give_up(0x8);
     } else if (warp >= THREADS / 32 - FINISHERS) {
         // ------------------------------------------------------------ finishers
-        // A warp for each team: sums over the team's warps (over both teams' by the first where they
-        // halved K) and what becomes of them; lane (row, column) of 16 x 2, both groups of rows, then
-        // the next two columns
+        // A warp for each team: sums over the team's warps and what becomes of them; lane (row, column)
+        // of 16 x 2, both groups of rows, then the next two columns
         const int fw = warp - (THREADS / 32 - FINISHERS), row = lane >> 1;
-        uint32_t n0 = 0, n1 = 0;                          // sub-items of each team so far
+        uint32_t n = 0;                                   // sub-items of the team so far
         bool ok = true;
         for (int q = 0; ok; ++q) {
             if (!(ok = __all_sync(0xffffffffu, wait_published(published, q, abort)))) break;
@@ -1480,44 +1478,18 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
             const int kind = it.kind;
             if (kind == END) break;
             const bool cells = kind != ROUTER && !weightless(kind);
-            const bool split = (p.n.split >> kind & 1u) != 0u;
             const bool routed = kind == ROUTED_GU || kind == ROUTED_DOWN;
             const int ncol = kind == ROUTED_GU ? __popc((unsigned)sh.tab[it.ti].mask) : it.ncol;
             const bool packed = cells && ncol <= 4 && act_plan<WT>(p, it).planes == 2;
-            for (int rr = 0; cells && rr < it.reps; ++rr) {
-                const int team = split ? 0 : rr & 1;
-                const uint32_t n = team ? n1 : n0, m1 = n1;
-                if (team) ++n1; else ++n0;
-                if (split) ++n1;
-                // Where the first warp reads both teams' sums it must not be ahead of the second one, nor this one
-                // behind: a wait knows a barrier's phases only modulo two.  So the second warp waits for its team's
-                // sums as well, its arrival counts towards their release, and the first waits for its earlier items.
-                if (split && fw) {
-                    if (!(ok = warp_wait(sh.cells + 16u + 8u * (m1 & 1u), m1 >> 1 & 1u, abort))) break;
-                    if (lane == 0) mbar_arrive(sh.free + 16u + 8u * (m1 & 1u));
-                    continue;
-                }
-                if (split) {
-                    int good = 1;
-                    if (lane == 0) {
-                        const uint32_t other = smem_u32(sh.flags + 32 + CONSUMERS + 1);
-                        const long long t1 = clock64();
-                        while ((int)lds_acquire(other) < q && good)
-                            if (*abort || clock64() - t1 > 2 * WAIT_LIMIT_CYCLES) good = 0;
-                    }
-                    if (!(ok = __shfl_sync(0xffffffffu, good, 0) != 0)) break;
-                }
-                if (team != fw) continue;
+            for (int rr = fw; cells && rr < it.reps; rr += 2, ++n) {
                 const int r = out_row(kind, it.j0 + rr) + row;
-                const float *cell0 = sh.red + (8 * (n & 1u) + 4 * team) * RED_WARP + row * 8 + (lane & 1);
-                const float *cell1 = sh.red + (8 * (m1 & 1u) + 4) * RED_WARP + row * 8 + (lane & 1);   // (split)
+                const float *cell = sh.red + (8 * (n & 1u) + 4 * fw) * RED_WARP + row * 8 + (lane & 1);
 #pragma unroll 1
                 for (int t0 = 0; t0 < ncol; t0 += 2) {
                     const int t = t0 + (lane & 1);
                     const bool real = t < ncol;
                     if (t0 == 0) {
-                        ok = warp_wait(sh.cells + 16u * team + 8u * (n & 1u), n >> 1 & 1u, abort);
-                        if (ok && split) ok = warp_wait(sh.cells + 16u + 8u * (m1 & 1u), m1 >> 1 & 1u, abort);
+                        ok = warp_wait(sh.cells + 16u * fw + 8u * (n & 1u), n >> 1 & 1u, abort);
                         if (!ok) break;
                     }
                     float add = 0.f;
@@ -1531,11 +1503,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                         slot = sh.tab[it.ti].slot[t];
                         if (kind == ROUTED_DOWN) add = sh.select.weight[slot];
                     }
-                    float v0 = red_sum(cell0 + t0, packed), v1 = red_sum(cell0 + t0 + RED_GROUP, packed);
-                    if (split) {
-                        v0 += red_sum(cell1 + t0, packed);
-                        v1 += red_sum(cell1 + t0 + RED_GROUP, packed);
-                    }
+                    const float v0 = red_sum(cell + t0, packed), v1 = red_sum(cell + t0 + RED_GROUP, packed);
                     if (kind == SHARED_GU || kind == ROUTED_GU) {
                         const float h = glu_act(p.act, v0, v1, p.gate_cap, p.up_cap);
                         if (kind == SHARED_GU) {
@@ -1564,10 +1532,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 }
                 if (!ok) break;
                 __syncwarp();
-                if (lane == 0) {
-                    for (int i = 0; i < FINISHERS; ++i) mbar_arrive(sh.free + 16u * team + 8u * (n & 1u));
-                    if (split) mbar_arrive(sh.free + 16u + 8u * (m1 & 1u));
-                }
+                if (lane == 0) mbar_arrive(sh.free + 16u * fw + 8u * (n & 1u));
             }
             __syncwarp();
             if (ok && lane == 0) sts_release(smem_u32(sh.flags + 32 + CONSUMERS + fw), (unsigned)(q + 1));
@@ -1668,10 +1633,9 @@ cudaError_t launch(const FewMaps &m, const FewParams &p, size_t smem, cudaStream
 
 namespace {
 // Sub-items per item: pairs (one for each team) until an item has ITEM_BYTES, but leaving every block
-// about eight items of the phase; 1 where the teams halve K.
+// about eight items of the phase.
 int reps_for(int64_t sub_bytes, int64_t subs, int blocks)
 {
-    if (sub_bytes > SPLIT_BYTES) return 1;
     const int64_t most = std::min<int64_t>(MAX_REPS, ITEM_BYTES / sub_bytes) / 2 * 2;
     return (int)std::max<int64_t>(2, std::min<int64_t>(most, subs / (8 * (int64_t)blocks) / 2 * 2));
 }
@@ -1704,8 +1668,6 @@ Plan make_plan(const lmoe_config &c, bool mx4, int T, int blocks)
     n.up_n = c.standard ? 0 : items(c.d / 16, n.up_r);
     n.rgu_inv = 1.0f / (float)n.rgu_n;
     n.rd_inv = 1.0f / (float)n.rd_n;
-    const int64_t sub[] = {SPLIT_BYTES + 1, down, sgu, rgu, sd, rd, 0, up};     // by kind
-    for (int k = ROUTER; k <= UP; ++k) n.split |= (uint32_t)(sub[k] > SPLIT_BYTES) << k;
     return n;
 }
 }  // namespace
