@@ -46,12 +46,12 @@
 //               consumers themselves these cost 67 us of 439 with 6 tokens and 4-bit experts
 //
 // What it takes (d 7168, l 1792, f 2048, 384 experts, 32 a token; bytes at the copy rate of 6.46 TB/s):
-//   1 token            158 us, 92 % of the rate
-//   8 tokens           726 us, 96 %
-//   1 token, 4 bits    139 us, 47 %; 6 tokens 372 us, 48 %: the consumers' instructions bound the 4-bit
-//                      stages (products skipped: 112 of then 151 us, 277 of 500).  Eight warps a team
-//                      or deeper unrolling were slower, the instruction buffers being what they compete for
-// and at d 2048, l 512, f 1408, 256 experts, 24 a token, 1 token: 62 us, 36 %: the seven dependent
+//   1 token            156 us, 93 % of the rate
+//   8 tokens           711 us, 98 %
+//   1 token, 4 bits    128 us, 51 %; 6 tokens 351 us, 51 %: the consumers' instructions bound the 4-bit
+//                      stages (with the products skipped, 277 us were left of 500 at the time).  Eight warps
+//                      a team or deeper unrolling were slower: warps compete for the instruction buffers
+// and at d 2048, l 512, f 1408, 256 experts, 24 a token, 1 token: 56 us, 40 %: the seven dependent
 // stages have latencies (selection 5 us, the last three stages 13 us) that a stream of 22 us cannot hide.
 //
 // Arithmetic: bf16 weights are the A operand of m16n8k16 (16 weight rows), the tokens its
@@ -1632,12 +1632,15 @@ cudaError_t launch(const FewMaps &m, const FewParams &p, size_t smem, cudaStream
 }  // namespace
 
 namespace {
-// Sub-items per item: pairs (one for each team) until an item has ITEM_BYTES, but leaving every block
-// about eight items of the phase.
+// Sub-items per item: pairs (one for each team) until an item has ITEM_BYTES, but leaving every block about
+// eight items of the phase, or two where sub-items are below 64 KB: there the costs per item (its activations,
+// its signal) weigh more than the blocks' uneven ends.  Eight against two: 1 token at d 2048 60 against 56 us, 6
+// tokens with 4-bit experts at d 7168 365 against 351; above 64 KB four against eight: 159 against 156 us.
 int reps_for(int64_t sub_bytes, int64_t subs, int blocks)
 {
     const int64_t most = std::min<int64_t>(MAX_REPS, ITEM_BYTES / sub_bytes) / 2 * 2;
-    return (int)std::max<int64_t>(2, std::min<int64_t>(most, subs / (8 * (int64_t)blocks) / 2 * 2));
+    const int64_t items = sub_bytes < 64 * 1024 ? 2 : 8;
+    return (int)std::max<int64_t>(2, std::min<int64_t>(most, subs / (items * blocks) / 2 * 2));
 }
 
 Plan make_plan(const lmoe_config &c, bool mx4, int T, int blocks)
