@@ -53,6 +53,8 @@ CASES = [
     dict(T=8, d=7168, l=1792, f=128, E=8, k=3), dict(T=1, d=7168, l=64, f=128, E=8, k=3),       # segments, halved K
     dict(T=7, d=4096, l=4096, f=256, E=6, k=2, fs=2688),                                        # long rows everywhere
     dict(T=1, d=2048, l=512, f=1408, E=64, k=24, fs=1408),
+    dict(T=8, d=7168, l=64, f=128, E=1024, k=64),                                               # the most of everything
+    dict(T=8, d=256, l=128, f=8192, E=8, k=8, fs=8192),                                         # hidden rows in segments
 ]
 
 

@@ -345,6 +345,28 @@ def test_layer_host_and_noalloc_forms():
         assert torch.equal(host[n], want[n].cpu()) and torch.equal(out[n], want[n])
 
 
+def test_layer_in_a_graph_and_launch_count():
+    from torch.profiler import ProfilerActivity, profile
+    w = li.custom("mx4", 48, 256, 128, 256, 16, 4, 128, seed=5)
+    layer, _, _ = mx4_layer(w)
+    xs = [li.tokens(w, seed=i).cuda() for i in range(2)]
+    want = [layer(x) for x in xs]
+    x, out = xs[0].clone(), layer.empty_outputs(48)
+    layer.forward_into(x, out)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        layer.forward_into(x, out)
+    x.copy_(xs[1])
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(out[n], want[1][n]) for n in out)
+    with profile(activities=[ProfilerActivity.CUDA]) as p:
+        layer.forward_into(x, out)
+        torch.cuda.synchronize()
+    kernels = [e for e in p.events() if "lmoe" in e.name and "cuda" not in e.name.lower()[:4]]
+    assert len(kernels) == layer.launch_count(48)
+
+
 def test_prompt_then_tokens():
     """A prompt through lmoe_forward and its first tokens again through the few-token form, on one 4-bit layer: the
     same experts, and results apart by the 4-bit rounding of z and H that only the former has.
