@@ -1297,6 +1297,9 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 // ---- fp32: lane (4-value piece, rows rq + 4 i); two tiles, of one k-block or of two
                 float acc[2][4][FEW_MAX_T] = {};
                 const int piece = lane & 7, rq = lane >> 3;
+                uint32_t off[FEW_MAX_T];                   // of the columns' rows
+#pragma unroll
+                for (int t = 0; t < FEW_MAX_T; ++t) off[t] = (uint32_t)(__shfl_sync(0xffffffffu, tok, t) * a.stride);
                 ok = stages(mine, [&](int c, int k0) {
                     const uint32_t tile = sh.ring + (uint32_t)s * STAGE_BYTES + mytile;
 #pragma unroll
@@ -1315,7 +1318,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
 #pragma unroll
                             for (int t = 0; t < FEW_MAX_T; ++t)
                                 if (t < ncol) {
-                                    const uint4 v = lds128(act + (uint32_t)(__shfl_sync(0xffffffffu, tok, t) * a.stride + 4 * k));
+                                    const uint4 v = lds128(act + off[t] + (uint32_t)(4 * k));
 #pragma unroll
                                     for (int i = 0; i < 4; ++i) {
                                         acc[g][i][t] = fmaf(w[i].x, __uint_as_float(v.x), acc[g][i][t]);
