@@ -64,6 +64,7 @@
 // sum in fp32.  fp32 layers: fp32 FMA.  Router: products and sums in 64 bits, because the selection
 // has to be that of the scores and not of their rounding.
 #include <algorithm>
+#include <cfloat>
 
 #include <cuda_fp16.h>
 
@@ -292,10 +293,11 @@ __device__ __forceinline__ double widen_bf16(uint32_t f)
     return __hiloint2double((int)((f & 0x80000000u) | (((f & 0x7fff0000u) >> 3) + 0x38000000u)), 0);
 }
 
-// Order-preserving 64-bit key of a double (-0 counts as 0).
+// Order-preserving 64-bit key of a biased score (-0 counts as 0).  NaN and what is below -FLT_MAX
+// count as -FLT_MAX, as in the selection of lmoe_forward: they come last, lower index first.
 __device__ __forceinline__ unsigned long long key64(double v)
 {
-    const unsigned long long u = (unsigned long long)__double_as_longlong(v + 0.0);
+    const unsigned long long u = (unsigned long long)__double_as_longlong(fmax(v, -(double)FLT_MAX) + 0.0);
     return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
 }
 
