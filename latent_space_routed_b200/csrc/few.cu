@@ -119,6 +119,8 @@ struct FewParams {
     float gate_cap, up_cap, eps;
     const void *x;
     const float *bias;
+    const float *Wr;
+    const uint32_t *wr_top;  // largest |W_r| (bits)
     void *y, *p_out, *u_out;
     int32_t *sel;
     unsigned *ctl;
@@ -282,8 +284,12 @@ __device__ __forceinline__ bool wait_count(const unsigned *ctl, int word, unsign
 }
 
 // fp32 bits (those of a bf16 in the upper half) as a double by integer operations: the conversion
-// instruction takes 8 cycles of a quarter SM, these 3 to 5.  Zeros and subnormals come out as
-// 2^-127 (1 + m), which is nothing beside a score's 2^-53.
+// instruction takes 8 cycles of a quarter SM, these 3 to 5.  They know no exponents 0 and 255: zeros and
+// subnormals come out as 2^-127 (1 + m), infinities and NaN as finite numbers.  So they serve only where
+// every value of x and W_r is below 2^32 (ROUTER_WIDE): a zero's term is then below 2^-95, a whole sum of
+// them below 2^-71, and 1/2, the score where a sum begins to tell, has neighbours 2^-54 apart.  Otherwise
+// exact_scores takes the item's products anew.
+constexpr uint32_t ROUTER_WIDE = (127u + 32u) << 23;
 __device__ __forceinline__ double widen(uint32_t f)
 {
     return __hiloint2double((int)((f & 0x80000000u) | (((f & 0x7fffffffu) >> 3) + 0x38000000u)), (int)(f << 29));
@@ -291,6 +297,16 @@ __device__ __forceinline__ double widen(uint32_t f)
 __device__ __forceinline__ double widen_bf16(uint32_t f)
 {
     return __hiloint2double((int)((f & 0x80000000u) | (((f & 0x7fff0000u) >> 3) + 0x38000000u)), 0);
+}
+
+// The largest magnitude of fp32 values, as bits (NaN above infinity), into *top.
+__global__ void largest_kernel(const uint32_t *__restrict__ v, int64_t n, uint32_t *top)
+{
+    uint32_t m = 0u;
+    for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x)
+        m = max(m, v[i] & 0x7fffffffu);
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((threadIdx.x & 31) == 0) atomicMax(top, m);
 }
 
 // Order-preserving 64-bit key of a biased score (-0 counts as 0).  NaN and what is below -FLT_MAX
@@ -347,7 +363,7 @@ struct Shared {
     float *lred;             // loaders' sums [4]
     // [0] abort, [1] items published, [3] sets of x issued, [25] touched experts, [26, 28) stages issued to each
     // team; items passed: [16, 19) by each loader, [19] by the producer, [20] by the signaller; [32, 42) items
-    // finished by each consumer and finisher warp
+    // finished by each consumer and finisher warp; [44] the router's scores are to be taken anew (exact_scores)
     int *flags;
 };
 
@@ -716,6 +732,24 @@ __device__ __forceinline__ int touched_experts(const FewParams &p, const Select 
         }
     __syncwarp();
     return n;
+}
+
+// Scores of four experts from e0 on with converted values, a warp per pair of token and expert: for x or W_r
+// with values that `widen` does not know (see there).  Out of line: it is rarely called.
+template <int WT>
+__device__ __noinline__ void exact_scores(const FewParams &p, int e0, int warp, int lane)
+{
+    for (int i = warp; i < 4 * p.T; i += CONSUMERS) {
+        const int e = e0 + (i & 3), t = i >> 2;
+        if (e >= p.E) continue;
+        const float *w = p.Wr + (int64_t)e * p.d;
+        double v = 0.0;
+        for (int c = lane; c < p.d; c += 32)
+            v = fma((double)__ldg(w + c), (double)token_value<WT>(p.x, (int64_t)t * p.d + c), v);
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+        if (lane == 0) p.r64[(int64_t)t * p.E + e] = 1.0 / (1.0 + exp(-v));
+    }
 }
 
 // u for 32 latent columns (one per lane) of every token: the token's slots dealt to 8 / T
@@ -1226,8 +1260,30 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                 // ---- 4 rows, 64-bit products: lane (row, 4-value piece)
                 double acc[FEW_MAX_T] = {};
                 const int row = lane >> 3, piece = lane & 7;
+                uint32_t top = __ldg(p.wr_top);        // the largest of |W_r| and this warp's share of x
                 ok = stages(true, [&](int c, int k0) {
                     const uint32_t tile = sh.ring + (uint32_t)s * STAGE_BYTES + mytile;
+                    {
+                        // (read again, a 16-byte piece per lane; a pass over all of x at the start cost 2 us)
+                        constexpr int EB = WT == W_F32 ? 4 : 2;
+                        const int kblk = c * 32 + sub * 8, bytes = 32 * EB * min(8, nkb - kblk);
+                        const uint32_t at = act + (uint32_t)(EB * (kblk * 32 - k0));
+#pragma unroll
+                        for (int i = 16 * lane; i < 256 * EB; i += 512)
+                            if (i < bytes)
+#pragma unroll 2
+                                for (int t = 0; t < p.T; ++t) {
+                                    const uint4 v = lds128(at + (uint32_t)(t * a.stride + i));
+                                    if (WT == W_F32) {
+                                        top = max(max(top, v.x & 0x7fffffffu), max(v.y & 0x7fffffffu, v.z & 0x7fffffffu));
+                                        top = max(top, v.w & 0x7fffffffu);
+                                    } else {
+                                        const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                                                    __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+                                        top = max(top, max(m, m << 16));
+                                    }
+                                }
+                    }
                     // two k-blocks (512 bytes each: 4 rows) per round: the body stays in the
                     // instruction buffers (unrolled over a stage it took 3 K cycles, most of them fetches)
 #pragma unroll 1
@@ -1271,6 +1327,8 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                     release();
                 });
                 if (!ok) break;
+                volatile int *anew = sh.flags + 44;
+                if (top >= ROUTER_WIDE) *anew = 1;
                 double *rd = reinterpret_cast<double *>(sh.sums);     // [8 warps][4 rows][8 tokens]
 #pragma unroll
                 for (int t = 0; t < FEW_MAX_T; ++t)
@@ -1280,7 +1338,9 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
                         if (piece == 0) rd[warp * 32 + row * 8 + t] = acc[t];
                     }
                 if (!(ok = bar.sync())) break;
-                if (warp == 0) {
+                if (*anew) {
+                    exact_scores<WT>(p, 4 * it.j0, warp, lane);
+                } else if (warp == 0) {
                     const int e = 4 * it.j0 + (lane >> 3), t = lane & 7;
                     if (e < p.E && t < p.T) {
                         double v = 0.0;
@@ -1722,6 +1782,14 @@ bool few_make_maps(const lmoe_config &c, const FewWeights &w, FewMaps *m)
     return ok && two(&m->routed_gu, w.Wgu, l, E * 2 * f, 64) && two(&m->routed_down, w.D, f, E * l, 16);
 }
 
+cudaError_t few_largest(const float *v, int64_t n, uint32_t *top, cudaStream_t s)
+{
+    cudaError_t e = cudaMemsetAsync(top, 0, sizeof(uint32_t), s);
+    if (e != cudaSuccess) return e;
+    largest_kernel<<<1024, 256, 0, s>>>((const uint32_t *)v, n, top);
+    return cudaGetLastError();
+}
+
 cudaError_t few_launch(const lmoe_config &c, const FewMaps &m, const FewWeights &w, const float *bias, const void *x, int T,
                        void *y, int32_t *sel, void *p_out, void *u_out, void *workspace, bool stall_test,
                        cudaStream_t s)
@@ -1733,7 +1801,7 @@ cudaError_t few_launch(const lmoe_config &c, const FewMaps &m, const FewWeights 
     p.n = make_plan(c, mx4, T, tc_num_sms());
     p.T = T; p.d = c.d; p.l = c.l; p.f = c.f; p.E = c.E; p.k = c.k; p.fs = c.f_shared; p.act = c.act;
     p.standard = c.standard; p.gate_cap = c.gate_cap; p.up_cap = c.up_cap; p.eps = c.eps;
-    p.x = x; p.bias = bias; p.y = y; p.p_out = p_out; p.u_out = u_out; p.sel = sel;
+    p.x = x; p.bias = bias; p.Wr = w.Wr; p.wr_top = w.Wr_top; p.y = y; p.p_out = p_out; p.u_out = u_out; p.sel = sel;
     p.ctl = (unsigned *)(ws + L.ctl); p.r64 = (double *)(ws + L.r64);
     p.z = (float *)(ws + L.z); p.hs = (float *)(ws + L.hs); p.H = (float *)(ws + L.H);
     p.part = (float *)(ws + L.part); p.ysl = (float *)(ws + L.ysl); p.u = (float *)(ws + L.u);

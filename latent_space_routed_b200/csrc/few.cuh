@@ -18,6 +18,7 @@ struct FewMaps {
 // Weights of a handle, in its own layouts.
 struct FewWeights {
     const float *Wr;
+    const uint32_t *Wr_top;              // largest magnitude in Wr, as bits
     const void *Wdown, *Wgu_s, *Wcat;
     const void *Wgu, *D;                 // token type; codes when mx4
     const void *Wgu_scales, *D_scales;   // mx4: [rows, pitch] with pitches mx4_scale_pitch(l), (f)
@@ -26,6 +27,9 @@ struct FewWeights {
 
 // Bytes between the scale rows of a handle's 4-bit experts, for rows of K values.
 inline int64_t mx4_scale_pitch(int64_t K) { return (K / 32 + 15) / 16 * 16; }
+
+// The largest magnitude of n fp32 values, as bits, to *top (device).
+cudaError_t few_largest(const float *v, int64_t n, uint32_t *top, cudaStream_t s);
 
 bool few_make_maps(const lmoe_config &c, const FewWeights &w, FewMaps *m);
 

@@ -113,6 +113,7 @@ struct lmoe_handle {
     bool mx4 = false;
     uint8_t *Wgu_scales = nullptr;   // [E, 2f, mx4_scale_pitch(l)]
     uint8_t *D_scales = nullptr;     // [E, l, mx4_scale_pitch(f)]
+    uint32_t *Wr_top = nullptr;      // largest |W_r| (bits), for the few-token layer
     FewMaps few;                     // few-token layer: tensor maps of the weights above
     FewWeights few_w;
     bool few_ok = false;
@@ -287,7 +288,8 @@ lmoe_status check_config(const lmoe_config *c, bool *tc)
 void free_handle(lmoe_handle *h)
 {
     if (!h) return;
-    void *ptrs[] = {h->Wr, h->Wr3, h->b, h->Wdown, h->Wgu, h->D, h->Wgu_s, h->Wcat, h->Wgu_scales, h->D_scales};
+    void *ptrs[] = {h->Wr, h->Wr3, h->b, h->Wdown, h->Wgu, h->D, h->Wgu_s, h->Wcat, h->Wgu_scales, h->D_scales,
+                    h->Wr_top};
     for (void *p : ptrs)
         if (p) cudaFree(p);
     if (h->side) cudaStreamDestroy(h->side);
@@ -431,7 +433,9 @@ static lmoe_status create_handle(const lmoe_config *cfg, const lmoe_weights *w, 
     STEP(cudaStreamCreateWithFlags(&h->copy_out, cudaStreamNonBlocking));
     for (cudaEvent_t &e : h->ev_host) STEP(cudaEventCreateWithFlags(&e, cudaEventDisableTiming));
     if (few_ok) {
-        h->few_w = {h->Wr, h->Wdown, h->Wgu_s, h->Wcat, h->Wgu, h->D, h->Wgu_scales, h->D_scales, h->mx4};
+        ALLOC(h->Wr_top, sizeof(uint32_t));
+        STEP(few_largest(h->Wr, (int64_t)c.E * c.d, h->Wr_top, s));
+        h->few_w = {h->Wr, h->Wr_top, h->Wdown, h->Wgu_s, h->Wcat, h->Wgu, h->D, h->Wgu_scales, h->D_scales, h->mx4};
         h->few_ok = few_make_maps(c, h->few_w, &h->few);
     }
     STEP(cudaStreamSynchronize(s));
