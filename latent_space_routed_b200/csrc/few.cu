@@ -565,6 +565,16 @@ __device__ __forceinline__ void store_token(void *x, int64_t i, float v)
     else ((bf16 *)x)[i] = __float2bfloat16_rn(v);
 }
 
+// Scores of a lane's selected experts (the first of `left` > 0, the second of `left` > 32) over the token's largest.
+__device__ __noinline__ float2 score_ratios(const double *r, int e0, int e1, int left)
+{
+    const double a = left > 0 ? __ldcg(r + e0) : 0.0, b = left > 32 ? __ldcg(r + e1) : 0.0;
+    double m = fmax(a, b);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return make_float2((float)(a / m), (float)(b / m));
+}
+
 // Selection and weights of token t by one warp: the k-th largest 64-bit score key by
 // bisection on the bits of its high word that the keys do not share; low words and
 // indices decide only where the high words tie (rare); then the k in order of key, equal
@@ -677,9 +687,18 @@ __device__ __forceinline__ void select_token(const FewParams &p, const Select &q
                 rv[h] = score[ex[h]];
                 cand[lane + 32 * h] = (unsigned long long)hi[ex[h]] << 32 | lo[ex[h]];
             }
-        float sum = rv[0] + rv[1];
+        float sum;
+#pragma unroll 1
+        for (bool again = false;; again = true) {
+            sum = rv[0] + rv[1];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);      // (the same in all lanes)
+            if (sum >= 1e-30f || again) break;
+            // scores that fp32 holds roughly or not at all
+            const float2 r = score_ratios(p.r64 + (int64_t)t * E, ex[0], ex[1], p.k - lane);
+            rv[0] = r.x;
+            rv[1] = r.y;
+        }
         __syncwarp();
 #pragma unroll
         for (int h = 0; h < 2; ++h) {

@@ -107,3 +107,17 @@ def test_nan_router_rows_are_left_out_as_in_lmoe_forward():
     assert torch.equal(few["selected_experts"], many["selected_experts"])
     assert not ((few["selected_experts"] == 3) | (few["selected_experts"] == 8)).any()
     assert torch.isfinite(few["output"]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("low", [60, 80, 100, 110, 300, 700])
+def test_weights_of_scores_below_fp32(low, dtype):
+    """Logits -low, -low - 1/2, ...: scores that fp32 holds roughly or not at all have the weights of their ratios."""
+    w, W, _ = make(3, 256, 64, 128, 16, 6, dtype=dtype)
+    x = torch.ones_like(li.tokens(w))
+    W["W_r"] = (-(low + torch.arange(16).flip(0) * 0.5) / 256)[:, None].repeat(1, 256)     # exact sums
+    W["b"] = torch.zeros(16)
+    layer = layer_of(w, W)
+    out = layer.forward_few(x.cuda())
+    check_router(out, x, W, 6)
+    check(out, x, W, w)
