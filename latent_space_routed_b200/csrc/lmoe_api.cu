@@ -569,9 +569,9 @@ lmoe_status lmoe_mx4_gemm(const void *a_codes, const void *a_scales, int64_t M, 
     if (offsets && E > 1024) return fail(LMOE_ERR_UNSUPPORTED, "E=%d > 1024", E);
     if (M == 0 || N == 0) return LMOE_OK;
     if (K == 0 || K % 64) return fail(LMOE_ERR_UNSUPPORTED, "K=%lld is not a positive multiple of 64", (long long)K);
-    // rows of W and columns are indexed in 32 bits up to the end of the last tile (192 of either)
+    // rows of W, columns and K are indexed in 32 bits up to the end of the last tile (192) or stage (256)
     const int64_t rows = (offsets ? E : 1) * N, most = 0x7fffffffLL;
-    if (M > most / 2 || K > most || N > most - 256 || rows > most - 256 || ((M + 127) / 128 + (offsets ? E : 0)) > most / ((N + 63) / 64))
+    if (M > most / 2 || K > most - 256 || N > most - 256 || rows > most - 256 || ((M + 127) / 128 + (offsets ? E : 0)) > most / ((N + 63) / 64))
         return fail(LMOE_ERR_UNSUPPORTED, "sizes exceed 2^31");
     if (!a_codes || !a_scales || !w_codes || !w_scales || !out) return fail(LMOE_ERR_INVALID_ARG, "NULL pointer");
     if (((uintptr_t)a_codes | (uintptr_t)w_codes) & 15u)

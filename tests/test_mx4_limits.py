@@ -15,3 +15,10 @@ def test_row_indices_past_the_last_tile_fit(kw):
     """The last tile's 192 rows of W are indexed in 32 bits: E N and N stop 256 short of 2^31."""
     assert _gemm(**kw) == UNS
     assert "2^31" in lm.lmoe_last_error()
+
+
+@pytest.mark.parametrize("K", [2 ** 31 - 64, 2 ** 31 - 128, 2 ** 31 - 256])
+def test_columns_past_the_last_stage_fit(K):
+    """K is taken in stages of 256 values, counted in 32 bits."""
+    assert _gemm(K=K, M=1, N=1, ldo=1) == UNS
+    assert "2^31" in lm.lmoe_last_error()
