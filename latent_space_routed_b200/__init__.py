@@ -15,6 +15,7 @@ import contextlib
 import ctypes
 import functools
 import os
+import threading
 from typing import Dict, NamedTuple, Optional
 
 import torch
@@ -441,6 +442,7 @@ class LatentMoE:
         self.device = dev
         self._ws = None
         self._few_ws = {}
+        self._captured_ws = []
 
     def close(self):
         if getattr(self, "handle", None):
@@ -475,27 +477,41 @@ class LatentMoE:
                      out["latent_routed_aggregate"], ws, ws.numel(), stream)
         return out
 
-    def few_workspace(self, T: int) -> torch.Tensor:
-        """The layer's own workspace of forward_few_into for T tokens."""
-        ws = self._few_ws.get(T)
+    def few_workspace(self, T: int, stream=None) -> torch.Tensor:
+        """The workspace that forward_few_into takes by itself for T tokens: one for each stream and thread, whose
+        calls follow one another (two threads' calls on one stream may not: each is a memset and a kernel)."""
+        key = (T, _stream(stream), threading.get_ident())
+        ws = self._few_ws.get(key)
         if ws is None:
-            ws = self._few_ws[T] = torch.empty(max(lmoe_few_workspace_size(self.handle, T), 256), dtype=torch.uint8,
-                                               device=self.device)
+            ws = self._few_ws[key] = self._new_few_workspace(T, stream)
         return ws
+
+    def _new_few_workspace(self, T: int, stream) -> torch.Tensor:
+        with _with(self.device, stream):
+            return torch.empty(max(lmoe_few_workspace_size(self.handle, T), 256), dtype=torch.uint8, device=self.device)
 
     def forward_few_into(self, x: torch.Tensor, out: Dict[str, torch.Tensor], workspace: Optional[torch.Tensor] = None,
                          stream=None):
         """The layer for x [T, d] of 1 to 8 tokens in one kernel, into the four output tensors.
 
-        Calls that may overlap on the GPU, and graphs that may replay beside other
-        calls, need a ``workspace`` of their own (``lmoe_few_workspace_size`` bytes)."""
+        ``workspace`` (``lmoe_few_workspace_size`` bytes) must not be shared by calls that may overlap on the
+        GPU.  Without it, calls outside a capture use ``few_workspace``, and each captured call gets a buffer of
+        its own, which the layer keeps (a graph may replay beside anything): give a graph of many calls one."""
         T = x.shape[0]
         if x.dim() != 2 or x.shape[1] != self.cfg.d or x.dtype != self.dtype or not x.is_contiguous():
             raise ValueError(f"x must be a contiguous {self.dtype} tensor [T, {self.cfg.d}]")
-        ws = self.few_workspace(T) if workspace is None else workspace
+        ws = self._few_workspace_of_call(T, stream) if workspace is None else workspace
         lmoe_forward_few(self.handle, x, T, out["output"], out["selected_experts"], out["mixture_weights"],
                          out["latent_routed_aggregate"], ws, ws.numel(), stream)
         return out
+
+    def _few_workspace_of_call(self, T: int, stream) -> torch.Tensor:
+        with contextlib.nullcontext() if stream is None else _with(self.device, stream):
+            capturing = torch.cuda.is_current_stream_capturing()
+        if not capturing:
+            return self.few_workspace(T, stream)
+        self._captured_ws.append(self._new_few_workspace(T, stream))
+        return self._captured_ws[-1]
 
     def forward_few(self, x: torch.Tensor, stream=None) -> Dict[str, torch.Tensor]:
         """``layer(x)`` for at most 8 tokens, in one kernel."""

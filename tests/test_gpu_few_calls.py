@@ -1,0 +1,84 @@
+"""Calls of the few-token layer as programs make them: several streams and threads, graphs, tensors that do not fit."""
+import threading
+
+import pytest
+import torch
+
+import latent_space_routed_b200 as lm
+import lmoe_inputs as li
+from test_gpu_few import check, make
+
+pytestmark = pytest.mark.gpu
+
+
+def same(a, b):
+    return all(torch.equal(a[n], b[n]) for n in a)
+
+
+def test_workspaces_of_streams_and_threads_differ():
+    """A buffer of the layer's own serves calls that follow one another only: one stream, one thread."""
+    w, W, layer = make(4, 256, 64, 128, 16, 4)
+    s = torch.cuda.Stream()
+    mine = layer.few_workspace(4)
+    with torch.cuda.stream(s):
+        other = layer.few_workspace(4)
+    got = []
+    t = threading.Thread(target=lambda: got.append(layer.few_workspace(4)))
+    t.start(), t.join()
+    assert len({v.data_ptr() for v in (mine, other, got[0], layer.few_workspace(5))}) == 4
+    assert layer.few_workspace(4).data_ptr() == mine.data_ptr() == layer.few_workspace(4, torch.cuda.current_stream()).data_ptr()
+    assert layer.few_workspace(4, s).data_ptr() == layer.few_workspace(4, s.cuda_stream).data_ptr() == other.data_ptr()
+
+
+def test_two_streams_and_threads_without_workspaces():
+    w, W, layer = make(6, 512, 128, 256, 32, 6)
+    xs = [li.tokens(w, seed=i).cuda() for i in range(4)]
+    want = [layer.forward_few(x) for x in xs]
+    torch.cuda.synchronize()
+    got = []
+
+    def calls(streams, on_thread_stream):
+        for i in range(40):
+            s = streams[i % len(streams)]
+            if on_thread_stream:                       # by the argument, or as the current stream
+                got.append((i % 4, layer.forward_few(xs[i % 4], stream=s)))
+            else:
+                with torch.cuda.stream(s):
+                    got.append((i % 4, layer.forward_few(xs[i % 4])))
+
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    calls(streams[:2], False)
+    calls(streams[1:], True)
+    threads = [threading.Thread(target=calls, args=([streams[i % 2]], i > 1)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert len(got) == 240
+    for i, out in got:
+        assert same(out, want[i])
+
+
+def test_graphs_without_workspaces_replay_at_once():
+    w, W, layer = make(4, 512, 128, 256, 32, 6)
+    xs = [li.tokens(w, seed=i).cuda() for i in range(2)]
+    want = [layer.forward_few(x) for x in xs]
+    graphs = []
+    for x in xs:                                       # captured on one stream, one after the other
+        g, out = torch.cuda.CUDAGraph(), layer.empty_outputs(4)
+        with torch.cuda.graph(g):
+            layer.forward_few_into(x, out)
+            layer.forward_few_into(x, out)
+        graphs.append((g, out))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (g, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        eager = layer.forward_few(xs[1])
+    torch.cuda.synchronize()
+    assert same(eager, want[1])
+    for (_, out), r in zip(graphs, want):
+        assert same(out, r)
