@@ -492,7 +492,8 @@ class LatentMoE:
 
     def forward_few_into(self, x: torch.Tensor, out: Dict[str, torch.Tensor], workspace: Optional[torch.Tensor] = None,
                          stream=None):
-        """The layer for x [T, d] of 1 to 8 tokens in one kernel, into the four output tensors.
+        """The layer for x [T, d] of 1 to 8 tokens in one kernel, into the four output tensors (x that
+        is not 16-byte aligned is copied first).
 
         ``workspace`` (``lmoe_few_workspace_size`` bytes) must not be shared by calls that may overlap on the
         GPU.  Without it, calls outside a capture use ``few_workspace``, and each captured call gets a buffer of
@@ -500,6 +501,9 @@ class LatentMoE:
         T = x.shape[0]
         if x.dim() != 2 or x.shape[1] != self.cfg.d or x.dtype != self.dtype or not x.is_contiguous():
             raise ValueError(f"x must be a contiguous {self.dtype} tensor [T, {self.cfg.d}]")
+        if x.data_ptr() % 16:
+            with contextlib.nullcontext() if stream is None else _with(self.device, stream):
+                x = x.clone()
         ws = self._few_workspace_of_call(T, stream) if workspace is None else workspace
         lmoe_forward_few(self.handle, x, T, out["output"], out["selected_experts"], out["mixture_weights"],
                          out["latent_routed_aggregate"], ws, ws.numel(), stream)

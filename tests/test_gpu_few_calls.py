@@ -82,3 +82,16 @@ def test_graphs_without_workspaces_replay_at_once():
     assert same(eager, want[1])
     for (_, out), r in zip(graphs, want):
         assert same(out, r)
+
+
+def test_tokens_at_any_address():
+    """x that is contiguous but not 16-byte aligned is copied, as mx4_quantize does."""
+    for dtype in ("bf16", "f32"):
+        w, W, layer = make(3, 256, 64, 128, 16, 4, dtype=dtype)
+        x = li.tokens(w)
+        want = layer.forward_few(x.cuda())
+        flat = torch.empty(3 * 256 + 1, dtype=layer.dtype, device="cuda")
+        odd = flat[1:].view(3, 256).copy_(x)
+        assert odd.data_ptr() % 16
+        assert same(layer.forward_few(odd), want)
+        assert same(layer.forward_few_into(odd, layer.empty_outputs(3)), want)
