@@ -499,14 +499,22 @@ class LatentMoE:
         GPU.  Without it, calls outside a capture use ``few_workspace``, and each captured call gets a buffer of
         its own, which the layer keeps (a graph may replay beside anything): give a graph of many calls one."""
         T = x.shape[0]
-        if x.dim() != 2 or x.shape[1] != self.cfg.d or x.dtype != self.dtype or not x.is_contiguous():
-            raise ValueError(f"x must be a contiguous {self.dtype} tensor [T, {self.cfg.d}]")
+        c = self.cfg
+        if x.dim() != 2 or x.shape[1] != c.d or x.dtype != self.dtype or not x.is_contiguous() or x.device != self.device:
+            raise ValueError(f"x must be a contiguous {self.dtype} tensor [T, {c.d}] on {self.device}")
+        for name, cols, dtype in (("output", c.d, self.dtype), ("selected_experts", c.k, torch.int32),
+                                  ("mixture_weights", c.k, self.dtype), ("latent_routed_aggregate", c.l, self.dtype)):
+            t = out[name]
+            if t.dtype != dtype or t.numel() < T * cols or not t.is_contiguous() or t.device != self.device:
+                raise ValueError(f"{name} must be a contiguous {dtype} tensor of {T} x {cols} values or more on {self.device}")
+        if workspace is not None and (workspace.device != self.device or not workspace.is_contiguous()):
+            raise ValueError(f"workspace must be a contiguous tensor on {self.device}")
         if x.data_ptr() % 16:
             with contextlib.nullcontext() if stream is None else _with(self.device, stream):
                 x = x.clone()
         ws = self._few_workspace_of_call(T, stream) if workspace is None else workspace
         lmoe_forward_few(self.handle, x, T, out["output"], out["selected_experts"], out["mixture_weights"],
-                         out["latent_routed_aggregate"], ws, ws.numel(), stream)
+                         out["latent_routed_aggregate"], ws, ws.numel() * ws.element_size(), stream)
         return out
 
     def _few_workspace_of_call(self, T: int, stream) -> torch.Tensor:
