@@ -299,7 +299,7 @@ class Mx4(NamedTuple):
     def shape(self):
         return (*self.codes.shape[:-1], 2 * self.codes.shape[-1])
 
-    def check(self, what: str) -> "Mx4":
+    def check(self, what: str, device: Optional[torch.device] = None) -> "Mx4":
         c, s = self.codes, self.scales
         if c.dtype != torch.uint8 or s.dtype != torch.uint8:
             raise TypeError(f"{what}: codes and scales must be uint8, got {c.dtype} and {s.dtype}")
@@ -308,6 +308,8 @@ class Mx4(NamedTuple):
                              f"{tuple(c.shape)}, {tuple(s.shape)}")
         if not c.is_cuda or c.device != s.device:
             raise ValueError(f"{what}: codes and scales must be on one CUDA device")
+        if device is not None and c.device != device:
+            raise ValueError(f"{what} must be on {device}, not {c.device}")
         if not c.is_contiguous() or not s.is_contiguous():
             raise ValueError(f"{what}: codes and scales must be contiguous")
         return self
@@ -420,6 +422,14 @@ class LatentMoE:
         self.cfg = cfg
         self.dtype = _TORCH_DT[cfg.dtype]
         dev = torch.device("cuda", torch.cuda.current_device())
+        self.mx4 = any(isinstance(weights[n], Mx4) for n in ("G", "U", "D"))
+        if self.mx4:
+            shapes = {"G": (cfg.E, cfg.f, cfg.l), "U": (cfg.E, cfg.f, cfg.l), "D": (cfg.E, cfg.l, cfg.f)}
+            for n, shape in shapes.items():
+                if not isinstance(weights[n], Mx4):
+                    raise TypeError("G, U and D must all be Mx4 tensors, or none of them")
+                if weights[n].check(n, dev).shape != shape:
+                    raise ValueError(f"{n}: shape {weights[n].shape} != {shape}")
         w = {}
         for n in ("W_r", "b", "W_down", "W_up", "G", "U", "D", "Gs", "Us", "Ds"):
             if cfg.standard and n in ("W_down", "W_up"):
@@ -428,14 +438,7 @@ class LatentMoE:
                 continue
             want = torch.float32 if n in ("W_r", "b") else self.dtype
             w[n] = weights[n].to(device=dev, dtype=want).contiguous()
-        self.mx4 = any(isinstance(weights[n], Mx4) for n in ("G", "U", "D"))
         if self.mx4:
-            shapes = {"G": (cfg.E, cfg.f, cfg.l), "U": (cfg.E, cfg.f, cfg.l), "D": (cfg.E, cfg.l, cfg.f)}
-            for n, shape in shapes.items():
-                if not isinstance(weights[n], Mx4):
-                    raise TypeError("G, U and D must all be Mx4 tensors, or none of them")
-                if weights[n].check(n).shape != shape:
-                    raise ValueError(f"{n}: shape {weights[n].shape} != {shape}")
             self.handle = lmoe_create_mx4(cfg, w, {n: weights[n] for n in shapes}, stream)
         else:
             self.handle = lmoe_create(cfg, w, stream)
