@@ -322,6 +322,8 @@ def _with(device, stream):
         if not isinstance(stream, torch.cuda.Stream):
             handle = _stream(stream)
             stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
         return torch.cuda.stream(stream)
     return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 

@@ -18,3 +18,14 @@ def test_experts_of_another_device_are_refused(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)       # the layer would be made there
     with pytest.raises(ValueError, match="G must be on cuda:1"):
         lm.LatentMoE(lm.config_for(w), {**W, **Q})
+
+
+def test_streams_of_another_device_are_refused():
+    """A kernel launched there would read this device's addresses."""
+    s = torch.cuda.Stream()
+    with pytest.raises(ValueError, match="stream"):
+        lm._with(torch.device("cuda", 1), s)
+    with lm._with(torch.device("cuda", 0), s):
+        assert torch.cuda.current_stream() == s
+    with lm._with(torch.device("cuda", 0), torch.cuda.ExternalStream(s.cuda_stream)):
+        assert torch.cuda.current_stream().cuda_stream == s.cuda_stream
