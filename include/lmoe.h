@@ -350,6 +350,9 @@ LMOE_API lmoe_status lmoe_set_stage_events(lmoe_handle *h, void *const *events, 
  *      or hangs; the context stays usable.  (arg ignored.)
  *  LMOE_INJECT_STALL_NEXT_FEW  a wait of the next lmoe_forward_few call runs out
  *      in the same way (arg ignored).
+ *  LMOE_INJECT_STALL_NEXT_MX4  a wait of the next 4-bit product (lmoe_mx4_gemm, or
+ *      one of lmoe_forward's with 4-bit experts) runs out in the same way (arg
+ *      ignored).
  *  LMOE_INJECT_FAIL_ALLOC  the arg-th device allocation (1-based) of the next
  *      lmoe_create fails as if cudaMalloc had: lmoe_create returns LMOE_ERR_OOM
  *      and frees what it had allocated.
@@ -357,6 +360,7 @@ LMOE_API lmoe_status lmoe_set_stage_events(lmoe_handle *h, void *const *events, 
 #define LMOE_INJECT_STALL_NEXT_GEMM 1
 #define LMOE_INJECT_FAIL_ALLOC 2
 #define LMOE_INJECT_STALL_NEXT_FEW 3
+#define LMOE_INJECT_STALL_NEXT_MX4 4
 LMOE_API lmoe_status lmoe_debug_inject(int32_t what, int32_t arg);
 
 /* Number of kernels one lmoe_forward of T tokens launches (its two memsets,

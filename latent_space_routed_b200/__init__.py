@@ -223,7 +223,7 @@ def lmoe_forward_host(h, x_host, T, output_host, selected_experts_host, mixture_
 
 
 LMOE_NOALLOC_WORKSPACE_BYTES = 64 << 20
-LMOE_INJECT_STALL_NEXT_GEMM, LMOE_INJECT_FAIL_ALLOC, LMOE_INJECT_STALL_NEXT_FEW = 1, 2, 3
+LMOE_INJECT_STALL_NEXT_GEMM, LMOE_INJECT_FAIL_ALLOC, LMOE_INJECT_STALL_NEXT_FEW, LMOE_INJECT_STALL_NEXT_MX4 = 1, 2, 3, 4
 LMOE_FEW_MAX_T = 8
 
 
@@ -373,11 +373,45 @@ def mx4_gemm_workspace(device=None) -> torch.Tensor:
                        device=torch.device("cuda", torch.cuda.current_device()) if device is None else device)
 
 
+# status words of mx4_gemm calls without a workspace: device index -> stream -> workspace
+_mx4_words: Dict[int, Dict[int, torch.Tensor]] = {}
+
+
+def _mx4_word(device: torch.device) -> torch.Tensor:
+    """The status word of the current stream (of `device`).  Words only ever gain bits, so calls may share one; a
+    captured call takes one that exists, since its own would be zeroed by every replay."""
+    words = _mx4_words.setdefault(device.index, {})
+    key = _stream(None)
+    if key not in words:
+        if torch.cuda.is_current_stream_capturing():
+            return next(iter(words.values())) if words else mx4_gemm_workspace(device)
+        words[key] = mx4_gemm_workspace(device)
+    return words[key]
+
+
+def mx4_gemm_check(device=None):
+    """Wait for the device (the current one by default), then raise LmoeError (LMOE_ERR_DEVICE_TIMEOUT) if a bounded
+    wait gave up in an mx4_gemm call on it that had no ``workspace``; their outputs are then invalid.  (A call that
+    was captured before any other had been made on its device has no word here: give such a call a workspace.)"""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    with torch.cuda.device(device):
+        torch.cuda.synchronize()
+        failed = None
+        for word in list(_mx4_words.get(torch.cuda.current_device(), {}).values()):
+            try:
+                lmoe_mx4_gemm_check(word)
+            except LmoeError as e:
+                failed = e
+    if failed is not None:
+        raise failed
+
+
 def mx4_gemm(a: Mx4, w: Mx4, offsets: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16,
              out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """a [M, K] times w [N, K] transposed, in 4 bits with fp32 sums; with offsets [E + 1] (int32, on the device)
     rows offsets[e] to offsets[e + 1] of a times w[e] of w [E, N, K].  ``out`` [M, N] (its dtype counts then) may
-    have a row stride; without it, rows that belong to no expert are zero."""
+    have a row stride; without it, rows that belong to no expert are zero.  ``mx4_gemm_check`` reports a wait that
+    gave up, ``lmoe_mx4_gemm_check`` that of a call with a ``workspace``."""
     a.check("a"), w.check("w")
     if a.codes.dim() != 2 or w.codes.dim() != (2 if offsets is None else 3):
         raise ValueError("a must be [M, K] and w [N, K], or [E, N, K] with offsets")
@@ -401,7 +435,7 @@ def mx4_gemm(a: Mx4, w: Mx4, offsets: Optional[torch.Tensor] = None, dtype: torc
     if w.codes.device != dev or out.device != dev or (workspace is not None and workspace.device != dev):
         raise ValueError(f"all tensors must be on {dev}")
     with _with(dev, stream):
-        ws = mx4_gemm_workspace(dev) if workspace is None else workspace
+        ws = _mx4_word(dev) if workspace is None else workspace
         lmoe_mx4_gemm(a.codes, a.scales, M, w.codes, w.scales, N, K, offsets, E, _LM_DT[out.dtype], out,
                       out.stride(0) if M > 1 else N, ws, ws.numel() * ws.element_size())
     return out

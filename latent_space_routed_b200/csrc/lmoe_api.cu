@@ -639,6 +639,10 @@ lmoe_status lmoe_debug_inject(int32_t what, int32_t arg)
         g_stall_few.store(1);
         return LMOE_OK;
     }
+    if (what == LMOE_INJECT_STALL_NEXT_MX4) {
+        mx4_debug_stall_next();
+        return LMOE_OK;
+    }
     if (what == LMOE_INJECT_FAIL_ALLOC) {
         if (arg < 1) return fail(LMOE_ERR_INVALID_ARG, "allocation index must be >= 1");
         g_fail_alloc_at.store(arg);

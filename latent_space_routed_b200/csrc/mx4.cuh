@@ -41,5 +41,7 @@ struct Mx4GemmArgs {
     int64_t ldo;
 };
 cudaError_t launch_mx4_gemm(const Mx4GemmArgs &g, int32_t *status, cudaStream_t s);
+// Failure-detection test hook: a wait of the next launch_mx4_gemm runs out.
+void mx4_debug_stall_next();
 
 }  // namespace lmoe

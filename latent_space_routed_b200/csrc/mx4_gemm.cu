@@ -68,6 +68,7 @@ struct Params {
     const float *row_w;           // WEIGHTED: weight of each row
     float gate_cap, up_cap;
     int32_t *status;
+    int stall_test;
 };
 
 // Shared-memory descriptor: K-major, 128-byte swizzle, 8-row atoms 1024 bytes apart.
@@ -374,7 +375,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             // ------------------------------------------------------ MMA issuer
             int s = 0, local = 0;
             uint32_t ph = 0;
-            bool ok = true;
+            bool ok = !p.stall_test || mbar_wait(accf, 0u, abort);      // (the failure-detection test: nothing arrives there)
             for (int item = blockIdx.x; item < total && ok; item += gridDim.x, ++local) {
                 const int acc = local & 1;
                 if (!(ok = mbar_wait(acce + 8 * acc, ((uint32_t)(local >> 1) & 1u) ^ 1u, abort))) break;
@@ -543,6 +544,8 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
+std::atomic<int> g_stall_next{0};
+
 template <typename TO, int MODE>
 cudaError_t launch(const CUtensorMap &a, const CUtensorMap &w, const Params &p, int grid, cudaStream_t s)
 {
@@ -560,6 +563,8 @@ cudaError_t launch(const CUtensorMap &a, const CUtensorMap &w, const Params &p, 
 }
 }  // namespace
 
+void mx4_debug_stall_next() { g_stall_next.store(1); }
+
 cudaError_t launch_mx4_gemm(const Mx4GemmArgs &g, int32_t *status, cudaStream_t s)
 {
     CUtensorMap a, w;
@@ -570,7 +575,7 @@ cudaError_t launch_mx4_gemm(const Mx4GemmArgs &g, int32_t *status, cudaStream_t 
     Params p = {};
     p.a_scales = g.a_scales; p.w_scales = g.w_scales; p.a_pitch = g.a_pitch; p.w_pitch = g.w_pitch;
     p.M = g.M; p.N = g.N; p.K = g.K; p.E = g.E; p.grouped = g.offsets != nullptr; p.offsets = g.offsets;
-    p.out = g.out; p.ldo = g.ldo; p.status = status;
+    p.out = g.out; p.ldo = g.ldo; p.status = status; p.stall_test = g_stall_next.exchange(0);
     const int64_t ntn = (g.N + BN - 1) / BN;
     const int64_t tiles = ((g.M + BM - 1) / BM + (g.offsets ? g.E : 0)) * ntn;     // at most
     const int sms = tc_num_sms() > 0 ? tc_num_sms() : 148;
