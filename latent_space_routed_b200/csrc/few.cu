@@ -167,7 +167,7 @@ __device__ __forceinline__ ActPlan act_plan(const FewParams &p, const Item &it)
     }
     a.kseg = a.K;
     a.nseg = 1;
-    if (it.ncol * a.planes * act_stride(a.K, a.eb, mx4) > p.slot_bytes) {
+    if (it.ncol * a.planes * min(act_stride(a.K, a.eb, mx4), 1 << 24) > p.slot_bytes) {     // (within 32 bits)
         // whole steps of 1024 values (a stage holds 128 to 1024), as many as fit
         const int per = p.slot_bytes / (it.ncol * a.planes) - 64;
         a.kseg = per / (1024 * a.eb) * 1024;
@@ -1832,13 +1832,14 @@ cudaError_t few_launch(const lmoe_config &c, const FewMaps &m, const FewWeights 
     // Activation slots: the longest row set of any item, up to 58 KB (longer ones
     // come in segments); the rest of shared memory is the weight ring.
     const bool f32 = c.dtype == LMOE_F32;
-    auto need = [&](int K, int eb, int planes, bool q) { return T * planes * act_stride(K, eb, q); };
+    constexpr int SLOT_MAX = 58 * 1024;
+    auto need = [&](int K, int eb, int planes, bool q) { return T * planes * std::min(act_stride(K, eb, q), SLOT_MAX); };
     int slot = need(c.d, f32 ? 4 : 2, 1, false);
     const int two = f32 ? 1 : 2, eb = f32 ? 4 : 2;
     slot = std::max(slot, need(c.l, eb, two, true));
     slot = std::max(slot, need(c.f, eb, two, true));
     slot = std::max(slot, need(c.f_shared, eb, two, true));
-    slot = std::min(slot, 58 * 1024);
+    slot = std::min(slot, SLOT_MAX);
     slot = std::max(slot, std::min(T, LOADERS) * select_bytes((c.E + 127) / 128 * 128));     // the selection's scratch
     slot = (slot + 1023) / 1024 * 1024;
     p.slot_bytes = slot;

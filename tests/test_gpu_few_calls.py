@@ -95,3 +95,35 @@ def test_tokens_at_any_address():
         assert odd.data_ptr() % 16
         assert same(layer.forward_few(odd), want)
         assert same(layer.forward_few_into(odd, layer.empty_outputs(3)), want)
+
+
+def test_hidden_rows_of_2_to_the_26():
+    """8 tokens' rows of the hidden are 2^31 bytes of activation terms: sizes beyond 32 bits come in segments too.
+    Sums of 2^26 fp32 products in chains add errors of random sign, 2^13 2^-25 of a row's typical value; the rest as in
+    test_gpu_few."""
+    T, d, f = 8, 64, 2 ** 26
+    w, W, _ = make(T, d, d, 128, 1, 1)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    Q = {}
+    for n, shape in (("G", (1, f, d)), ("U", (1, f, d)), ("D", (1, d, f))):
+        codes = torch.randint(0, 256, (*shape[:-1], shape[-1] // 2), generator=g, device="cuda", dtype=torch.uint8)
+        # values of 2^-5 in G and U, of 2^-13 in D
+        scales = torch.full((*shape[:-1], shape[-1] // 32), 121 if n != "D" else 113, device="cuda", dtype=torch.uint8)
+        Q[n] = lm.Mx4(codes, scales)
+    cfg = lm.make_config(d, d, f, 1, 1, 128)
+    layer = lm.LatentMoE(cfg, {**{n: v.cuda() for n, v in W.items()}, **Q})
+    x = li.tokens(w).cuda()
+    out = layer.forward_few(x)
+    lm.lmoe_check_device(layer.handle, T, layer.few_workspace(T))
+    z = x.double() @ W["W_down"].double().cuda().T
+    u, n = torch.zeros(T, d, dtype=torch.float64, device="cuda"), 2 ** 21
+    for i in range(0, f, n):
+        G, U = (lm.mx4_dequantize(lm.Mx4(Q[k].codes[0, i:i + n], Q[k].scales[0, i:i + n]), torch.float32).double() for k in "GU")
+        D = lm.mx4_dequantize(lm.Mx4(Q["D"].codes[0, :, i // 2:(i + n) // 2].contiguous(),
+                                     Q["D"].scales[0, :, i // 32:(i + n) // 32].contiguous()), torch.float32).double()
+        a = z @ G.T
+        u += (a * torch.sigmoid(a) * (z @ U.T)) @ D.T
+    got = out["latent_routed_aggregate"].double()
+    assert ((got - u).abs() <= 2.0 ** -8 * u.abs() + 2.0 ** -9 * u.abs().amax(1, keepdim=True)).all()
+    del layer, Q, out
+    torch.cuda.empty_cache()
