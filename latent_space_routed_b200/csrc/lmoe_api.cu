@@ -116,7 +116,7 @@ struct lmoe_handle {
     uint32_t *Wr_top = nullptr;      // largest |W_r| (bits), for the few-token layer
     FewMaps few;                     // few-token layer: tensor maps of the weights above
     FewWeights few_w;
-    bool few_ok = false;
+    const char *few_missing = nullptr;   // why this handle has no few-token layer
     void *Wgu_s;      // [4 f_s, d] interleaved (both shared experts as one of width 2 f_s)
     void *Wcat;       // [d, 2 f_s + l]
     void *const *stage_events;  // caller's cudaEvent_t[LMOE_NUM_STAGES + 1] or NULL
@@ -355,7 +355,6 @@ static lmoe_status create_handle(const lmoe_config *cfg, const lmoe_weights *w, 
     }
     st = tc_check_device();   // the tensor-map encoder and an sm_100 device
     if (tc && st != LMOE_OK) return st;
-    const bool few_ok = st == LMOE_OK;
     cudaStream_t s = (cudaStream_t)stream;
     lmoe_handle *h = new lmoe_handle();
     h->cfg = *cfg;
@@ -432,11 +431,13 @@ static lmoe_status create_handle(const lmoe_config *cfg, const lmoe_weights *w, 
     STEP(cudaStreamCreateWithFlags(&h->copy_in, cudaStreamNonBlocking));
     STEP(cudaStreamCreateWithFlags(&h->copy_out, cudaStreamNonBlocking));
     for (cudaEvent_t &e : h->ev_host) STEP(cudaEventCreateWithFlags(&e, cudaEventDisableTiming));
-    if (few_ok) {
+    if (st != LMOE_OK) {
+        h->few_missing = "needs an sm_100 device";
+    } else {
         ALLOC(h->Wr_top, sizeof(uint32_t));
         STEP(few_largest(h->Wr, (int64_t)c.E * c.d, h->Wr_top, s));
         h->few_w = {h->Wr, h->Wr_top, h->Wdown, h->Wgu_s, h->Wcat, h->Wgu, h->D, h->Wgu_scales, h->D_scales, h->mx4};
-        h->few_ok = few_make_maps(c, h->few_w, &h->few);
+        if (!few_make_maps(c, h->few_w, &h->few)) h->few_missing = "has no tensor maps: their encoding failed at creation";
     }
     STEP(cudaStreamSynchronize(s));
 #undef ALLOC
@@ -495,7 +496,7 @@ lmoe_status lmoe_forward_few(lmoe_handle *h, const void *x, int64_t T, void *out
         return fail(LMOE_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, few_workspace_bytes(h->cfg, T));
     if ((uintptr_t)workspace % 256) return fail(LMOE_ERR_WORKSPACE, "workspace not 256-byte aligned");
     if ((uintptr_t)x & 15u) return fail(LMOE_ERR_UNSUPPORTED, "x must be 16-byte aligned");
-    if (!h->few_ok) return fail(LMOE_ERR_UNSUPPORTED, "the few-token layer needs an sm_100 device");
+    if (h->few_missing) return fail(LMOE_ERR_UNSUPPORTED, "the few-token layer %s", h->few_missing);
     const lmoe_status st = check_current_device(h);
     if (st != LMOE_OK) return st;
     LMOE_CUDA(few_launch(h->cfg, h->few, h->few_w, h->b, x, (int)T, output, selected_experts, mixture_weights,
