@@ -578,6 +578,7 @@ lmoe_status lmoe_mx4_gemm(const void *a_codes, const void *a_scales, int64_t M, 
     if (((uintptr_t)a_codes | (uintptr_t)w_codes) & 15u)
         return fail(LMOE_ERR_UNSUPPORTED, "codes must be 16-byte aligned");
     if ((uintptr_t)out % (dtype == LMOE_BF16 ? 2 : 4)) return fail(LMOE_ERR_UNSUPPORTED, "out is misaligned");
+    if ((uintptr_t)offsets % 4) return fail(LMOE_ERR_UNSUPPORTED, "offsets are misaligned");
     const lmoe_status st = tc_device_once();
     if (st != LMOE_OK) return fail(st, "4-bit products need an sm_100 device");
     Mx4GemmArgs g = {};

@@ -22,3 +22,9 @@ def test_columns_past_the_last_stage_fit(K):
     """K is taken in stages of 256 values, counted in 32 bits."""
     assert _gemm(K=K, M=1, N=1, ldo=1) == UNS
     assert "2^31" in lm.lmoe_last_error()
+
+
+@pytest.mark.parametrize("at", [1, 2, 3])
+def test_offsets_are_words(at):
+    assert _gemm(off=A + at, E=2) == UNS
+    assert "offsets" in lm.lmoe_last_error()
