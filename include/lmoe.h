@@ -226,7 +226,8 @@ LMOE_API lmoe_status lmoe_few_workspace_size(const lmoe_handle *h, int64_t T, si
  * lmoe_forward's by roundings.  Results do not depend on timing: two calls on
  * the same inputs are bit-identical.  Workspace regions and stage events are
  * not available; lmoe_check_device on this workspace reports its waits.
- * UNSUPPORTED: T > LMOE_FEW_MAX_T, x not 16-byte aligned, or no sm_100 device.
+ * UNSUPPORTED: T > LMOE_FEW_MAX_T, x not 16-byte aligned, an output not aligned
+ * to its type, or no sm_100 device.
  * INVALID_ARG also when the handle's device is not current. */
 LMOE_API lmoe_status lmoe_forward_few(lmoe_handle *h, const void *x, int64_t T, void *output,
                                       int32_t *selected_experts, void *mixture_weights,

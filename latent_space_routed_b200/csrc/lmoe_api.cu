@@ -496,6 +496,9 @@ lmoe_status lmoe_forward_few(lmoe_handle *h, const void *x, int64_t T, void *out
         return fail(LMOE_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, few_workspace_bytes(h->cfg, T));
     if ((uintptr_t)workspace % 256) return fail(LMOE_ERR_WORKSPACE, "workspace not 256-byte aligned");
     if ((uintptr_t)x & 15u) return fail(LMOE_ERR_UNSUPPORTED, "x must be 16-byte aligned");
+    if (((uintptr_t)output | (uintptr_t)mixture_weights | (uintptr_t)latent_routed_aggregate) % h->tb ||
+        (uintptr_t)selected_experts % 4)
+        return fail(LMOE_ERR_UNSUPPORTED, "an output is not aligned to its type");
     if (h->few_missing) return fail(LMOE_ERR_UNSUPPORTED, "the few-token layer %s", h->few_missing);
     const lmoe_status st = check_current_device(h);
     if (st != LMOE_OK) return st;

@@ -127,3 +127,15 @@ def test_hidden_rows_of_2_to_the_26():
     assert ((got - u).abs() <= 2.0 ** -8 * u.abs() + 2.0 ** -9 * u.abs().amax(1, keepdim=True)).all()
     del layer, Q, out
     torch.cuda.empty_cache()
+
+
+def test_misaligned_outputs_are_refused():
+    """By the C name, whose addresses are anything: stores of the token type and of int32 would fault."""
+    w, W, layer = make(3, 256, 64, 128, 16, 4)
+    x, ws = li.tokens(w).cuda(), layer.few_workspace(3)
+    room = torch.empty(4, 8192, dtype=torch.uint8, device="cuda")
+    for which, by in ((0, 1), (1, 2), (2, 1), (3, 1)):
+        o = [room[i].data_ptr() + (by if i == which else 0) for i in range(4)]
+        with pytest.raises(lm.LmoeError, match="aligned") as e:
+            lm.lmoe_forward_few(layer.handle, x, 3, *o, ws, ws.numel())
+        assert e.value.status == lm.LMOE_ERR_UNSUPPORTED
