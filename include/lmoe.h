@@ -174,8 +174,8 @@ LMOE_API lmoe_status lmoe_mx4_dequantize(const void *codes, const void *scales, 
  *                      of out that belong to no expert are left as they were
  *  out                 [M, N] dtype, row stride ldo elements
  *  workspace           LMOE_MX4_GEMM_WORKSPACE_BYTES, 256-byte aligned, zero
- *                      before its first call; calls that may overlap need one
- *                      each
+ *                      before its first call; calls may share one, whose
+ *                      status then is that of all of them
  * K is a positive multiple of 64, codes are 16-byte aligned, E <= 1024.  M or N 0 is a
  * no-op.  Runs on the current device, which must be the tensors'.
  * INVALID_ARG: NULL pointer, negative size, unknown dtype, E < 1, ldo < N.
@@ -224,7 +224,13 @@ LMOE_API lmoe_status lmoe_few_workspace_size(const lmoe_handle *h, int64_t T, si
  * scores in 64 bits, and keeps z, the experts' hidden values and RMSNorm(u) in
  * more than the token type's precision, so its results differ from
  * lmoe_forward's by roundings.  Results do not depend on timing: two calls on
- * the same inputs are bit-identical.  Workspace regions and stage events are
+ * the same inputs are bit-identical.  A score that is NaN (NaN in x or W_r, or
+ * infinity times zero) is selected last, as in lmoe_forward, and makes the
+ * token's mixture weights NaN if it is selected.  Blocks of 4-bit experts with
+ * scale byte 0 (2^-127) count as zeros.
+ * When to call it: for fp32 layers always; for bf16 layers up to 4 tokens, with
+ * 4-bit experts up to 3, it is the faster form at most sizes (beyond them
+ * lmoe_forward is, by up to 5 %, with 4-bit experts by up to a third).  Workspace regions and stage events are
  * not available; lmoe_check_device on this workspace reports its waits.
  * UNSUPPORTED: T > LMOE_FEW_MAX_T, x not 16-byte aligned, an output not aligned
  * to its type, or no sm_100 device.

@@ -45,14 +45,18 @@
 //   warps 14-15 finishers, one a team: sums over the team's warps, gates, weights and stores.  By the
 //               consumers themselves these cost 67 us of 439 with 6 tokens and 4-bit experts
 //
-// What it takes (d 7168, l 1792, f 2048, 384 experts, 32 a token; bytes at the copy rate of 6.46 TB/s):
-//   1 token            156 us, 93 % of the rate
-//   8 tokens           711 us, 98 %
-//   1 token, 4 bits    128 us, 51 %; 6 tokens 351 us, 51 %: the consumers' instructions bound the 4-bit
+// What it takes (d 7168, l 1792, f 2048, 384 experts, 32 a token; bytes at the copy rate of 6.46 TB/s), in turn with
+// other work, and (in brackets) alone in a loop:
+//   1 token            161 us (157), 91 % of the rate
+//   8 tokens           772 us (714), 90 %
+//   1 token, 4 bits    130 us (129), 51 %; 6 tokens 352 us (348), 51 %: the consumers' instructions bound the 4-bit
 //                      stages (with the products skipped, 277 us were left of 500 at the time).  Eight warps
 //                      a team or deeper unrolling were slower: warps compete for the instruction buffers
 // and at d 2048, l 512, f 1408, 256 experts, 24 a token, 1 token: 56 us, 40 %: the seven dependent
 // stages have latencies (selection 5 us, the last three stages 13 us) that a stream of 22 us cannot hide.
+// 512 threads leave 128 registers each, which the 4-bit and fp32 instantiations use up.  fp32 spills (32 bytes of
+// stores, 108 of loads); the 4-bit one does not, and how the compiler gets by shows in the time of 6 tokens: variants
+// of the selection's code that left 4 to 52 bytes of spills there ran at 348 to 358 us.
 //
 // Arithmetic: bf16 weights are the A operand of m16n8k16 (16 weight rows), the tokens its
 // eight columns, fp32 sums.  tcgen05 would need 128 rows per tile and gains nothing here: the

@@ -14,9 +14,10 @@
 // What bounds it is memory wherever the layer uses it: codes and scales are 17/32 of
 // a byte per value, the outputs 2 or 4 bytes each (prompt slot rows: outputs are 55 %
 // of the bytes), and with few rows per expert the weights are nearly all of them.
-// Measured: 32 decode tokens (1024 x 4096 x 1792 over 384 experts, fp32 out) 247-265 us, 83 to 89 % of the copy
-// rate; prompt rows (196608 x 5376 x 1024, 512 experts) 1040-1090 us, 2000 TFLOP/s, 54 %, where operands from L2
-// (40 KB per stage and tile) and the stores share the time: 845 us with one product of four, 920 without stores.
+// Measured in turn with other work, and (in brackets) alone in a loop: 32 decode tokens (1024 x 4096 x 1792 over 384
+// experts, fp32 out) 313 us, 70 % of the copy rate (262, 84 %); prompt rows (196608 x 5376 x 1024, 512 experts)
+// 1244 us, 1740 TFLOP/s, 46 % of the copy rate (1120-1165), where operands from L2 (40 KB per stage and tile) and the
+// stores share the time: when it took 1086 us, 845 with one product of four, 920 without stores.
 //
 // Epilogues: plain (bf16 or fp32 rows); rows times a weight each (the routed down-projection);
 // and the gate of the routed experts with requantisation: columns alternate between 32
