@@ -180,7 +180,7 @@ LMOE_API lmoe_status lmoe_mx4_dequantize(const void *codes, const void *scales, 
  * no-op.  Runs on the current device, which must be the tensors'.
  * INVALID_ARG: NULL pointer, negative size, unknown dtype, E < 1, ldo < N.
  * UNSUPPORTED: K, alignment, E > 1024, K, N or E N past 2^31 - 257, M past
- * 2^30, no sm_100 device.
+ * 2^30 - 1 or more than 2^31 - 1 tiles of 128 x 64, no sm_100 device.
  * WORKSPACE: too small or misaligned. */
 LMOE_API lmoe_status lmoe_mx4_gemm(const void *a_codes, const void *a_scales, int64_t M, const void *w_codes,
                                    const void *w_scales, int64_t N, int64_t K, const int32_t *offsets, int32_t E,

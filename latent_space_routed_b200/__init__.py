@@ -385,7 +385,7 @@ def _mx4_word(device: torch.device) -> torch.Tensor:
     if key not in words:
         if torch.cuda.is_current_stream_capturing():
             return next(iter(words.values())) if words else mx4_gemm_workspace(device)
-        words[key] = mx4_gemm_workspace(device)
+        words.setdefault(key, mx4_gemm_workspace(device))      # (two threads may be here)
     return words[key]
 
 
@@ -537,30 +537,34 @@ class LatentMoE:
         ``workspace`` (``lmoe_few_workspace_size`` bytes) must not be shared by calls that may overlap on the
         GPU.  Without it, calls outside a capture use ``few_workspace``, and each captured call gets a buffer of
         its own, which the layer keeps (a graph may replay beside anything): give a graph of many calls one."""
-        T = x.shape[0]
-        c = self.cfg
-        if x.dim() != 2 or x.shape[1] != c.d or x.dtype != self.dtype or not x.is_contiguous() or x.device != self.device:
-            raise ValueError(f"x must be a contiguous {self.dtype} tensor [T, {c.d}] on {self.device}")
+        T, c, dev = x.shape[0], self.cfg, self.device
+        if x.dim() != 2 or x.shape[1] != c.d or x.dtype != self.dtype or not x.is_contiguous() or x.device != dev:
+            raise ValueError(f"x must be a contiguous {self.dtype} tensor [T, {c.d}] on {dev}")
         for name, cols, dtype in (("output", c.d, self.dtype), ("selected_experts", c.k, torch.int32),
                                   ("mixture_weights", c.k, self.dtype), ("latent_routed_aggregate", c.l, self.dtype)):
             t = out[name]
-            if t.dtype != dtype or t.numel() < T * cols or not t.is_contiguous() or t.device != self.device:
-                raise ValueError(f"{name} must be a contiguous {dtype} tensor of {T} x {cols} values or more on {self.device}")
-        if workspace is not None and (workspace.device != self.device or not workspace.is_contiguous()):
-            raise ValueError(f"workspace must be a contiguous tensor on {self.device}")
+            if t.dtype != dtype or t.numel() < T * cols or not t.is_contiguous() or t.device != dev:
+                raise ValueError(f"{name} must be a contiguous {dtype} tensor of {T} x {cols} values or more on {dev}")
+        if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
         if x.data_ptr() % 16:
             with contextlib.nullcontext() if stream is None else _with(self.device, stream):
                 x = x.clone()
-        ws = self._few_workspace_of_call(T, stream) if workspace is None else workspace
+        handle = _stream(stream)
+        ws = self._few_workspace_of_call(T, stream, handle) if workspace is None else workspace
         lmoe_forward_few(self.handle, x, T, out["output"], out["selected_experts"], out["mixture_weights"],
-                         out["latent_routed_aggregate"], ws, ws.numel() * ws.element_size(), stream)
+                         out["latent_routed_aggregate"], ws, ws.numel() * ws.element_size(), handle)
         return out
 
-    def _few_workspace_of_call(self, T: int, stream) -> torch.Tensor:
-        with contextlib.nullcontext() if stream is None else _with(self.device, stream):
+    def _few_workspace_of_call(self, T: int, stream, handle: int) -> torch.Tensor:
+        if stream is None:
             capturing = torch.cuda.is_current_stream_capturing()
+        else:
+            with _with(self.device, stream):
+                capturing = torch.cuda.is_current_stream_capturing()
         if not capturing:
-            return self.few_workspace(T, stream)
+            ws = self._few_ws.get((T, handle, threading.get_ident()))
+            return self.few_workspace(T, stream) if ws is None else ws
         self._captured_ws.append(self._new_few_workspace(T, stream))
         return self._captured_ws[-1]
 
