@@ -285,7 +285,8 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     uint8_t *g = smem_raw + (base - raw);
     uint64_t *bars = reinterpret_cast<uint64_t *>(g + (size_t)STAGES * STAGE_BYTES);
     const uint32_t full = smem_u32(bars), empty = full + 8 * STAGES, accf = empty + 8 * STAGES, acce = accf + 16;
-    int *words = reinterpret_cast<int *>(bars + 2 * STAGES + 4);     // [0] TMEM base, [1] abort, [2] issued, [3] scan
+    const uint32_t idle = acce + 16;                                  // after a failure: no product in flight
+    int *words = reinterpret_cast<int *>(bars + 2 * STAGES + 5);     // [0] TMEM base, [1] abort, [2] issued, [3] scan
     volatile int *abort = words + 1;
     int *tile_off = reinterpret_cast<int *>(g + (size_t)STAGES * STAGE_BYTES + 256);
     int *row_off = tile_off + MAX_E + 1;
@@ -300,6 +301,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             mbar_init(accf + 8 * a, 1);
             mbar_init(acce + 8 * a, EPI_WARPS);
         }
+        mbar_init(idle, 1);
         words[1] = words[2] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -541,6 +543,11 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         const int issued = words[2];
         for (int i = max(0, issued - STAGES); i < issued; ++i)
             if (!mbar_wait(full + 8 * (i % STAGES), (uint32_t)(i / STAGES) & 1u, &none)) break;
+    }
+    if (*abort && threadIdx.x == 32) {       // (the issuer) and products in flight before their memory goes away
+        int none = 0;
+        commit(idle);
+        mbar_wait(idle, 0u, &none);
     }
     __syncthreads();
     if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
